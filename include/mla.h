@@ -24,6 +24,14 @@
  *   mla_naive_decode the decompress-then-attend form, a comparison point only
  *                    ("The MLA decode speedup hiding in your model card",
  *                    section "The naive form, written out")
+ * and of the rest of the layer around it (the pages have no counterpart of these):
+ *   mla_rope         rotary positions of query or key rows, split from the part
+ *                    of each head that is not rotated
+ *   mla_pages_update block tables, lengths and the new tokens' positions and
+ *                    slots from the requests' lengths, pages from a ring of free ones
+ *   mla_latent_store the new tokens' latents normalised, their keys rotated, the
+ *                    rows written to the cache's slots (bf16 or FP8)
+ *   mla_linear       out = residual + act(x . W + bias)
  * The latent cache is bf16 or FP8 (E4M3 codes with one scale per cache), see
  * mla_cache.
  *
@@ -381,6 +389,173 @@ MLA_API int mla_prefill(const mla_dims *dims, const void *q_nope, const void *q_
  * it) into *status: MLA_OK, MLA_ERR_SEQLEN, MLA_ERR_PAGE or MLA_ERR_TIMEOUT.
  * Returns MLA_ERR_CUDA if the copy or the wait fails. */
 MLA_API int mla_read_status(const void *workspace, int *status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The rest of the layer around the attention.  Beyond the conventions at the top:
+ *  - Rows may sit inside wider ones where a stride is an argument; strides count
+ *    elements and are multiples of 8 (16 bytes).  Inputs and outputs must not
+ *    overlap except where stated.
+ *  - `status` (optional, device int32, 4-byte aligned) takes the place of the
+ *    workspace's status word: a problem only the device can see leaves its code
+ *    there if the word holds 0.  The call never clears it, so one word can collect
+ *    the first error of many calls; the caller zeroes it.
+ * ------------------------------------------------------------------------ */
+
+/* How a rotary pair lies in a row of d_rope values. */
+typedef enum {
+    MLA_ROPE_INTERLEAVED = 0, /* pair i is (2i, 2i+1) */
+    MLA_ROPE_HALF = 1         /* pair i is (i, i + d_rope/2) */
+} mla_rope_layout;
+
+/* Angular frequency f_i of pair i, b = base, d = d_rope, s = factor. */
+typedef enum {
+    MLA_ROPE_PLAIN = 0,  /* f_i = b^(-2i/d) */
+    MLA_ROPE_LINEAR = 1, /* f_i = b^(-2i/d) / s: positions divided by s */
+    MLA_ROPE_NTK = 2,    /* f_i = (b s^(d/(d-2)))^(-2i/d): the slowest pair stretched by s, the fastest kept */
+    MLA_ROPE_YARN = 3    /* by parts: f_i kept for pairs below `low`, divided by s above `high`, linear in i
+                            between them.  A pair that turns n times in original_len positions has the index
+                            i(n) = d ln(original_len / (2 pi n)) / (2 ln b); low = max(floor(i(beta_fast)), 0),
+                            high = min(ceil(i(beta_slow)), d - 1) (high - low at least 0.001) */
+} mla_rope_scaling;
+
+typedef struct {
+    int d_rope;             /* a multiple of 16 from 16 to 64 */
+    int layout;             /* mla_rope_layout */
+    int scaling;            /* mla_rope_scaling */
+    double base;            /* > 1 */
+    double factor;          /* s, > 0 (not read by MLA_ROPE_PLAIN) */
+    int original_len;       /* MLA_ROPE_YARN: > 0 */
+    double beta_fast;       /* MLA_ROPE_YARN: > 0, usually 32 */
+    double beta_slow;       /* MLA_ROPE_YARN: > 0, usually 1 */
+    double mscale;          /* factor on cos and sin, > 0 (1: a pure rotation) */
+    const double *inv_freq; /* host, d_rope/2 frequencies in radians a position that replace all of the above
+                               but d_rope, layout and mscale; NULL = the formulas */
+} mla_rope_config;
+
+/* The rotation of one model, filled in by mla_rope_init and read by the entry
+ * points below (by value: it can live on the stack).  Frequencies are held as the
+ * fraction of a turn a position makes, in units of 2^-64: position times that,
+ * modulo 2^64, is the angle of any position below 2^31 without loss. */
+typedef struct {
+    int d_rope;
+    int layout;
+    float mscale;
+    int reserved;
+    unsigned long long turn[32];
+} mla_rope_plan;
+
+/* Works out *plan on the host (no device is touched).  MLA_ERR_UNSUPPORTED for a
+ * width, layout or scaling outside the lists above, MLA_ERR_SHAPE for values
+ * outside the ranges or not finite. */
+MLA_API int mla_rope_init(const mla_rope_config *config, mla_rope_plan *plan);
+
+/* Rotary positions, and the split of a projected query into its two parts.  Row
+ * (b, i, h) of x holds d_pass values that are copied to pass_out and d_rope values
+ * that are rotated into rope_out (d_rope as in dims and plan, d_pass = d_nope where
+ * pass_out is given, else 0).  With t = position . turn and pair (u, v):
+ *   (u, v) -> mscale (u cos t - v sin t, u sin t + v cos t)     (fp32, bf16 out)
+ * transpose = 1 turns the other way: the rotation's transpose, which carries
+ * gradients back and, with mscale 1, undoes the rotation.
+ * x bf16: row (b, i, h) at x + (b*s_q + i)*token_stride + h*head_stride;
+ * head_stride >= d_pass + d_rope (H = 1: not read), token_stride >= H rows.
+ * positions int32 [B][s_q]; NULL: token (b, i) is at seq_lens[b] - s_q + i.  A
+ * token with a negative position is padding: its outputs stay as they were.
+ * pass_out [B][s_q][H][d_nope], rope_out [B][s_q][H][d_rope], dense.  Without
+ * pass_out, rope_out may be x itself if x is dense. */
+MLA_API int mla_rope(const mla_dims *dims, const mla_rope_plan *plan, const void *x, long long token_stride,
+                     long long head_stride, const int *positions, const int *seq_lens, void *pass_out,
+                     void *rope_out, int transpose, void *stream);
+
+/* The pages of a batch.  Free pages sit in a ring, taken at its head and given
+ * back at its tail, so that a page just given back is the last to be used again. */
+typedef struct {
+    int B;               /* requests */
+    int page_size;       /* tokens a page, a multiple of 64 */
+    int max_pages;       /* columns of block_table; max_pages * page_size <= 2^30 */
+    int num_pages;       /* pages of the pool; num_pages * page_size < 2^31 */
+    int *block_table;    /* device [B][max_pages], updated: as mla_cache.block_table */
+    int *free_ring;      /* device [num_pages], updated: page ids */
+    const int *state;    /* device [2]: index of the oldest free entry, number of free entries */
+    int *state_out;      /* device [2]: the same after the call */
+} mla_page_pool;
+
+/* Takes every request from old_lens[b] to new_lens[b] tokens.  With
+ * pages(n) = ceil(n / page_size), requests in order:
+ *   - one that grows takes pages(new) - pages(old) pages from the ring, entered in
+ *     the columns pages(old)...pages(new)-1 of its row of block_table;
+ *   - one that shrinks (a finished request: new = 0; rejected drafts) gives the
+ *     pages of the columns pages(new)...pages(old)-1 back, in order; the entries
+ *     stay in the table, where no length reaches them any more;
+ *   - its max(new - old, 0) new tokens are numbered from token_start[b] on, with
+ *     their positions old...new-1 and slots: the row page*page_size + position %
+ *     page_size of the pool that mla_latent_store writes.
+ * seq_lens[b] = new_lens[b].  Pages given back are not taken in the same call.
+ * Requests that cannot be served keep seq_lens[b] = old_lens[b] and their row of
+ * the table, and their tokens have position and slot -1:
+ *   - a length below 0 or above max_pages * page_size (MLA_ERR_SEQLEN; such a
+ *     request counts as having no new tokens);
+ *   - one whose pages, counted with those of all requests before it, are more than
+ *     the ring holds (MLA_ERR_PAGE);
+ *   - one whose tokens end behind max_tokens (MLA_ERR_SHAPE).
+ * A ring entry outside the pool is entered as -1, its tokens' slots are -1, and
+ * MLA_ERR_PAGE is recorded; so is a state outside the ring (then no pages move).
+ * Entries of positions and slots behind the last token are -1.
+ * old_lens, new_lens, seq_lens int32 [B]; token_start int32 [B + 1] (sums that
+ * pass 2^31 - 1 stay there); positions, slots int32 [max_tokens].  Inputs are left
+ * as they are: the outputs must be other buffers.  A call repeated on the same
+ * inputs, before any other call on the pool, does the same again.  B <= 65535. */
+MLA_API int mla_pages_update(const mla_page_pool *pool, const int *old_lens, const int *new_lens, int max_tokens,
+                             int *seq_lens, int *token_start, int *positions, int *slots, int *status,
+                             void *stream);
+
+/* Writes the new tokens' rows of the latent cache from their down-projection
+ * [c | k] (d_c + d_rope values a token, row t at x + t*token_stride, t = b*s_q + i):
+ *   c' = c / sqrt(mean(c^2) + eps) * norm_weight     (norm_weight NULL: c' = c)
+ *   k' = k rotated by the token's position           (plan NULL: k' = k)
+ * computed in fp32 and rounded once, to bf16 or to the E4M3 code of value /
+ * kv_scale (nearest even, saturated to +-448; NaN stays NaN).  norm_weight bf16 [d_c].
+ * Token t goes to row slots[t] of a paged pool (int32 [B][s_q], as
+ * mla_pages_update gives them; a negative slot is skipped); slots NULL: to row
+ * seq_lens[b] - s_q + i of sequence b, as mla_cache_append.  Two tokens of one call
+ * must not share a row.  positions as for mla_rope (read only with a plan; a
+ * negative one skips the token); NULL: seq_lens[b] - s_q + i.
+ * Recorded in status, the token's row not written: MLA_ERR_PAGE (a slot or page
+ * outside the pool), MLA_ERR_SEQLEN (a length outside [s_q, capacity] where
+ * seq_lens is read).  Slots with a contiguous cache are MLA_ERR_UNSUPPORTED. */
+MLA_API int mla_latent_store(const mla_dims *dims, const mla_rope_plan *plan, const void *x, long long token_stride,
+                             const void *norm_weight, float eps, const int *positions, const int *slots,
+                             const mla_cache *cache, int *status, void *stream);
+
+typedef enum {
+    MLA_ACT_NONE = 0,
+    MLA_ACT_RELU = 1,
+    MLA_ACT_SILU = 2,     /* v / (1 + exp(-v)) */
+    MLA_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2 */
+    MLA_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+} mla_act;
+
+typedef struct {
+    int M;                     /* rows of x (tokens), at most 65535 * 128 */
+    int K;                     /* contraction width, a multiple of 8 up to 2^20 */
+    int N;                     /* output width, a multiple of 8 up to 2^20 */
+    int act;                   /* mla_act */
+    long long x_stride;        /* elements between rows of x, out and residual: */
+    long long out_stride;      /* multiples of 8, at least the width */
+    long long residual_stride; /* (not read without a residual) */
+} mla_linear_desc;
+
+/* Bytes of workspace mla_linear needs (0 for invalid arguments). */
+MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *desc);
+
+/* Matrix product with its epilogue: the projections around the attention (query,
+ * latent and output projection, the latter added to the residual stream).
+ *   out[m, n] = residual[m, n] + act(sum_k x[m, k] W[k, n] + bias[n])
+ * fp32 accumulation and epilogue, one rounding to bf16.  x [M][K], w [K][N] dense,
+ * bias [N] or NULL, residual [M][N] or NULL, out [M][N], all bf16.  out may be
+ * residual itself.  Results do not depend on the timing of the GPU.  A bounded
+ * device wait that runs out leaves NaN in the outputs it concerns. */
+MLA_API int mla_linear(const mla_linear_desc *desc, const void *x, const void *w, const void *bias,
+                       const void *residual, void *out, void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

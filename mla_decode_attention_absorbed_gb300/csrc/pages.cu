@@ -1,0 +1,219 @@
+// Block tables, lengths, positions and slots of a batch from its requests' old
+// and new lengths; pages from a ring of free ones.
+//
+// Three sums run over the requests in order: new tokens, pages taken, pages given
+// back.  They are sums of non-negative integers that stop at 2^31 - 1, which keeps
+// them associative, so every CTA forms all of them by itself (a batch's lengths are
+// a few hundred KB at most and come from L2): one launch, no exchange between CTAs
+// and no counters to clear.  A CTA keeps the sums before every group of requests in
+// shared memory (1024 groups); a token, a page taken or a page given back is then
+// found by bisection over the groups and a walk inside one.
+#include "layer.h"
+
+namespace mla {
+namespace {
+
+constexpr int kGroups = 1024;
+constexpr int kBig = 0x7fffffff;
+
+__device__ __forceinline__ int sat_add(int x, int y) { return (int)min((uint32_t)x + (uint32_t)y, (uint32_t)kBig); }
+
+struct Sums {
+    int tokens, taken, given;
+};
+__device__ __forceinline__ Sums add(const Sums &x, const Sums &y) {
+    return Sums{sat_add(x.tokens, y.tokens), sat_add(x.taken, y.taken), sat_add(x.given, y.given)};
+}
+
+struct Request {
+    int old_len, new_len, had, has;  // lengths, and the pages they fill
+    bool valid;
+    Sums n;  // its own tokens, pages taken, pages given back
+};
+
+__device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
+    Request r;
+    r.old_len = __ldg(a.old_lens + b);
+    r.new_len = __ldg(a.new_lens + b);
+    const int most = a.max_pages * a.page_size;  // at most 2^30
+    r.valid = r.old_len >= 0 && r.new_len >= 0 && r.old_len <= most && r.new_len <= most;
+    r.had = r.has = 0;
+    r.n = Sums{0, 0, 0};
+    if (r.valid) {
+        r.had = (r.old_len + a.page_size - 1) / a.page_size;
+        r.has = (r.new_len + a.page_size - 1) / a.page_size;
+        r.n = Sums{max(r.new_len - r.old_len, 0), max(r.has - r.had, 0), max(r.had - r.has, 0)};
+    }
+    return r;
+}
+
+struct Ring {
+    int head, count;
+    bool ok;
+};
+
+// Whether a request whose sums end at `end` (itself included) is served.
+__device__ __forceinline__ bool served(const PagesArgs &a, const Ring &ring, const Request &r, const Sums &end) {
+    return r.valid && (r.n.taken == 0 || end.taken <= ring.count) && (r.n.tokens == 0 || end.tokens <= a.max_tokens) &&
+           (ring.ok || (r.n.taken == 0 && r.n.given == 0));
+}
+
+__device__ __forceinline__ int ring_at(const PagesArgs &a, int from, int k) {  // from < num_pages, k <= num_pages
+    const unsigned i = (unsigned)from + (unsigned)k;
+    return (int)(i >= (unsigned)a.num_pages ? i - a.num_pages : i);
+}
+
+// The last group whose sum of member `which` is at most k (groups' first sums are
+// non-decreasing and begin at 0).
+template <int Sums::*which>
+__device__ __forceinline__ int find_group(const Sums *first, int groups, int k) {
+    int lo = 0, hi = groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (first[mid].*which <= k) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The request that holds item k of member `which`, and the sums before it.
+template <int Sums::*which>
+__device__ __forceinline__ Request find_request(const PagesArgs &a, const Sums *first, int groups, int per, int k, int &b,
+                                                Sums &before) {
+    const int g = find_group<which>(first, groups, k);
+    b = g * per;
+    before = first[g];
+    Request r = load_request(a, b);
+    // item k lies before the sums of all requests (the callers' bound), so the walk ends
+    // inside the batch
+    while (sat_add(before.*which, r.n.*which) <= k && b + 1 < a.B) {
+        before = add(before, r.n);
+        r = load_request(a, ++b);
+    }
+    return r;
+}
+
+__global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ PagesArgs a, int per) {
+    __shared__ Sums first[kGroups];
+    __shared__ Sums warp_sums[32];
+    __shared__ Sums total_s;
+    __shared__ int taken_s;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, groups = (a.B + per - 1) / per;
+    Ring ring{__ldg(a.state), __ldg(a.state + 1), true};
+    if (ring.head < 0 || ring.head >= a.num_pages || ring.count < 0 || ring.count > a.num_pages) ring.ok = false;
+
+    // sums before every group
+    Sums mine{0, 0, 0};
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine = add(mine, load_request(a, b).n);
+    Sums run = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        Sums up{__shfl_up_sync(~0u, run.tokens, o), __shfl_up_sync(~0u, run.taken, o), __shfl_up_sync(~0u, run.given, o)};
+        if (lane >= o) run = add(run, up);
+    }
+    if (lane == 31) warp_sums[warp] = run;
+    if (tid == 0) taken_s = 0;
+    __syncthreads();
+    if (warp == 0) {
+        Sums w = lane < (int)blockDim.x / 32 ? warp_sums[lane] : Sums{0, 0, 0};
+        for (int o = 1; o < 32; o <<= 1) {
+            Sums up{__shfl_up_sync(~0u, w.tokens, o), __shfl_up_sync(~0u, w.taken, o), __shfl_up_sync(~0u, w.given, o)};
+            if (lane >= o) w = add(w, up);
+        }
+        if (lane < (int)blockDim.x / 32) warp_sums[lane] = w;  // sums up to and with warp `lane`
+        if (lane == 31) total_s = w;
+    }
+    __syncthreads();
+    {
+        // sums before this thread's group: before its warp, and before it within the warp
+        Sums before = warp > 0 ? warp_sums[warp - 1] : Sums{0, 0, 0};
+        Sums up{__shfl_up_sync(~0u, run.tokens, 1), __shfl_up_sync(~0u, run.taken, 1), __shfl_up_sync(~0u, run.given, 1)};
+        if (lane > 0) before = add(before, up);
+        if (tid < groups) first[tid] = before;
+        // the group's requests: lengths, starts, and what the whole batch takes
+        const bool writes = tid % (int)gridDim.x == (int)blockIdx.x;
+        int most = 0;
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+            const Request r = load_request(a, b);
+            const Sums end = add(before, r.n);
+            const bool fits = served(a, ring, r, end);
+            if (fits && r.n.taken > 0) most = end.taken;
+            if (writes) {
+                a.seq_lens[b] = fits ? r.new_len : r.old_len;
+                a.token_start[b] = before.tokens;
+                if (!fits)
+                    set_status(a.status, !r.valid ? MLA_ERR_SEQLEN
+                                         : !ring.ok || (r.n.taken > 0 && end.taken > ring.count) ? MLA_ERR_PAGE
+                                                                                                 : MLA_ERR_SHAPE);
+            }
+            before = end;
+        }
+        if (most > 0) atomicMax(&taken_s, most);
+    }
+    __syncthreads();
+    const Sums total = total_s;
+    const int taken = taken_s;  // served takers are the first ones: their sums do not exceed the ring's count
+    // pages given back that the ring has room for (all of them, in a consistent pool)
+    const int given = ring.ok ? min(total.given, a.num_pages - ring.count) : 0;
+    const int gsize = gridDim.x * blockDim.x, gid = blockIdx.x * blockDim.x + tid;
+    if (gid == 0) {
+        a.token_start[a.B] = total.tokens;
+        a.state_out[0] = ring.ok ? ring_at(a, ring.head, taken) : ring.head;
+        a.state_out[1] = ring.ok ? ring.count - taken + given : ring.count;
+        if (!ring.ok || given < total.given) set_status(a.status, MLA_ERR_PAGE);
+    }
+
+    for (int k = gid; k < taken; k += gsize) {
+        int b;
+        Sums before;
+        const Request r = find_request<&Sums::taken>(a, first, groups, per, k, b, before);
+        int page = __ldg(a.ring + ring_at(a, ring.head, k));
+        if (page < 0 || page >= a.num_pages) {
+            set_status(a.status, MLA_ERR_PAGE);
+            page = -1;
+        }
+        a.table[(long long)b * a.max_pages + r.had + (k - before.taken)] = page;
+    }
+    const int tail = ring.ok ? ring_at(a, ring.head, ring.count) : 0;
+    for (int k = gid; k < given; k += gsize) {
+        int b;
+        Sums before;
+        const Request r = find_request<&Sums::given>(a, first, groups, per, k, b, before);
+        a.ring[ring_at(a, tail, k)] = a.table[(long long)b * a.max_pages + r.has + (k - before.given)];
+    }
+    for (int k = gid; k < a.max_tokens; k += gsize) {
+        int pos = -1, slot = -1;
+        if (k < total.tokens) {
+            int b;
+            Sums before;
+            const Request r = find_request<&Sums::tokens>(a, first, groups, per, k, b, before);
+            if (served(a, ring, r, add(before, r.n))) {
+                pos = r.old_len + (k - before.tokens);
+                const int col = pos / a.page_size;
+                int page;
+                if (col < r.had) page = a.table[(long long)b * a.max_pages + col];
+                else page = __ldg(a.ring + ring_at(a, ring.head, before.taken + col - r.had));
+                if (page >= 0 && page < a.num_pages) slot = page * a.page_size + pos % a.page_size;
+                else set_status(a.status, MLA_ERR_PAGE);
+            }
+        }
+        a.positions[k] = pos;
+        a.slots[k] = slot;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t st) {
+    const int per = a.B > 0 ? (a.B + kGroups - 1) / kGroups : 1;
+    const int groups = (a.B + per - 1) / per;
+    // enough threads for the groups' sums, and CTAs for the tokens
+    int threads = groups > 0 ? (groups + 31) / 32 * 32 : 32;
+    if (threads < 256 && a.max_tokens > threads) threads = 256;
+    const long long want = ((long long)a.max_tokens + 4 * threads - 1) / (4 * threads);
+    const int sms = layer_num_sms();
+    const int grid = want < 1 ? 1 : want > sms ? sms : (int)want;
+    pages_update<<<grid, threads, 0, st>>>(a, per);
+    return cudaGetLastError();
+}
+
+}  // namespace mla

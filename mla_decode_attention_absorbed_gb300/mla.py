@@ -46,8 +46,36 @@ EXPORTS = ("mla_status_string", "mla_abi_version", "mla_absorb_q", "mla_decode_w
            "mla_naive_decode", "mla_read_status", "mla_decode_attn_noalloc", "mla_cache_append_workspace_size",
            "mla_cache_append", "mla_decode_sparse_workspace_size", "mla_decode_attn_sparse", "mla_prefill_crossover",
            "mla_prefill_expand_workspace_size", "mla_prefill_expand", "mla_prefill_workspace_size", "mla_prefill",
-           "mla_decode_step", "mla_set_wait_limit_ns")
+           "mla_decode_step", "mla_set_wait_limit_ns", "mla_rope_init", "mla_rope", "mla_pages_update",
+           "mla_latent_store", "mla_linear_workspace_size", "mla_linear")
 PATH_ABSORB, PATH_EXPAND = 0, 1
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("d_rope", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_int), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("mscale", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("d_rope", ctypes.c_int), ("layout", ctypes.c_int), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int), ("turn", ctypes.c_ulonglong * 32)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("block_table", ctypes.c_void_p), ("free_ring", ctypes.c_void_p),
+                ("state", ctypes.c_void_p), ("state_out", ctypes.c_void_p)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int), ("act", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong),
+                ("residual_stride", ctypes.c_longlong)]
 
 
 def lib_path() -> str:
@@ -108,6 +136,19 @@ def load(path: str | None = None):
     lib.mla_decode_attn_noalloc.restype = I
     lib.mla_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
     lib.mla_set_wait_limit_ns.restype = I
+    LL, pr, pp, pl = ctypes.c_longlong, ctypes.POINTER(RopePlan), ctypes.POINTER(PagePool), ctypes.POINTER(LinearDesc)
+    lib.mla_rope_init.argtypes = [ctypes.POINTER(RopeConfig), pr]
+    lib.mla_rope_init.restype = I
+    lib.mla_rope.argtypes = [pd, pr, P, LL, LL, P, P, P, P, I, P]
+    lib.mla_rope.restype = I
+    lib.mla_pages_update.argtypes = [pp, P, P, I, P, P, P, P, P, P]
+    lib.mla_pages_update.restype = I
+    lib.mla_latent_store.argtypes = [pd, pr, P, LL, P, ctypes.c_float, P, P, pc, P, P]
+    lib.mla_latent_store.restype = I
+    lib.mla_linear_workspace_size.argtypes = [pl]
+    lib.mla_linear_workspace_size.restype = SZ
+    lib.mla_linear.argtypes = [pl, P, P, P, P, P, P, SZ, P]
+    lib.mla_linear.restype = I
     if path is None:
         _lib = lib
     return lib
@@ -376,6 +417,207 @@ def read_status(workspace, stream=None) -> int:
     v = ctypes.c_int(0)
     _check(load().mla_read_status(_ptr(workspace), ctypes.byref(v), _stream(stream)), "mla_read_status")
     return int(v.value)
+
+
+# ------------------------------------------------------------- the layer around the attention
+def _want(t, what: str, dtype, shape=None, dense=True):
+    """t is a CUDA tensor of this type (and shape) on the current device, dense if asked."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have the shape {shape}, not {tuple(t.shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{what} must be dense")
+
+
+def rope_plan(d_rope: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0, scaling: int = ROPE_PLAIN,
+              factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+              mscale: float = 1.0, inv_freq=None) -> RopePlan:
+    """mla_rope_init: the rotation of one model (host only).  ``inv_freq``, d_rope / 2
+    frequencies in radians a position, replaces base and scaling."""
+    freq = None
+    if inv_freq is not None:
+        freq = [float(f) for f in inv_freq]
+        if len(freq) != d_rope // 2:
+            raise ValueError(f"inv_freq must have d_rope / 2 = {d_rope // 2} entries, not {len(freq)}")
+        freq = (ctypes.c_double * len(freq))(*freq)
+    cfg = RopeConfig(d_rope, layout, scaling, base, factor, original_len, beta_fast, beta_slow, mscale, freq)
+    plan = RopePlan()
+    _check(load().mla_rope_init(ctypes.byref(cfg), ctypes.byref(plan)), "mla_rope_init")
+    return plan
+
+
+def _check_positions(prob: Problem, positions, seq_lens):
+    if positions is not None:
+        _want(positions, "positions", torch.int32)
+        if positions.numel() != prob.B * prob.s_q:
+            raise ValueError("positions must hold one entry a token")
+    if seq_lens is not None:
+        _want(seq_lens, "seq_lens", torch.int32, (prob.B,))
+
+
+def rope(prob: Problem, plan: RopePlan, x, positions=None, seq_lens=None, q_nope=None, q_rope=None,
+         transpose: bool = False, stream=None):
+    """mla_rope: x [B, s_q, H, d_nope + d_rope] (rows of heads may lie inside wider ones) split
+    and rotated, returns (q_nope, q_rope); x [B, s_q, H, d_rope] rotated, returns q_rope (which
+    may be x itself).  Tokens are at ``positions`` [B, s_q], or the last of ``seq_lens`` [B]."""
+    lib = load()
+    B, s_q, H = prob.B, prob.s_q, prob.H
+    _want(x, "x", torch.bfloat16, dense=False)
+    if x.dim() != 4 or x.shape[:3] != (B, s_q, H) or x.stride(3) != 1 or (
+            B > 1 and s_q > 1 and x.stride(0) != s_q * x.stride(1)):
+        raise ValueError("x must be [B, s_q, H, width] with evenly spaced tokens and contiguous values")
+    split = x.shape[3] == prob.d_nope + prob.d_rope
+    if not split and x.shape[3] != prob.d_rope:
+        raise ValueError("x must have rows of d_nope + d_rope or d_rope values")
+    _check_positions(prob, positions, seq_lens)
+    if q_rope is None:
+        q_rope = torch.empty(B, s_q, H, prob.d_rope, dtype=torch.bfloat16, device=x.device)
+    else:
+        _want(q_rope, "q_rope", torch.bfloat16, (B, s_q, H, prob.d_rope))
+    if split and q_nope is None:
+        q_nope = torch.empty(B, s_q, H, prob.d_nope, dtype=torch.bfloat16, device=x.device)
+    elif split:
+        _want(q_nope, "q_nope", torch.bfloat16, (B, s_q, H, prob.d_nope))
+    elif q_nope is not None:
+        raise ValueError("rows of d_rope values have no part for q_nope")
+    d = prob.dims()
+    head_stride = x.stride(2) if H > 1 else x.shape[3]
+    token_stride = x.stride(1) if s_q > 1 else x.stride(0) if B > 1 else (H - 1) * head_stride + x.shape[3]
+    _check(lib.mla_rope(ctypes.byref(d), ctypes.byref(plan), _ptr(x), token_stride, head_stride, _ptr(positions),
+                        _ptr(seq_lens), _ptr(q_nope), _ptr(q_rope), int(transpose), _stream(stream)), "mla_rope")
+    return (q_nope, q_rope) if split else q_rope
+
+
+@dataclass
+class Pages:
+    """A batch's pages: the block table (int32 [B, max_pages]) and the ring of free page ids
+    (int32 [num_pages]), both updated by ``pages_update``."""
+    block_table: torch.Tensor
+    free_ring: torch.Tensor
+    page_size: int = 64
+
+    def __post_init__(self):
+        _want(self.block_table, "block_table", torch.int32)
+        _want(self.free_ring, "free_ring", torch.int32)
+        if self.block_table.dim() != 2 or self.free_ring.dim() != 1:
+            raise ValueError("block_table must be [B, max_pages], free_ring [num_pages]")
+
+    @classmethod
+    def empty(cls, B: int, max_pages: int, num_pages: int, page_size: int = 64, device="cuda"):
+        """A pool with every page free, and the ring's state for the first update."""
+        table = torch.full((B, max_pages), -1, dtype=torch.int32, device=device)
+        ring = torch.arange(num_pages, dtype=torch.int32, device=device)
+        return cls(table, ring, page_size), torch.tensor([0, num_pages], dtype=torch.int32, device=device)
+
+
+@dataclass
+class PagesStep:
+    """What one ``pages_update`` gives: the batch's lengths, the ring's state, and for the new
+    tokens where each request's begin, their positions and their slots."""
+    seq_lens: torch.Tensor
+    ring_state: torch.Tensor
+    token_start: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+
+
+def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, out: PagesStep | None = None,
+                 status=None, stream=None) -> PagesStep:
+    """mla_pages_update: every request from old_lens[b] to new_lens[b] tokens.  ``out`` (the
+    result of an earlier call) is written over; its tensors must not be this call's inputs."""
+    lib = load()
+    B = pages.block_table.shape[0]
+    dev = pages.block_table.device
+    _want(ring_state, "ring_state", torch.int32, (2,))
+    _want(old_lens, "old_lens", torch.int32, (B,))
+    _want(new_lens, "new_lens", torch.int32, (B,))
+    if status is not None:
+        _want(status, "status", torch.int32)
+    if out is None:
+        out = PagesStep(*(torch.empty(n, dtype=torch.int32, device=dev)
+                          for n in (B, 2, B + 1, max_tokens, max_tokens)))
+    else:
+        for t, n, what in ((out.seq_lens, B, "seq_lens"), (out.ring_state, 2, "ring_state"),
+                           (out.token_start, B + 1, "token_start"), (out.positions, max_tokens, "positions"),
+                           (out.slots, max_tokens, "slots")):
+            _want(t, what, torch.int32, (n,))
+    pool = PagePool(B, pages.page_size, pages.block_table.shape[1], pages.free_ring.shape[0],
+                    pages.block_table.data_ptr(), pages.free_ring.data_ptr(), ring_state.data_ptr(),
+                    out.ring_state.data_ptr())
+    _check(lib.mla_pages_update(ctypes.byref(pool), _ptr(old_lens), _ptr(new_lens), max_tokens, _ptr(out.seq_lens),
+                                _ptr(out.token_start), _ptr(out.positions), _ptr(out.slots), _ptr(status),
+                                _stream(stream)), "mla_pages_update")
+    return out
+
+
+def latent_store(prob: Problem, x, cache: Cache, plan: RopePlan | None = None, norm_weight=None, eps: float = 1e-6,
+                 positions=None, slots=None, status=None, stream=None) -> None:
+    """mla_latent_store: rows [c | k] of the new tokens (x [B * s_q, d_c + d_rope], inside wider
+    rows or not) normalised, rotated and written to the cache, whose kv buffer is modified."""
+    lib = load()
+    _want(x, "x", torch.bfloat16, (prob.B * prob.s_q, prob.d_c + prob.d_rope), dense=False)
+    if x.stride(1) != 1:
+        raise ValueError("x must have contiguous values")
+    if norm_weight is not None:
+        _want(norm_weight, "norm_weight", torch.bfloat16, (prob.d_c,))
+    _check_positions(prob, positions, None)
+    if slots is not None:
+        _want(slots, "slots", torch.int32)
+        if slots.numel() != prob.B * prob.s_q:
+            raise ValueError("slots must hold one entry a token")
+    if status is not None:
+        _want(status, "status", torch.int32)
+    d = prob.dims()
+    stride = x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    _check(lib.mla_latent_store(ctypes.byref(d), None if plan is None else ctypes.byref(plan), _ptr(x), stride,
+                                _ptr(norm_weight), float(eps), _ptr(positions), _ptr(slots), ctypes.byref(cache),
+                                _ptr(status), _stream(stream)), "mla_latent_store")
+
+
+def _linear_desc(x, w, out, residual, act) -> LinearDesc:
+    def stride(t, width):
+        return t.stride(0) if t is not None and t.shape[0] > 1 else width
+
+    N = w.shape[1]
+    return LinearDesc(x.shape[0], w.shape[0], N, act, stride(x, w.shape[0]), stride(out, N), stride(residual, N))
+
+
+def linear_workspace_size(M: int, K: int, N: int) -> int:
+    desc = LinearDesc(M, K, N, ACT_NONE, K, N, N)
+    n = load().mla_linear_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise ValueError("mla_linear_workspace_size rejected the arguments")
+    return int(n)
+
+
+def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, workspace=None, stream=None):
+    """mla_linear: residual + act(x . w + bias), x [M, K] and residual [M, N] with any row stride
+    (multiples of 8), w [K, N] dense.  ``out`` may be ``residual``."""
+    lib = load()
+    _want(x, "x", torch.bfloat16, dense=False)
+    _want(w, "w", torch.bfloat16)
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[0] or x.stride(1) != 1:
+        raise ValueError("x must be [M, K] with contiguous values, w [K, N]")
+    M, N = x.shape[0], w.shape[1]
+    if bias is not None:
+        _want(bias, "bias", torch.bfloat16, (N,))
+    for t, what in ((residual, "residual"), (out, "out")):
+        if t is not None:
+            _want(t, what, torch.bfloat16, (M, N), dense=False)
+            if t.stride(1) != 1:
+                raise ValueError(f"{what} must have contiguous values")
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+    desc = _linear_desc(x, w, out, residual, act)
+    if workspace is None:
+        n = lib.mla_linear_workspace_size(ctypes.byref(desc))
+        workspace = alloc_workspace(n, x.device)
+    _check(lib.mla_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), _ptr(workspace),
+                          workspace.numel(), _stream(stream)), "mla_linear")
+    return out
 
 
 class Decoder:
