@@ -544,7 +544,8 @@ typedef struct {
     long long residual_stride; /* (not read without a residual) */
 } mla_linear_desc;
 
-/* Bytes of workspace mla_linear needs (0 for invalid arguments). */
+/* Bytes of workspace mla_linear needs (0 for invalid arguments).  Up to 256 bytes
+ * none is used, and workspace may be NULL. */
 MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *desc);
 
 /* Matrix product with its epilogue: the projections around the attention (query,

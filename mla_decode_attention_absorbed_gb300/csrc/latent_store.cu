@@ -11,7 +11,8 @@
 namespace mla {
 namespace {
 
-constexpr int kWarps = 4;  // tokens a CTA
+constexpr int kWarps = 4;  // warps a CTA
+constexpr int kCtasPerSm = 8;
 
 // Two values as E4M3 codes (v0 in the low byte): nearest even, saturating at +-448.
 __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
@@ -20,163 +21,177 @@ __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
     return r;
 }
 
-// Row of the cache token t goes to, or -1: skipped, or recorded in status.
-__device__ __forceinline__ long long store_row(const StoreArgs &a, int t, int lane, long long &at) {
+// What a warp reads of one token before it can compute: the row, and where it goes.
+struct Row {
+    uint4 c[2];   // 16-byte chunks lane and lane + 32 of the latent
+    uint32_t k;   // the lane's pair of the key, bf16 x 2
+    int slot;     // slots, else the sequence's length (which pos may need, too)
+    int pos, len;
+};
+
+template <bool kHalf>
+__device__ __forceinline__ Row load_row(const StoreArgs &a, int t, int lane) {
+    Row r;
+    const __nv_bfloat16 *src = a.x + t * a.token_stride;
+    const int nc = a.d_c / 8, nf = a.d_rope / 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r.c[i] = make_uint4(0, 0, 0, 0);
+        if (lane + 32 * i < nc) r.c[i] = *(reinterpret_cast<const uint4 *>(src) + lane + 32 * i);
+    }
+    r.k = 0;
+    if (lane < nf) {
+        const unsigned short *k = reinterpret_cast<const unsigned short *>(src + a.d_c);
+        r.k = kHalf ? k[lane] | (uint32_t)k[lane + nf] << 16 : *reinterpret_cast<const uint32_t *>(k + 2 * lane);
+    }
+    const bool by_lens = !a.slots || (a.rotate && !a.positions);
+    r.len = by_lens ? __ldg(a.cache.seq_lens + (a.s_q == 1 ? t : t / a.s_q)) : 0;
+    r.slot = a.slots ? __ldg(a.slots + t) : 0;
+    r.pos = a.rotate && a.positions ? __ldg(a.positions + t) : 0;
+    return r;
+}
+
+// Element offset in the cache of token t's row, or -1: skipped, or recorded in status.
+__device__ __forceinline__ long long row_offset(const StoreArgs &a, Row &r, int t, int lane) {
     const AttnParams &c = a.cache;
     const long long W = a.d_c + a.d_rope;
-    if (a.slots) {
-        const int s = __ldg(a.slots + t);
-        if (s < 0) return -1;
-        if (s >= c.num_pages * c.page_size) {
-            if (lane == 0) set_status(a.status, MLA_ERR_PAGE);
-            return -1;
-        }
-        at = s * W;
-        return s;
+    int error = 0;
+    long long at = -1;
+    if (a.slots && r.slot < 0) return -1;
+    int b = t, j = 0;
+    if (!a.slots || (a.rotate && !a.positions)) {  // where the lengths say
+        b = a.s_q == 1 ? t : t / a.s_q;
+        j = r.len - a.s_q + (t - b * a.s_q);
+        if (!seq_len_ok(c, r.len)) error = MLA_ERR_SEQLEN;
+        if (!a.positions) r.pos = j;
     }
-    const int b = t / a.s_q, L = __ldg(c.seq_lens + b);
-    if (!seq_len_ok(c, L)) {
-        if (lane == 0) set_status(a.status, MLA_ERR_SEQLEN);
-        return -1;
-    }
-    const int j = L - a.s_q + t % a.s_q;
-    if (c.block_table == nullptr) {
+    if (!error && a.rotate && r.pos < 0) return -1;
+    if (error) {
+    } else if (a.slots) {
+        if (r.slot >= c.num_pages * c.page_size) error = MLA_ERR_PAGE;
+        at = r.slot * W;
+    } else if (c.block_table == nullptr) {
         at = (long long)b * c.seq_stride + j * W;
-        return j;
+    } else {
+        const int page = __ldg(c.block_table + (long long)b * c.max_pages + j / c.page_size);
+        if (page < 0 || page >= c.num_pages) error = MLA_ERR_PAGE;
+        at = ((long long)page * c.page_size + j % c.page_size) * W;
     }
-    const int page = __ldg(c.block_table + (long long)b * c.max_pages + j / c.page_size);
-    if (page < 0 || page >= c.num_pages) {
-        if (lane == 0) set_status(a.status, MLA_ERR_PAGE);
+    if (error) {
+        if (lane == 0) set_status(a.status, error);
         return -1;
     }
-    at = ((long long)page * c.page_size + j % c.page_size) * W;
-    return j;
+    return at;
+}
+
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
 }
 
 template <bool kFp8, bool kHalf>
 __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant__ StoreArgs a) {
-    const int lane = threadIdx.x % 32, t = blockIdx.x * kWarps + threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, nw = gridDim.x * kWarps;
+    const int nc = a.d_c / 8, nf = a.d_rope / 2;
+    int t = blockIdx.x * kWarps + threadIdx.x / 32;
     if (t >= a.tokens) return;
-    const __nv_bfloat16 *src = a.x + t * a.token_stride;
-    const int nc = a.d_c / 8;
-    // the row's loads first: none of them waits for the slot, the position or the weight
-    uint4 raw[2] = {}, wt[2] = {};
+    Row row = load_row<kHalf>(a, t, lane);
+    float wt[2][8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int c = lane + 32 * i;
-        if (c < nc) {
-            raw[i] = *(reinterpret_cast<const uint4 *>(src) + c);
-            if (a.weight) wt[i] = __ldg(reinterpret_cast<const uint4 *>(a.weight) + c);
-        }
-    }
-    const int nf = a.d_rope / 2;
-    float u = 0.f, v = 0.f;
-    if (lane < nf) {
-        const __nv_bfloat16 *k = src + a.d_c;
-        if (kHalf) {
-            u = __bfloat162float(k[lane]);
-            v = __bfloat162float(k[lane + nf]);
-        } else {
-            const float2 uv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(k + 2 * lane));
-            u = uv.x;
-            v = uv.y;
-        }
-    }
-    long long at = 0;
-    if (store_row(a, t, lane, at) < 0) return;
-    if (a.rotate) {
-        int pos;
-        if (a.positions) {
-            pos = __ldg(a.positions + t);
-        } else {
-            const int L = __ldg(a.cache.seq_lens + t / a.s_q);
-            pos = L - a.s_q + t % a.s_q;
-            if (!seq_len_ok(a.cache, L)) {  // slots with the lengths' positions
-                if (lane == 0) set_status(a.status, MLA_ERR_SEQLEN);
-                return;
-            }
-        }
-        if (pos < 0) return;
-        if (lane < nf) {
-            const float2 y = rope_turn(u, v, rope_cos_sin(a.plan.turn[lane], pos, a.plan.mscale, 1.f));
-            u = y.x;
-            v = y.y;
-        }
-    }
-    float f[2][8], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t w4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (a.weight && lane + 32 * i < nc) v = __ldg(reinterpret_cast<const uint4 *>(a.weight) + lane + 32 * i);
+        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float2 p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w4[e]));
-            f[i][2 * e] = p.x;
-            f[i][2 * e + 1] = p.y;
-            sum = fmaf(p.x, p.x, fmaf(p.y, p.y, sum));
+            const float2 p = unpack(w4[e]);
+            wt[i][2 * e] = p.x;
+            wt[i][2 * e + 1] = p.y;
         }
     }
-    if (a.weight) {
+    const float part = 1.f / (float)a.d_c;
+    const unsigned long long turn = a.rotate && lane < nf ? a.plan.turn[lane] : 0;
+    while (true) {
+        const int next = t + nw;
+        const bool more = next < a.tokens;
+        Row r = row;
+        if (more) row = load_row<kHalf>(a, next, lane);  // on its way while this row is computed
+        const long long at = row_offset(a, r, t, lane);
+        if (at >= 0) {
+            float f[2][8], sum = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        const float r = 1.f / sqrtf(sum / (float)a.d_c + a.eps);
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w4[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t w4[4] = {wt[i].x, wt[i].y, wt[i].z, wt[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w4[e]));
-                f[i][2 * e] *= r * p.x;
-                f[i][2 * e + 1] *= r * p.y;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 p = unpack(w4[e]);
+                    f[i][2 * e] = p.x;
+                    f[i][2 * e + 1] = p.y;
+                    sum = fmaf(p.x, p.x, fmaf(p.y, p.y, sum));
+                }
             }
-        }
-    }
-    if (kFp8) {
-        uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
-        const float s = a.cache.kv_scale;
+            if (a.weight) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = lane + 32 * i;
-            if (c < nc)
-                *(reinterpret_cast<uint2 *>(dst) + c) =
-                    make_uint2(e4m3x2(f[i][0] / s, f[i][1] / s) | e4m3x2(f[i][2] / s, f[i][3] / s) << 16,
-                               e4m3x2(f[i][4] / s, f[i][5] / s) | e4m3x2(f[i][6] / s, f[i][7] / s) << 16);
-        }
-        if (lane < nf) {
-            const uint32_t k = e4m3x2(u / s, v / s);
-            dst += a.d_c;
-            if (kHalf) {
-                dst[lane] = (uint8_t)k;
-                dst[lane + nf] = (uint8_t)(k >> 8);
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                const float inv = rsqrtf(fmaf(sum, part, a.eps));
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[i][e] *= inv * wt[i][e];
+            }
+            float2 k = unpack(r.k);
+            if (a.rotate) k = rope_turn(k.x, k.y, rope_cos_sin(turn, r.pos, a.plan.mscale, 1.f));
+            if (kFp8) {
+                uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
+                const float s = a.cache.kv_scale;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = lane + 32 * i;
+                    if (c < nc)
+                        *(reinterpret_cast<uint2 *>(dst) + c) =
+                            make_uint2(e4m3x2(f[i][0] / s, f[i][1] / s) | e4m3x2(f[i][2] / s, f[i][3] / s) << 16,
+                                       e4m3x2(f[i][4] / s, f[i][5] / s) | e4m3x2(f[i][6] / s, f[i][7] / s) << 16);
+                }
+                if (lane < nf) {
+                    const uint32_t code = e4m3x2(k.x / s, k.y / s);
+                    dst += a.d_c;
+                    if (kHalf) {
+                        dst[lane] = (uint8_t)code;
+                        dst[lane + nf] = (uint8_t)(code >> 8);
+                    } else {
+                        *reinterpret_cast<unsigned short *>(dst + 2 * lane) = (unsigned short)code;
+                    }
+                }
             } else {
-                *reinterpret_cast<unsigned short *>(dst + 2 * lane) = (unsigned short)k;
-            }
-        }
-    } else {
-        __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(static_cast<const __nv_bfloat16 *>(a.cache.kv)) + at;
+                __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(static_cast<const __nv_bfloat16 *>(a.cache.kv)) + at;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = lane + 32 * i;
-            if (c < nc)
-                *(reinterpret_cast<uint4 *>(dst) + c) =
-                    make_uint4(sm100::pack_bf16x2(f[i][0], f[i][1]), sm100::pack_bf16x2(f[i][2], f[i][3]),
-                               sm100::pack_bf16x2(f[i][4], f[i][5]), sm100::pack_bf16x2(f[i][6], f[i][7]));
-        }
-        if (lane < nf) {
-            dst += a.d_c;
-            if (kHalf) {
-                dst[lane] = __float2bfloat16_rn(u);
-                dst[lane + nf] = __float2bfloat16_rn(v);
-            } else {
-                *reinterpret_cast<uint32_t *>(dst + 2 * lane) = sm100::pack_bf16x2(u, v);
+                for (int i = 0; i < 2; ++i) {
+                    const int c = lane + 32 * i;
+                    if (c < nc)
+                        *(reinterpret_cast<uint4 *>(dst) + c) =
+                            make_uint4(sm100::pack_bf16x2(f[i][0], f[i][1]), sm100::pack_bf16x2(f[i][2], f[i][3]),
+                                       sm100::pack_bf16x2(f[i][4], f[i][5]), sm100::pack_bf16x2(f[i][6], f[i][7]));
+                }
+                if (lane < nf) {
+                    dst += a.d_c;
+                    if (kHalf) {
+                        dst[lane] = __float2bfloat16_rn(k.x);
+                        dst[lane + nf] = __float2bfloat16_rn(k.y);
+                    } else {
+                        *reinterpret_cast<uint32_t *>(dst + 2 * lane) = sm100::pack_bf16x2(k.x, k.y);
+                    }
+                }
             }
         }
+        if (!more) return;
+        t = next;
     }
 }
 
 }  // namespace
 
 cudaError_t launch_latent_store(const StoreArgs &a, cudaStream_t st) {
-    const int grid = (a.tokens + kWarps - 1) / kWarps;
+    int grid = (a.tokens + kWarps - 1) / kWarps;
+    if (grid > layer_num_sms() * kCtasPerSm) grid = layer_num_sms() * kCtasPerSm;
     const bool half = a.rotate && a.plan.layout == MLA_ROPE_HALF;
     if (a.cache.kv_fp8) {
         if (half) latent_rows<true, true><<<grid, 32 * kWarps, 0, st>>>(a);

@@ -209,7 +209,7 @@ MLA_API int mla_pages_update(const mla_page_pool *pool, const int *old_lens, con
         return MLA_ERR_UNSUPPORTED;
     mla::PagesArgs a{pool->B, pool->page_size, pool->max_pages, pool->num_pages, max_tokens, pool->block_table,
                      pool->free_ring, pool->state, pool->state_out, old_lens, new_lens, seq_lens, token_start,
-                     positions, slots, status};
+                     positions, slots, status, 64.f / (float)pool->page_size};
     return result(mla::launch_pages_update(a, as_stream(stream)));
 }
 
@@ -273,9 +273,10 @@ MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, c
                        void *out, void *workspace, size_t ws_bytes, void *stream) {
     int s = check_linear(d, residual != nullptr);
     if (s) return s;
-    if (!workspace) return MLA_ERR_NULL;
+    const size_t need = mla_linear_workspace_size(d);
+    if (!workspace && need > 256) return MLA_ERR_NULL;
     if (!aligned(workspace, 16)) return MLA_ERR_ALIGN;
-    if (ws_bytes < mla_linear_workspace_size(d)) return MLA_ERR_WORKSPACE;
+    if (ws_bytes < need) return MLA_ERR_WORKSPACE;
     if (d->M == 0) return MLA_OK;
     if (!x || !w || !out) return MLA_ERR_NULL;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16))

@@ -6,16 +6,24 @@
 // ring that is nearly all weights, and the epilogue's lanes are 32 neighbouring
 // columns of one output row.
 //
-// K runs in chunks of 64 through a ring of TMA stages.  The work is tiles x chunks.
-// With many tiles, a CTA takes whole tiles; with few, the tiles laid end to end are
-// dealt out in equal runs of chunks, one a CTA: a run covers the end of one tile,
-// whole ones, and the start of another.  A whole tile is finished in place; the
-// pieces of a cut one go to the workspace in fp32, and a second kernel adds them in
-// the order of K and applies the epilogue, so that results do not depend on which
-// CTA was first.
+// K runs in chunks of 64 through a ring of TMA stages.  The work is tiles x chunks, cut
+// in one of three ways:
+//   whole    a CTA takes whole tiles;
+//   cluster  2, 4 or 8 CTAs of a cluster take a tile's K in equal parts, exchange their
+//            accumulators through distributed shared memory and finish a share of the
+//            tokens each;
+//   runs     the tiles laid end to end are dealt out in equal runs of chunks, one a CTA:
+//            the end of one tile, whole ones, the start of another.  The pieces of a cut
+//            tile go to the workspace in fp32, and a second kernel joins them.
+// Parts are always added in the order of K, so results do not depend on timing.
 //
-// Warps: 0 issues the loads, 1 the MMAs, 2-5 drain the accumulators (two of them, so
-// that one tile's epilogue runs beside the next one's products).
+// Warps: 0 issues the loads, 1 the MMAs, 2-9 drain the accumulators (two of them, so
+// that one tile's epilogue runs beside the next one's products).  The epilogue turns its
+// 32 columns x 16 tokens over in shared memory, so that a lane has 8 columns of a token:
+// residual and output move as 16 bytes a lane (column by column, 2 bytes a lane, a
+// 256-token tile's epilogue took 36 us; it is the tail of the whole launch).
+#include <atomic>
+
 #include "layer.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -27,14 +35,18 @@ using namespace sm100;
 
 constexpr int kBN = 128;  // columns of W a tile
 constexpr int kBK = 64;
-constexpr int kThreads = 192;
-constexpr int kMinChunks = 4;  // chunks a CTA's run holds at least
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;  // two for each quarter of an accumulator's rows
+constexpr int kStep = 16;     // tokens an epilogue warp turns over at a time
+constexpr int kPitch = 36;  // floats between the tokens of a turned tile: conflict-free columns, 16-byte rows
+constexpr int kMinChunks = 4;  // chunks a CTA's run of a cut tile holds at least
 
 struct Plan {
     int bt;                // tokens a tile
     int tiles_m, tiles_n;  // tile t: tokens (t % tiles_m) * bt, columns (t / tiles_m) * 128
     int nk;                // chunks a tile
     int grid;
+    int cluster;           // CTAs that share a tile's K (1: none)
     bool whole;            // whole tiles, CTA g the tiles g, g + grid, ...; else runs of chunks
 };
 
@@ -42,18 +54,65 @@ __host__ __device__ __forceinline__ long long run_start(const Plan &p, int g) {
     return (long long)p.tiles_m * p.tiles_n * p.nk * g / p.grid;
 }
 
+// The plan with the shortest estimate, in SM cycles.  What the parts were measured to take
+// (clock traces at M = 64, 333, 2048 and 4096, K = 1000 to 16384):
+//   a chunk of a tile   about 400 cycles for narrow tiles (waits and issue), 455 at 128 tokens,
+//                       600 at 256 (the MMAs alone: 512); or what it takes the card to bring
+//                       the weights for all CTAs at work, at 3500 bytes a cycle
+//   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
+//   a cluster's exchange  about 2000 cycles
+//   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back
+// E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
+// tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters.
 Plan make_plan(int M, int K, int N, int sms) {
-    Plan p;
-    p.bt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-    p.tiles_m = (M + p.bt - 1) / p.bt;
-    p.tiles_n = (N + kBN - 1) / kBN;
-    p.nk = (K + kBK - 1) / kBK;
-    const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    p.whole = tiles >= 2 * sms;
-    const long long most = p.whole ? tiles : (tiles * p.nk + kMinChunks - 1) / kMinChunks;
-    p.grid = most < sms ? (int)most : sms;
-    if (tiles % p.grid == 0) p.whole = true;  // equal runs of chunks are whole tiles
-    return p;
+    Plan best{};
+    double best_cost = 0.0;
+    for (int bt = 16; bt <= 256; bt *= 2) {
+        if (bt > 16 && bt / 2 >= M) break;
+        Plan p;
+        p.bt = bt;
+        p.tiles_m = (M + bt - 1) / bt;
+        p.tiles_n = (N + kBN - 1) / kBN;
+        p.nk = (K + kBK - 1) / kBK;
+        const long long tiles = (long long)p.tiles_m * p.tiles_n;
+        if (tiles > (1ll << 28)) continue;
+        auto chunk = [&](double ctas) {
+            const double c = 390.0 + 0.5 * bt > 2.35 * bt ? 390.0 + 0.5 * bt : 2.35 * bt;
+            const double hbm = ctas / p.tiles_m * 16384 / 3500.0;
+            return c < hbm ? hbm : c;
+        };
+        auto keep = [&](double cost) {
+            if (best.bt == 0 || cost < best_cost) {
+                best = p;
+                best_cost = cost;
+            }
+        };
+        const double epilogue = 1000.0 + 36.0 * bt;
+        p.whole = true;
+        for (p.cluster = 1; p.cluster <= 8; p.cluster *= 2) {
+            if (p.cluster > 1 && (p.nk < 2 * p.cluster || tiles > sms)) break;
+            // clusters that fit the SMs: fewer than an even share, as a cluster stays within
+            // one of the groups the SMs are built in
+            const int fit = p.cluster == 1 ? sms : p.cluster == 2 ? sms / 2 - 4 : p.cluster == 4 ? sms / 4 - 4 : sms / 8 - 5;
+            if (fit < 1) break;
+            const long long waves = (tiles + fit - 1) / fit;
+            p.grid = p.cluster > 1 ? (int)tiles * p.cluster : tiles < sms ? (int)tiles : sms;
+            const double at_work = (double)(tiles < fit ? tiles : fit) * p.cluster;
+            keep(waves * ((p.nk + p.cluster - 1) / p.cluster * chunk(at_work)) + epilogue +
+                 (p.cluster > 1 ? 2000.0 + (waves - 1) * (epilogue + 3000.0) : 0.0));
+        }
+        p.cluster = 1;
+        const long long most = (tiles * p.nk + kMinChunks - 1) / kMinChunks;
+        p.grid = most < sms ? (int)most : sms;
+        // equal runs of chunks are whole tiles; and over several waves whole tiles in order of
+        // the tokens share their weights in L2, which runs of tiles of a CTA's own do not
+        // (4096 x 16384 x 7168: 611 us whole, 775 us in runs)
+        if (tiles % p.grid == 0 || tiles >= 2 * sms) continue;
+        p.whole = false;
+        keep((double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk(p.grid) + epilogue + 6000.0 +
+             2.0 * (p.grid < tiles ? 2.0 * p.grid : p.grid + tiles) * kBN * bt * 4 / 3500.0);
+    }
+    return best;
 }
 
 template <int BT>
@@ -62,26 +121,34 @@ struct Smem {
     static constexpr int kXBytes = BT * kBK * 2;
     static constexpr int kStage = kWBytes + kXBytes;
     static constexpr int kStages = (200 * 1024) / kStage > 12 ? 12 : (200 * 1024) / kStage;
-    static constexpr int kBytes = kStages * kStage + 1024 /* barriers */ + 1024 /* alignment */;
+    static constexpr int kTurn = kEpiWarps * kStep * kPitch * 4;  // the epilogue warps' 16 tokens x 32 columns
+    static constexpr int kBytes = kStages * kStage + kTurn + 1024 /* barriers */ + 1024 /* alignment */;
+    static_assert(BT * kBN * 4 <= kStages * kStage, "a cluster's accumulators are exchanged in the ring");
     static constexpr uint32_t kTmemCols = 2 * BT < 32 ? 32 : 2 * BT;
 };
 
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {
     if (kAct == MLA_ACT_RELU) return v < 0.f ? 0.f : v;  // NaN stays
-    if (kAct == MLA_ACT_SILU) return v / (1.f + __expf(-v));
+    if (kAct == MLA_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
     // 1 + erf(z) = erfc(-z) and (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)): no cancellation where they are small
     if (kAct == MLA_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678f);
-    if (kAct == MLA_ACT_GELU_TANH) return v / (1.f + __expf(-1.59576912f * (v + 0.044715f * v * v * v)));
+    if (kAct == MLA_ACT_GELU_TANH) return __fdividef(v, 1.f + __expf(-1.59576912f * (v + 0.044715f * v * v * v)));
     return v;
 }
-__device__ __forceinline__ float activate(int act, float v) {
+template <int kAct, int N>
+__device__ __forceinline__ void activate_all(float (&v)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = activate<kAct>(v[e]);
+}
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&v)[N]) {
     switch (act) {
-        case MLA_ACT_RELU: return activate<MLA_ACT_RELU>(v);
-        case MLA_ACT_SILU: return activate<MLA_ACT_SILU>(v);
-        case MLA_ACT_GELU: return activate<MLA_ACT_GELU>(v);
-        case MLA_ACT_GELU_TANH: return activate<MLA_ACT_GELU_TANH>(v);
-        default: return v;
+        case MLA_ACT_RELU: activate_all<MLA_ACT_RELU>(v); break;
+        case MLA_ACT_SILU: activate_all<MLA_ACT_SILU>(v); break;
+        case MLA_ACT_GELU: activate_all<MLA_ACT_GELU>(v); break;
+        case MLA_ACT_GELU_TANH: activate_all<MLA_ACT_GELU_TANH>(v); break;
+        default: break;
     }
 }
 
@@ -93,11 +160,22 @@ struct Walk {
     const Plan &p;
     long long u, end;
     __device__ __forceinline__ Walk(const Plan &plan, int g) : p(plan) {
+        if (p.cluster > 1) {
+            u = g / p.cluster;
+            end = u + 1;
+            return;
+        }
         u = p.whole ? g : run_start(p, g);
         end = p.whole ? (long long)p.tiles_m * p.tiles_n : run_start(p, g + 1);
     }
     __device__ __forceinline__ bool next(Segment &s) {
         if (u >= end) return false;
+        if (p.cluster > 1) {
+            const int rank = blockIdx.x % p.cluster;
+            s = Segment{(int)u, p.nk * rank / p.cluster, p.nk * (rank + 1) / p.cluster};
+            u = end;
+            return true;
+        }
         if (p.whole) {
             s = Segment{(int)u, 0, p.nk};
             u += p.grid;
@@ -110,6 +188,61 @@ struct Walk {
         return true;
     }
 };
+
+// The epilogue of 8 columns of some of a tile's tokens.
+struct Finish {
+    int t0, n;  // the tile's first token, the first column
+    float bias[8];
+    uint4 res[2];
+
+    __device__ __forceinline__ Finish(const LinearArgs &a, int t0, int n) : t0(t0), n(n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bias[e] = 0.f;
+        if (a.bias && n < a.N) unpack8(*reinterpret_cast<const uint4 *>(a.bias + n), bias);
+    }
+    static __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
+            f[2 * e] = p.x;
+            f[2 * e + 1] = p.y;
+        }
+    }
+    // the residual of tokens t and t + 8 of the tile (those below nt).  out may be residual:
+    // a value is loaded by the thread that stores it, before it does
+    __device__ __forceinline__ void load_residual(const LinearArgs &a, int t, int nt) {
+        if (!a.residual || n >= a.N) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (t + 8 * i < nt)
+                res[i] = *reinterpret_cast<const uint4 *>(a.residual + (long long)(t0 + t + 8 * i) * a.residual_stride + n);
+    }
+    __device__ __forceinline__ void load_half(const LinearArgs &a, int t, int nt) {  // token t alone
+        if (a.residual && n < a.N && t < nt)
+            res[0] = *reinterpret_cast<const uint4 *>(a.residual + (long long)(t0 + t) * a.residual_stride + n);
+    }
+    // v: the products' sums of 8 columns of token t
+    __device__ __forceinline__ void store(const LinearArgs &a, int t, int nt, const float *v, uint4 res) const {
+        if (t >= nt || n >= a.N) return;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = v[e] + bias[e];
+        activate(a.act, y);
+        if (a.residual) {
+            float r[8];
+            unpack8(res, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += r[e];
+        }
+        *reinterpret_cast<uint4 *>(a.out + (long long)(t0 + t) * a.out_stride + n) =
+            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+};
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 
 // Bounded wait that also ends when another warp of the CTA gave up.
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
@@ -125,20 +258,44 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
     }
 }
 
+// The same for a whole warp, unless it is `over` already: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(bool over, uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    if (__all_sync(~0u, over)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    const long long c0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+        if ((it & 15u) == 0 && __any_sync(~0u, *abort_flag || wait_expired(t0, c0))) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 template <int BT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, LinearArgs a, Plan plan) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using L = Smem<BT>;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTurn);
     uint64_t *empty = full + L::kStages;
     uint64_t *acc_full = empty + L::kStages;
     uint64_t *acc_empty = acc_full + 2;
     uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     pdl_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -148,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], kEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -164,96 +321,115 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk(plan, blockIdx.x);
     Segment seg;
 
-    if (warp == 0 && lane == 0) {
-        uint32_t it = 0;
-        bool ok = true;
+    // The loads' and the MMAs' loops are run by whole warps on values that are the same in
+    // every lane, and one elected lane issues: the operands stay in uniform registers.  (With
+    // the loops in a single lane, a chunk took 583 cycles whatever its width, all of it
+    // issue; the MMAs of the widest tile take 512.)
+    if (warp == 0) {
+        uint32_t s = 0, phase = 1, issued = 0;
+        bool ok = true, free = mbar_test_wait(&empty[0], 1);
         while (ok && walk.next(seg)) {
             const int t0 = seg.tile % plan.tiles_m * BT, n0 = seg.tile / plan.tiles_m * kBN;
-            for (int kc = seg.k0; kc < seg.k1; ++kc, ++it) {
-                const uint32_t s = it % L::kStages;
-                if (it >= L::kStages && !wait_or_abort(&empty[s], (it / L::kStages - 1) & 1, abort_flag)) {
+            for (int kc = seg.k0; kc < seg.k1; ++kc) {
+                // the first round's waits are for the phase before the barriers' first: over at once
+                if (!warp_wait(free, &empty[s], phase, abort_flag)) {
                     ok = false;
                     break;
                 }
                 uint8_t *st = smem + s * L::kStage;
-                mbar_arrive_expect_tx(&full[s], L::kStage);
-                tma_load_2d(st, &tm_w, &full[s], n0, kc * kBK);
-                tma_load_2d(st + L::kWBytes / 2, &tm_w, &full[s], n0 + 64, kc * kBK);
-                tma_load_2d(st + L::kWBytes, &tm_x, &full[s], kc * kBK, t0);
+                uint64_t *bar = &full[s];
+                if (++s == L::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+                free = mbar_test_wait(&empty[s], phase);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, L::kStage);
+                    tma_load_2d(st, &tm_w, bar, n0, kc * kBK);
+                    tma_load_2d(st + L::kWBytes / 2, &tm_w, bar, n0 + 64, kc * kBK);
+                    tma_load_2d(st + L::kWBytes, &tm_x, bar, kc * kBK, t0);
+                }
+                ++issued;
             }
         }
         // given up: the copies in flight still land in this CTA's shared memory
         if (!ok)
-            for (uint32_t i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
+            for (uint32_t i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
                 mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         constexpr uint32_t idesc = idesc_bf16(kBN, BT, true, false);
-        uint32_t it = 0, n_seg = 0;
-        bool ok = true;
+        // descriptors of stage 0: a stage and a step of K move the start address (in 16 bytes)
+        const uint64_t w_desc = smem_desc_sw128(smem_u32(smem), 64 * 128, 1024);
+        const uint64_t x_desc = smem_desc_sw128(smem_u32(smem) + L::kWBytes, 16, 1024);
+        const uint32_t acc0 = __shfl_sync(~0u, tmem, 0);
+        uint32_t s = 0, phase = 0, n_seg = 0;
+        bool ok = true, there = false;
         for (; ok && walk.next(seg); ++n_seg) {
             const uint32_t b = n_seg & 1;
-            if (n_seg >= 2 && !wait_or_abort(&acc_empty[b], (n_seg / 2 - 1) & 1, abort_flag)) break;
+            if (n_seg >= 2 && !warp_wait(false, &acc_empty[b], (n_seg / 2 - 1) & 1, abort_flag)) break;
             tc_fence_after();
-            const uint32_t d = tmem + b * BT;
-            for (int kc = seg.k0; kc < seg.k1; ++kc, ++it) {
-                const uint32_t s = it % L::kStages;
-                if (!wait_or_abort(&full[s], (it / L::kStages) & 1, abort_flag)) {
+            const uint32_t d = acc0 + b * BT;
+            for (int kc = seg.k0; kc < seg.k1; ++kc) {
+                if (!warp_wait(there, &full[s], phase, abort_flag)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t sw = smem_u32(smem + s * L::kStage), sx = sw + L::kWBytes;
+                const uint64_t dw = w_desc + (uint64_t)(s * (L::kStage >> 4)), dx = x_desc + (uint64_t)(s * (L::kStage >> 4));
+                uint64_t *bar = &empty[s];
+                if (++s == L::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+                there = mbar_test_wait(&full[s], phase);  // its answer comes while the MMAs are issued
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk)
-                    mma_ss(d, smem_desc_sw128(sw + kk * 16 * 128, 64 * 128, 1024), smem_desc_sw128(sx + kk * 32, 16, 1024),
-                           idesc, kc > seg.k0 || kk > 0);
-                mma_commit(&empty[s]);
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        mma_ss(d, dw + kk * (16 * 128 >> 4), dx + kk * (32 >> 4), idesc, kk > 0 || kc > seg.k0);
+                    mma_commit(bar);
+                    if (kc + 1 == seg.k1) mma_commit(&acc_full[b]);
+                }
             }
-            if (ok) mma_commit(&acc_full[b]);
         }
-        if (*abort_flag) {  // let the MMAs in flight end before the memory they use is given up
-            mma_commit(drain);
+        if (!ok || *abort_flag) {  // let the MMAs in flight end before the memory they use is given up
+            if (elect_one()) mma_commit(drain);
             mbar_wait(drain, 0);
         }
     } else if (warp >= 2) {
-        const int q = warp & 3;
-        const int nl = q * 32 + lane;
+        const int q = warp & 3, c0 = (warp - 2) / 4 * kStep;  // its rows, and its first tokens
         bool ok = true;
         bool first_seg = true;
-        for (uint32_t n_seg = 0; walk.next(seg); ++n_seg) {
+        float *turn = reinterpret_cast<float *>(smem + L::kStages * L::kStage) + (warp - 2) * kStep * kPitch;
+        for (uint32_t n_seg = 0; plan.cluster == 1 && walk.next(seg); ++n_seg) {
             const uint32_t b = n_seg & 1;
-            ok = ok && wait_or_abort(&acc_full[b], (n_seg / 2) & 1, abort_flag);
-            tc_fence_after();
-            const int t0 = seg.tile % plan.tiles_m * BT, n = seg.tile / plan.tiles_m * kBN + nl;
-            const bool cut = seg.k0 > 0 || seg.k1 < plan.nk;
-            float *part = a.part + (2ll * blockIdx.x + (first_seg ? 0 : 1)) * (kBN * BT) + nl;
-            const float bias = a.bias && n < a.N ? __bfloat162float(a.bias[n]) : 0.f;
+            const int t0 = seg.tile % plan.tiles_m * BT, n0 = seg.tile / plan.tiles_m * kBN;
+            const bool cut = !plan.whole && (seg.k0 > 0 || seg.k1 < plan.nk);
             const int nt = min(BT, a.M - t0);
-            for (int c = 0; c < nt; c += 16) {
-                uint32_t r[16];
-                tmem_ld16(tmem + tmem_lane_base(q) + b * BT + c, r);
+            const uint32_t acc = tmem + tmem_lane_base(q) + b * BT;
+            Finish fin(a, t0, n0 + q * 32 + lane % 4 * 8);
+            if (!cut) fin.load_residual(a, c0 + lane / 4, nt);
+            ok = ok && wait_or_abort(&acc_full[b], (n_seg / 2) & 1, abort_flag);
+            __syncwarp();
+            tc_fence_after();
+            float *part = a.part + (2ll * blockIdx.x + (first_seg ? 0 : 1)) * (kBN * BT) + q * 32 + lane;
+            for (int c = c0; c < nt; c += 2 * kStep) {
+                uint32_t r[kStep];
+                tmem_ld16(acc + c, r);
                 tmem_ld_wait();
                 if (!ok)
-                    for (int e = 0; e < 16; ++e) r[e] = 0x7fc00000u;
+                    for (int e = 0; e < kStep; ++e) r[e] = 0x7fc00000u;
                 if (cut) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
+                    for (int e = 0; e < kStep; ++e)
                         if (c + e < nt) part[(c + e) * kBN] = __uint_as_float(r[e]);
-                } else if (n < a.N) {
-                    // all the residual's loads before the first store (out may be residual)
-                    __nv_bfloat16 res[16];
-                    if (a.residual) {
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (c + e < nt) res[e] = a.residual[(long long)(t0 + c + e) * a.residual_stride + n];
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        if (c + e >= nt) break;
-                        float v = activate(a.act, __uint_as_float(r[e]) + bias);
-                        if (a.residual) v += __bfloat162float(res[e]);
-                        a.out[(long long)(t0 + c + e) * a.out_stride + n] = __float2bfloat16_rn(v);
-                    }
+                    for (int e = 0; e < kStep; ++e) turn[e * kPitch + lane] = __uint_as_float(r[e]);
+                    __syncwarp();
+                    uint4 res = fin.res[0], res1 = fin.res[1];
+                    fin.load_residual(a, c + 2 * kStep + lane / 4, nt);  // the next tokens', under way meanwhile
+#pragma unroll 1
+                    for (int t = lane / 4; t < kStep; t += 8, res = res1)
+                        fin.store(a, c + t, nt, turn + t * kPitch + lane % 4 * 8, res);
                 }
                 __syncwarp();
             }
@@ -261,6 +437,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[b]);
             first_seg = false;
+        }
+    }
+    if (plan.cluster > 1) {
+        // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
+        // have, takes the parts of the tokens this CTA finishes, one slot a rank.
+        const int rank = blockIdx.x % plan.cluster, share = BT / plan.cluster;
+        const int tile = blockIdx.x / plan.cluster, t0 = tile % plan.tiles_m * BT, n0 = tile / plan.tiles_m * kBN;
+        const int nt = min(BT, a.M - t0), i0 = threadIdx.x - 64;  // 16 threads a token, 8 columns each
+        const int first = rank * share, last = min(nt, first + share);
+        Finish fin(a, t0, warp >= 2 ? n0 + i0 % 16 * 8 : a.N);
+        bool ok = true;
+        if (warp >= 2) {
+            fin.load_half(a, first + i0 / 16, last);
+            ok = wait_or_abort(&acc_full[0], 0, abort_flag);
+        }
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2) {
+            tc_fence_after();
+            const int q = warp & 3;
+            const uint32_t slot = smem_u32(smem) + (uint32_t)(rank * share * kBN + q * 32 + lane) * 4;
+            const int step = share < 16 ? share : 16;
+            // the quarter's two warps take every other run of 16 tokens
+            for (int c = (warp - 2) / 4 * step; c < nt; c += 2 * step) {
+                uint32_t r[16];
+                tmem_ld16(tmem + tmem_lane_base(q) + c, r);
+                tmem_ld_wait();
+                const int to = c / share;
+                const uint32_t at = map_to_rank(slot + (uint32_t)(c - to * share) * (kBN * 4), to);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < step) st_cluster_f32(at + e * (kBN * 4), ok ? __uint_as_float(r[e]) : __int_as_float(0x7fc00000));
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        cluster_sync();
+        const float *mine = reinterpret_cast<const float *>(smem) + i0 % 16 * 8;
+        // 16 tokens at a time, the next ones' residual under way meanwhile
+        for (int t = i0 / 16; warp >= 2 && first + t < last; t += 16) {
+            const uint4 res = fin.res[0];
+            fin.load_half(a, first + t + 16, last);
+            float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < plan.cluster; ++s) {
+                const float4 *v = reinterpret_cast<const float4 *>(mine + (s * share + t) * kBN);
+                const float4 lo = v[0], hi = v[1];
+                sum[0] += lo.x; sum[1] += lo.y; sum[2] += lo.z; sum[3] += lo.w;
+                sum[4] += hi.x; sum[5] += hi.y; sum[6] += hi.z; sum[7] += hi.w;
+            }
+            fin.store(a, first + t, last, sum, res);
         }
     }
     tc_fence_before();
@@ -300,18 +526,20 @@ __global__ void __launch_bounds__(32 * kJoinTokens) linear_join(LinearArgs a, Pl
     };
     if (a.bias) load4(a.bias + n, bias);
     if (a.residual) load4(a.residual + t * a.residual_stride + n, res);
+    // the first CTA's run may have begun with another tile, the others' begin with this one
+    const int slot0 = run_start(plan, g0) < u0 ? 1 : 0;
+    const float *piece = a.part + (2ll * g0 + slot0) * (kBN * plan.bt) + t_in * kBN + nl;
     pdl_wait();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int g = g0; g <= g1; ++g) {
-        const int slot = run_start(plan, g) >= u0 ? 0 : run_start(plan, g) / plan.nk == tile ? 0 : 1;
-        const float4 v = *reinterpret_cast<const float4 *>(a.part + (2ll * g + slot) * (kBN * plan.bt) + t_in * kBN + nl);
+        const float4 v = *reinterpret_cast<const float4 *>(piece + (2ll * (g - g0) - (g > g0 ? slot0 : 0)) * (kBN * plan.bt));
         acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
-    const float y[4] = {acc.x, acc.y, acc.z, acc.w};
-    float o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = activate(a.act, y[e] + bias[e]) + res[e];
-    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + n) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    float y[4] = {acc.x + bias[0], acc.y + bias[1], acc.z + bias[2], acc.w + bias[3]};
+    activate(a.act, y);
+    *reinterpret_cast<uint2 *>(a.out + t * a.out_stride + n) =
+        make_uint2(pack_bf16x2(y[0] + res[0], y[1] + res[1]), pack_bf16x2(y[2] + res[2], y[3] + res[3]));
 }
 
 template <int BT>
@@ -323,10 +551,26 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
     if (!encode_bf16_sw128(&tm_w, a.w, 2, wd, ws, wb) || !encode_bf16_sw128(&tm_x, a.x, 2, xd, xs, xb))
         return cudaErrorInvalidValue;
     const int smem = Smem<BT>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(linear_tc<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    linear_tc<BT><<<p.grid, kThreads, smem, st>>>(tm_w, tm_x, a, p);
-    return cudaGetLastError();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    static std::atomic<unsigned long long> ready{0};  // devices the kernel's shared memory is allowed on
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(linear_tc<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_tc<BT>, tm_w, tm_x, a, p);
 }
 
 }  // namespace

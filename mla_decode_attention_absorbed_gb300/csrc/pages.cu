@@ -36,12 +36,24 @@ __device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
     r.old_len = __ldg(a.old_lens + b);
     r.new_len = __ldg(a.new_lens + b);
     const int most = a.max_pages * a.page_size;  // at most 2^30
+    // pages of n tokens: n / 64 is exact in fp32 up to 2^24, its quotient by the page's
+    // 64-token units within one of the fp32 product, which the remainder puts right
+    const int units = a.page_size >> 6;
+    const float inv = a.inv_units;
+    auto pages = [&](int n) {
+        const int m = (n + 63) >> 6;
+        int q = (int)((float)m * inv);
+        const int rest = m - q * units;
+        if (rest < 0) --q;
+        if (rest >= units) ++q;
+        return q * units < m ? q + 1 : q;
+    };
     r.valid = r.old_len >= 0 && r.new_len >= 0 && r.old_len <= most && r.new_len <= most;
     r.had = r.has = 0;
     r.n = Sums{0, 0, 0};
     if (r.valid) {
-        r.had = (r.old_len + a.page_size - 1) / a.page_size;
-        r.has = (r.new_len + a.page_size - 1) / a.page_size;
+        r.had = pages(r.old_len);
+        r.has = pages(r.new_len);
         r.n = Sums{max(r.new_len - r.old_len, 0), max(r.has - r.had, 0), max(r.had - r.has, 0)};
     }
     return r;
@@ -92,6 +104,39 @@ __device__ __forceinline__ Request find_request(const PagesArgs &a, const Sums *
     }
     return r;
 }
+
+// Tokens [begin, end) of request b that lie in one page (or the rest of an unserved
+// request: pos -1).
+struct TokenRun {
+    int b, begin, end, pos, slot;
+    Sums before;
+    Request r;
+
+    __device__ __forceinline__ void locate(const PagesArgs &a, const Ring &ring, const Sums *first, int groups, int per, int k) {
+        // on through the next few requests, else by bisection
+        int steps = 0;
+        while (b >= 0 && sat_add(before.tokens, r.n.tokens) <= k) {
+            if (++steps > 4 || b + 1 >= a.B) {
+                b = -1;
+            } else {
+                before = add(before, r.n);
+                r = load_request(a, ++b);
+            }
+        }
+        if (b < 0) r = find_request<&Sums::tokens>(a, first, groups, per, k, b, before);
+        begin = k;
+        end = sat_add(before.tokens, r.n.tokens);
+        pos = slot = -1;
+        if (!served(a, ring, r, add(before, r.n))) return;
+        pos = r.old_len + (k - before.tokens);
+        const int col = pos / a.page_size, row = pos - col * a.page_size;
+        end = min(end, k + a.page_size - row);
+        const int page = col < r.had ? a.table[(long long)b * a.max_pages + col]
+                                     : __ldg(a.ring + ring_at(a, ring.head, before.taken + col - r.had));
+        if (page >= 0 && page < a.num_pages) slot = page * a.page_size + row;
+        else set_status(a.status, MLA_ERR_PAGE);
+    }
+};
 
 __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ PagesArgs a, int per) {
     __shared__ Sums first[kGroups];
@@ -162,6 +207,9 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
         if (!ring.ok || given < total.given) set_status(a.status, MLA_ERR_PAGE);
     }
 
+    // The three kinds of items begin a third of the grid apart, so that a small batch's run
+    // beside one another, not one after another.
+    const int rotated = gid + gsize / 3 < gsize ? gid + gsize / 3 : gid + gsize / 3 - gsize;
     for (int k = gid; k < taken; k += gsize) {
         int b;
         Sums before;
@@ -174,30 +222,47 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
         a.table[(long long)b * a.max_pages + r.had + (k - before.taken)] = page;
     }
     const int tail = ring.ok ? ring_at(a, ring.head, ring.count) : 0;
-    for (int k = gid; k < given; k += gsize) {
+    for (int k = rotated; k < given; k += gsize) {
         int b;
         Sums before;
         const Request r = find_request<&Sums::given>(a, first, groups, per, k, b, before);
         a.ring[ring_at(a, tail, k)] = a.table[(long long)b * a.max_pages + r.has + (k - before.given)];
     }
-    for (int k = gid; k < a.max_tokens; k += gsize) {
-        int pos = -1, slot = -1;
-        if (k < total.tokens) {
-            int b;
-            Sums before;
-            const Request r = find_request<&Sums::tokens>(a, first, groups, per, k, b, before);
-            if (served(a, ring, r, add(before, r.n))) {
-                pos = r.old_len + (k - before.tokens);
-                const int col = pos / a.page_size;
-                int page;
-                if (col < r.had) page = a.table[(long long)b * a.max_pages + col];
-                else page = __ldg(a.ring + ring_at(a, ring.head, before.taken + col - r.had));
-                if (page >= 0 && page < a.num_pages) slot = page * a.page_size + pos % a.page_size;
-                else set_status(a.status, MLA_ERR_PAGE);
+
+    // Tokens, four neighbours a lane.  A lane keeps the run it is in: neighbouring tokens of
+    // one request in one page, whose positions and slots count up from the run's first.
+    TokenRun run_of;
+    run_of.b = -1;
+    // A warp has a contiguous run of chunks, so that it walks on where it is.
+    const int warps = gsize / 32;
+    int w = gid / 32 + warps / 3;
+    if (w >= warps) w -= warps;
+    const long long chunks = ((long long)a.max_tokens + 127) / 128;
+    const long long c1 = chunks * (w + 1) / warps;
+    const bool wide = (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15) == 0;
+    for (long long c = chunks * w / warps; c < c1; ++c) {
+        const long long k0 = c * 128 + lane * 4;
+        int pos[4], slot[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int k = (int)k0 + e;
+            pos[e] = slot[e] = -1;
+            if (k >= total.tokens || k >= a.max_tokens) continue;
+            if (run_of.b < 0 || k >= run_of.end) run_of.locate(a, ring, first, groups, per, k);
+            if (run_of.pos >= 0) {
+                pos[e] = run_of.pos + (k - run_of.begin);
+                if (run_of.slot >= 0) slot[e] = run_of.slot + (k - run_of.begin);
             }
         }
-        a.positions[k] = pos;
-        a.slots[k] = slot;
+        if (wide && k0 + 4 <= a.max_tokens) {
+            *reinterpret_cast<int4 *>(a.positions + k0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(a.slots + k0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+            for (int e = 0; e < 4 && k0 + e < a.max_tokens; ++e) {
+                a.positions[k0 + e] = pos[e];
+                a.slots[k0 + e] = slot[e];
+            }
+        }
     }
 }
 
@@ -206,12 +271,13 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
 cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t st) {
     const int per = a.B > 0 ? (a.B + kGroups - 1) / kGroups : 1;
     const int groups = (a.B + per - 1) / per;
-    // enough threads for the groups' sums, and CTAs for the tokens
+    // enough threads for the groups' sums, and CTAs for the tokens (three at least: see the
+    // items' order)
     int threads = groups > 0 ? (groups + 31) / 32 * 32 : 32;
     if (threads < 256 && a.max_tokens > threads) threads = 256;
     const long long want = ((long long)a.max_tokens + 4 * threads - 1) / (4 * threads);
     const int sms = layer_num_sms();
-    const int grid = want < 1 ? 1 : want > sms ? sms : (int)want;
+    const int grid = want < 3 ? 3 : want > sms ? sms : (int)want;
     pages_update<<<grid, threads, 0, st>>>(a, per);
     return cudaGetLastError();
 }

@@ -84,12 +84,15 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st) {
-    // rows of one CTA: about 128 (128 heads of one token)
+    // Rows of one CTA: 128 where that makes four CTAs an SM, down to 16 where there are few.
+    int rows = 128;
+    const long long all = (long long)a.tokens * a.H;
+    while (rows > 16 && all < 4ll * layer_num_sms() * rows) rows /= 2;
     int tpb = 1, hpb = a.H;
-    if (a.H >= 128) {
-        hpb = 128;
+    if (a.H >= rows) {
+        hpb = rows;
     } else {
-        tpb = 128 / a.H;
+        tpb = rows / a.H;
         if (tpb > kMaxTokens) tpb = kMaxTokens;
     }
     const dim3 grid((a.tokens + tpb - 1) / tpb, (a.H + hpb - 1) / hpb);

@@ -420,16 +420,50 @@ def read_status(workspace, stream=None) -> int:
 
 
 # ------------------------------------------------------------- the layer around the attention
-def _want(t, what: str, dtype, shape=None, dense=True):
-    """t is a CUDA tensor of this type (and shape) on the current device, dense if asked."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+# These calls take a few microseconds on the GPU, so what a call costs on the host counts: every
+# property of a tensor is read once, and pointers and streams go to ctypes as plain integers.
+def _device(t, what: str) -> int:
+    """Index of t's device, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"{what} must be on the current CUDA device")
-    if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have the shape {shape}, not {tuple(t.shape)}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{what} must be dense")
+    return dev
+
+
+def _dense(t, what: str, dtype, dev: int, shape=None) -> int:
+    """Address of t, a dense tensor of this type (and shape) on device ``dev``."""
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what} must be a dense {dtype} tensor{'' if shape is None else f' {list(shape)}'} on device "
+                         f"{dev}, not {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _per_token(t, what: str, dev: int, tokens: int) -> int | None:
+    """Address of t, int32 with one entry a token, or None."""
+    if t is None:
+        return None
+    if t.numel() != tokens:
+        raise ValueError(f"{what} must hold one entry a token ({tokens}), not {t.numel()}")
+    return _dense(t, what, torch.int32, dev)
+
+
+def _rows(t, what: str, dev: int, shape) -> int:
+    """Address of t, a bf16 matrix of this shape with contiguous rows (any stride between them)."""
+    if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a torch.bfloat16 tensor {list(shape)} with contiguous rows on device {dev}, not "
+                         f"{t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+try:  # an allocation on the current device without the dispatcher: 1.3 us against torch.empty's 2.8 (Grace host)
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(shape, stride, dtype):
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
+
+def _raw_stream(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def rope_plan(d_rope: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0, scaling: int = ROPE_PLAIN,
@@ -449,45 +483,42 @@ def rope_plan(d_rope: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0
     return plan
 
 
-def _check_positions(prob: Problem, positions, seq_lens):
-    if positions is not None:
-        _want(positions, "positions", torch.int32)
-        if positions.numel() != prob.B * prob.s_q:
-            raise ValueError("positions must hold one entry a token")
-    if seq_lens is not None:
-        _want(seq_lens, "seq_lens", torch.int32, (prob.B,))
-
-
 def rope(prob: Problem, plan: RopePlan, x, positions=None, seq_lens=None, q_nope=None, q_rope=None,
          transpose: bool = False, stream=None):
     """mla_rope: x [B, s_q, H, d_nope + d_rope] (rows of heads may lie inside wider ones) split
     and rotated, returns (q_nope, q_rope); x [B, s_q, H, d_rope] rotated, returns q_rope (which
     may be x itself).  Tokens are at ``positions`` [B, s_q], or the last of ``seq_lens`` [B]."""
     lib = load()
-    B, s_q, H = prob.B, prob.s_q, prob.H
-    _want(x, "x", torch.bfloat16, dense=False)
-    if x.dim() != 4 or x.shape[:3] != (B, s_q, H) or x.stride(3) != 1 or (
-            B > 1 and s_q > 1 and x.stride(0) != s_q * x.stride(1)):
-        raise ValueError("x must be [B, s_q, H, width] with evenly spaced tokens and contiguous values")
-    split = x.shape[3] == prob.d_nope + prob.d_rope
-    if not split and x.shape[3] != prob.d_rope:
-        raise ValueError("x must have rows of d_nope + d_rope or d_rope values")
-    _check_positions(prob, positions, seq_lens)
-    if q_rope is None:
-        q_rope = torch.empty(B, s_q, H, prob.d_rope, dtype=torch.bfloat16, device=x.device)
-    else:
-        _want(q_rope, "q_rope", torch.bfloat16, (B, s_q, H, prob.d_rope))
-    if split and q_nope is None:
-        q_nope = torch.empty(B, s_q, H, prob.d_nope, dtype=torch.bfloat16, device=x.device)
-    elif split:
-        _want(q_nope, "q_nope", torch.bfloat16, (B, s_q, H, prob.d_nope))
+    B, s_q, H, d_nope, d_rope = prob.B, prob.s_q, prob.H, prob.d_nope, prob.d_rope
+    dev = _device(x, "x")
+    split = x.shape == (B, s_q, H, d_nope + d_rope)
+    if x.dtype != torch.bfloat16 or not (split or x.shape == (B, s_q, H, d_rope)):
+        raise ValueError(f"x must be torch.bfloat16 [B, s_q, H, d_nope + d_rope or d_rope], not {x.dtype} {list(x.shape)}")
+    st = x.stride()
+    if st[3] != 1 or (B > 1 and s_q > 1 and st[0] != s_q * st[1]):
+        raise ValueError(f"x must have contiguous values and evenly spaced tokens, not the strides {st}")
+    width = d_nope + d_rope if split else d_rope
+    head_stride = st[2] if H > 1 else width
+    token_stride = st[1] if s_q > 1 else st[0] if B > 1 else (H - 1) * head_stride + width
+    pos = _per_token(positions, "positions", dev, B * s_q)
+    lens = None if seq_lens is None else _dense(seq_lens, "seq_lens", torch.int32, dev, (B,))
+    nope = None
+    if split:
+        if q_nope is None:
+            q_nope = _empty_strided_cuda((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), torch.bfloat16)
+            nope = q_nope.data_ptr()
+        else:
+            nope = _dense(q_nope, "q_nope", torch.bfloat16, dev, (B, s_q, H, d_nope))
     elif q_nope is not None:
         raise ValueError("rows of d_rope values have no part for q_nope")
+    if q_rope is None:
+        q_rope = _empty_strided_cuda((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), torch.bfloat16)
+        turned = q_rope.data_ptr()
+    else:
+        turned = _dense(q_rope, "q_rope", torch.bfloat16, dev, (B, s_q, H, d_rope))
     d = prob.dims()
-    head_stride = x.stride(2) if H > 1 else x.shape[3]
-    token_stride = x.stride(1) if s_q > 1 else x.stride(0) if B > 1 else (H - 1) * head_stride + x.shape[3]
-    _check(lib.mla_rope(ctypes.byref(d), ctypes.byref(plan), _ptr(x), token_stride, head_stride, _ptr(positions),
-                        _ptr(seq_lens), _ptr(q_nope), _ptr(q_rope), int(transpose), _stream(stream)), "mla_rope")
+    _check(lib.mla_rope(ctypes.byref(d), ctypes.byref(plan), x.data_ptr(), token_stride, head_stride, pos, lens, nope,
+                        turned, int(transpose), _raw_stream(dev, stream)), "mla_rope")
     return (q_nope, q_rope) if split else q_rope
 
 
@@ -500,8 +531,9 @@ class Pages:
     page_size: int = 64
 
     def __post_init__(self):
-        _want(self.block_table, "block_table", torch.int32)
-        _want(self.free_ring, "free_ring", torch.int32)
+        dev = _device(self.block_table, "block_table")
+        _dense(self.block_table, "block_table", torch.int32, dev)
+        _dense(self.free_ring, "free_ring", torch.int32, dev)
         if self.block_table.dim() != 2 or self.free_ring.dim() != 1:
             raise ValueError("block_table must be [B, max_pages], free_ring [num_pages]")
 
@@ -529,27 +561,23 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
     """mla_pages_update: every request from old_lens[b] to new_lens[b] tokens.  ``out`` (the
     result of an earlier call) is written over; its tensors must not be this call's inputs."""
     lib = load()
-    B = pages.block_table.shape[0]
-    dev = pages.block_table.device
-    _want(ring_state, "ring_state", torch.int32, (2,))
-    _want(old_lens, "old_lens", torch.int32, (B,))
-    _want(new_lens, "new_lens", torch.int32, (B,))
-    if status is not None:
-        _want(status, "status", torch.int32)
+    table, ring = pages.block_table, pages.free_ring
+    dev = _device(table, "block_table")
+    B, max_pages = table.shape
+    state = _dense(ring_state, "ring_state", torch.int32, dev, (2,))
+    old = _dense(old_lens, "old_lens", torch.int32, dev, (B,))
+    new = _dense(new_lens, "new_lens", torch.int32, dev, (B,))
+    word = None if status is None else _dense(status, "status", torch.int32, dev)
     if out is None:
-        out = PagesStep(*(torch.empty(n, dtype=torch.int32, device=dev)
-                          for n in (B, 2, B + 1, max_tokens, max_tokens)))
+        out = PagesStep(*(_empty_strided_cuda((n,), (1,), torch.int32) for n in (B, 2, B + 1, max_tokens, max_tokens)))
+        at = [t.data_ptr() for t in (out.seq_lens, out.ring_state, out.token_start, out.positions, out.slots)]
     else:
-        for t, n, what in ((out.seq_lens, B, "seq_lens"), (out.ring_state, 2, "ring_state"),
-                           (out.token_start, B + 1, "token_start"), (out.positions, max_tokens, "positions"),
-                           (out.slots, max_tokens, "slots")):
-            _want(t, what, torch.int32, (n,))
-    pool = PagePool(B, pages.page_size, pages.block_table.shape[1], pages.free_ring.shape[0],
-                    pages.block_table.data_ptr(), pages.free_ring.data_ptr(), ring_state.data_ptr(),
-                    out.ring_state.data_ptr())
-    _check(lib.mla_pages_update(ctypes.byref(pool), _ptr(old_lens), _ptr(new_lens), max_tokens, _ptr(out.seq_lens),
-                                _ptr(out.token_start), _ptr(out.positions), _ptr(out.slots), _ptr(status),
-                                _stream(stream)), "mla_pages_update")
+        at = [_dense(t, what, torch.int32, dev, (n,)) for t, n, what in (
+            (out.seq_lens, B, "seq_lens"), (out.ring_state, 2, "ring_state"), (out.token_start, B + 1, "token_start"),
+            (out.positions, max_tokens, "positions"), (out.slots, max_tokens, "slots"))]
+    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], table.data_ptr(), ring.data_ptr(), state, at[1])
+    _check(lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, at[0], at[2], at[3], at[4], word,
+                                _raw_stream(dev, stream)), "mla_pages_update")
     return out
 
 
@@ -558,31 +586,17 @@ def latent_store(prob: Problem, x, cache: Cache, plan: RopePlan | None = None, n
     """mla_latent_store: rows [c | k] of the new tokens (x [B * s_q, d_c + d_rope], inside wider
     rows or not) normalised, rotated and written to the cache, whose kv buffer is modified."""
     lib = load()
-    _want(x, "x", torch.bfloat16, (prob.B * prob.s_q, prob.d_c + prob.d_rope), dense=False)
-    if x.stride(1) != 1:
-        raise ValueError("x must have contiguous values")
-    if norm_weight is not None:
-        _want(norm_weight, "norm_weight", torch.bfloat16, (prob.d_c,))
-    _check_positions(prob, positions, None)
-    if slots is not None:
-        _want(slots, "slots", torch.int32)
-        if slots.numel() != prob.B * prob.s_q:
-            raise ValueError("slots must hold one entry a token")
-    if status is not None:
-        _want(status, "status", torch.int32)
+    dev = _device(x, "x")
+    tokens, width = prob.B * prob.s_q, prob.d_c + prob.d_rope
+    rows = _rows(x, "x", dev, (tokens, width))
+    weight = None if norm_weight is None else _dense(norm_weight, "norm_weight", torch.bfloat16, dev, (prob.d_c,))
+    pos = _per_token(positions, "positions", dev, tokens)
+    slot = _per_token(slots, "slots", dev, tokens)
+    word = None if status is None else _dense(status, "status", torch.int32, dev)
     d = prob.dims()
-    stride = x.stride(0) if x.shape[0] > 1 else x.shape[1]
-    _check(lib.mla_latent_store(ctypes.byref(d), None if plan is None else ctypes.byref(plan), _ptr(x), stride,
-                                _ptr(norm_weight), float(eps), _ptr(positions), _ptr(slots), ctypes.byref(cache),
-                                _ptr(status), _stream(stream)), "mla_latent_store")
-
-
-def _linear_desc(x, w, out, residual, act) -> LinearDesc:
-    def stride(t, width):
-        return t.stride(0) if t is not None and t.shape[0] > 1 else width
-
-    N = w.shape[1]
-    return LinearDesc(x.shape[0], w.shape[0], N, act, stride(x, w.shape[0]), stride(out, N), stride(residual, N))
+    _check(lib.mla_latent_store(ctypes.byref(d), None if plan is None else ctypes.byref(plan), rows,
+                                x.stride(0) if tokens > 1 else width, weight, eps, pos, slot, ctypes.byref(cache), word,
+                                _raw_stream(dev, stream)), "mla_latent_store")
 
 
 def linear_workspace_size(M: int, K: int, N: int) -> int:
@@ -597,26 +611,31 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
     """mla_linear: residual + act(x . w + bias), x [M, K] and residual [M, N] with any row stride
     (multiples of 8), w [K, N] dense.  ``out`` may be ``residual``."""
     lib = load()
-    _want(x, "x", torch.bfloat16, dense=False)
-    _want(w, "w", torch.bfloat16)
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[0] or x.stride(1) != 1:
-        raise ValueError("x must be [M, K] with contiguous values, w [K, N]")
-    M, N = x.shape[0], w.shape[1]
-    if bias is not None:
-        _want(bias, "bias", torch.bfloat16, (N,))
-    for t, what in ((residual, "residual"), (out, "out")):
-        if t is not None:
-            _want(t, what, torch.bfloat16, (M, N), dense=False)
-            if t.stride(1) != 1:
-                raise ValueError(f"{what} must have contiguous values")
+    dev = _device(x, "x")
+    if w.dim() != 2 or x.dim() != 2:
+        raise ValueError("x must be [M, K], w [K, N]")
+    K, N = w.shape
+    M = x.shape[0]
+    rows, weight = _rows(x, "x", dev, (M, K)), _dense(w, "w", torch.bfloat16, dev)
+    b = None if bias is None else _dense(bias, "bias", torch.bfloat16, dev, (N,))
+    res = None if residual is None else _rows(residual, "residual", dev, (M, N))
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
-    desc = _linear_desc(x, w, out, residual, act)
+        out = _empty_strided_cuda((M, N), (N, 1), torch.bfloat16)
+        to = out.data_ptr()
+    else:
+        to = _rows(out, "out", dev, (M, N))
+    one = M <= 1  # a single row has no stride
+    desc = LinearDesc(M, K, N, act, K if one else x.stride(0), N if one else out.stride(0),
+                      N if one or residual is None else residual.stride(0))
+    at = ctypes.byref(desc)
     if workspace is None:
-        n = lib.mla_linear_workspace_size(ctypes.byref(desc))
-        workspace = alloc_workspace(n, x.device)
-    _check(lib.mla_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(out), _ptr(workspace),
-                          workspace.numel(), _stream(stream)), "mla_linear")
+        nbytes, ws = lib.mla_linear_workspace_size(at), None
+        if nbytes > 256:  # below that none is used
+            workspace = _empty_strided_cuda((nbytes,), (1,), torch.uint8)
+            ws = workspace.data_ptr()
+    else:
+        nbytes, ws = workspace.numel(), workspace.data_ptr()
+    _check(lib.mla_linear(at, rows, weight, b, res, to, ws, nbytes, _raw_stream(dev, stream)), "mla_linear")
     return out
 
 

@@ -162,8 +162,10 @@ def test_linear_refusals(lib):
         return lib.mla_linear(ctypes.byref(d), x, w, bias, residual, out, ws, nbytes, NUL)
 
     assert lib.mla_linear(None, A, A, A, A, A, A, 0, NUL) == 1
-    for name in ("x", "w", "out", "ws"):
+    for name in ("x", "w", "out"):
         assert call(**{name: NUL}) == 1, name
+    runs = desc(M=8, K=1000, N=20480, xs=1000, os=20480)  # 160 tiles: cut along K, with pieces in the workspace
+    assert lib.mla_linear_workspace_size(ctypes.byref(runs)) > 256 and call(runs, ws=NUL) == 1
     for name in ("x", "w", "bias", "residual", "out", "ws"):
         assert call(**{name: ODD}) == 4, name
     for bad, code in ((dict(M=-1), 2), (dict(K=0), 2), (dict(N=0), 2), (dict(K=60, xs=64), 4), (dict(N=124), 4),
