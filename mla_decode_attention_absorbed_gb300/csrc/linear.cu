@@ -48,6 +48,7 @@ struct Plan {
     int grid;
     int cluster;           // CTAs that share a tile's K (1: none)
     bool whole;            // whole tiles, CTA g the tiles g, g + grid, ...; else runs of chunks
+    bool pair;             // a tile is 256 columns, taken by a pair of CTAs
 };
 
 __host__ __device__ __forceinline__ long long run_start(const Plan &p, int g) {
@@ -88,6 +89,7 @@ Plan make_plan(int M, int K, int N, int sms) {
             }
         };
         const double epilogue = 1000.0 + 36.0 * bt;
+        p.pair = false;
         p.whole = true;
         for (p.cluster = 1; p.cluster <= 8; p.cluster *= 2) {
             if (p.cluster > 1 && (p.nk < 2 * p.cluster || tiles > sms)) break;
@@ -102,6 +104,15 @@ Plan make_plan(int M, int K, int N, int sms) {
                  (p.cluster > 1 ? 2000.0 + (waves - 1) * (epilogue + 3000.0) : 0.0));
         }
         p.cluster = 1;
+        if (bt == 256) {
+            p.pair = true;
+            p.tiles_n = (N + 2 * kBN - 1) / (2 * kBN);
+            const long long pairs = (long long)p.tiles_m * p.tiles_n, fit = sms / 2;
+            p.grid = 2 * (int)(pairs < fit ? pairs : fit);
+            keep((pairs + fit - 1) / fit * (p.nk * 530.0) + epilogue + 1000.0);
+            p.pair = false;
+            p.tiles_n = (N + kBN - 1) / kBN;
+        }
         const long long most = (tiles * p.nk + kMinChunks - 1) / kMinChunks;
         p.grid = most < sms ? (int)most : sms;
         // equal runs of chunks are whole tiles; and over several waves whole tiles in order of
@@ -115,10 +126,10 @@ Plan make_plan(int M, int K, int N, int sms) {
     return best;
 }
 
-template <int BT>
+template <int BT, bool kPair>
 struct Smem {
     static constexpr int kWBytes = kBN * kBK * 2;
-    static constexpr int kXBytes = BT * kBK * 2;
+    static constexpr int kXBytes = (kPair ? BT / 2 : BT) * kBK * 2;
     static constexpr int kStage = kWBytes + kXBytes;
     static constexpr int kStages = (200 * 1024) / kStage > 12 ? 12 : (200 * 1024) / kStage;
     static constexpr int kTurn = kEpiWarps * kStep * kPitch * 4;  // the epilogue warps' 16 tokens x 32 columns
@@ -165,7 +176,7 @@ struct Walk {
             end = u + 1;
             return;
         }
-        u = p.whole ? g : run_start(p, g);
+        u = p.pair ? g / 2 : p.whole ? g : run_start(p, g);
         end = p.whole ? (long long)p.tiles_m * p.tiles_n : run_start(p, g + 1);
     }
     __device__ __forceinline__ bool next(Segment &s) {
@@ -178,7 +189,7 @@ struct Walk {
         }
         if (p.whole) {
             s = Segment{(int)u, 0, p.nk};
-            u += p.grid;
+            u += p.pair ? p.grid / 2 : p.grid;
             return true;
         }
         s.tile = (int)(u / p.nk);
@@ -259,12 +270,13 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
 }
 
 // The same for a whole warp, unless it is `over` already: every lane gets the same answer.
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(bool over, uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     if (__all_sync(~0u, over)) return true;
     const uint64_t t0 = globaltimer_ns();
     const long long c0 = clock64();
     for (uint32_t it = 1;; ++it) {
-        if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(~0u, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
         if ((it & 15u) == 0 && __any_sync(~0u, *abort_flag || wait_expired(t0, c0))) {
             *abort_flag = 1;
             return false;
@@ -282,12 +294,50 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-template <int BT>
+// ---- the pair's forms: one MMA of 256 x BT over both CTAs' shared and tensor memory,
+// issued by the first of them (the leader)
+template <uint32_t kCols>
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst) {  // a whole warp in each CTA
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+template <uint32_t kCols>
+__device__ __forceinline__ void tmem_free_pair(uint32_t taddr) {  // a whole warp in each CTA
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "n"(kCols) : "memory");
+}
+// A copy into this CTA's shared memory whose bytes count on a barrier of the leader's
+// (a cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` of both CTAs when the MMAs issued so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int BT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, LinearArgs a, Plan plan) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    using L = Smem<BT>;
+    using L = Smem<BT, kPair>;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTurn);
     uint64_t *empty = full + L::kStages;
     uint64_t *acc_full = empty + L::kStages;
@@ -305,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kEpiWarps);
+            mbar_init(&acc_empty[i], kPair ? 2 * kEpiWarps : kEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -313,11 +363,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
     }
-    if (warp == 1) tmem_alloc<L::kTmemCols>(tmem_slot);
+    if (warp == 1) {
+        if (kPair) tmem_alloc_pair<L::kTmemCols>(tmem_slot);
+        else tmem_alloc<L::kTmemCols>(tmem_slot);
+    }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // the leader's barriers are ready for the other CTA
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // a tile's columns, and this CTA's part of them (and of its tokens' copies) in a pair
+    constexpr int kTileN = kPair ? 2 * kBN : kBN;
+    const int half = kPair ? (int)(blockIdx.x & 1) : 0;
     Walk walk(plan, blockIdx.x);
     Segment seg;
 
@@ -326,10 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the loops in a single lane, a chunk took 583 cycles whatever its width, all of it
     // issue; the MMAs of the widest tile take 512.)
     if (warp == 0) {
+        const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), 0) : 0;
         uint32_t s = 0, phase = 1, issued = 0;
         bool ok = true, free = mbar_test_wait(&empty[0], 1);
         while (ok && walk.next(seg)) {
-            const int t0 = seg.tile % plan.tiles_m * BT, n0 = seg.tile / plan.tiles_m * kBN;
+            const int t0 = seg.tile % plan.tiles_m * BT + half * (BT / 2);
+            const int n0 = seg.tile / plan.tiles_m * kTileN + half * kBN;
             for (int kc = seg.k0; kc < seg.k1; ++kc) {
                 // the first round's waits are for the phase before the barriers' first: over at once
                 if (!warp_wait(free, &empty[s], phase, abort_flag)) {
@@ -343,7 +402,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     phase ^= 1;
                 }
                 free = mbar_test_wait(&empty[s], phase);
-                if (elect_one()) {
+                if (kPair) {
+                    const uint32_t lead = lead_full + (uint32_t)(reinterpret_cast<uint8_t *>(bar) - reinterpret_cast<uint8_t *>(full));
+                    if (elect_one()) {
+                        if (half == 0) mbar_arrive_expect_tx(bar, 2 * L::kStage);
+                        tma_load_2d_pair(st, &tm_w, lead, n0, kc * kBK);
+                        tma_load_2d_pair(st + L::kWBytes / 2, &tm_w, lead, n0 + 64, kc * kBK);
+                        tma_load_2d_pair(st + L::kWBytes, &tm_x, lead, kc * kBK, t0);
+                    }
+                } else if (elect_one()) {
                     mbar_arrive_expect_tx(bar, L::kStage);
                     tma_load_2d(st, &tm_w, bar, n0, kc * kBK);
                     tma_load_2d(st + L::kWBytes / 2, &tm_w, bar, n0 + 64, kc * kBK);
@@ -352,12 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++issued;
             }
         }
-        // given up: the copies in flight still land in this CTA's shared memory
-        if (!ok)
+        // given up: the copies in flight still land in this CTA's shared memory (a pair's are
+        // counted by the leader)
+        if (!ok && half == 0)
             for (uint32_t i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
                 mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1);
-    } else if (warp == 1) {
-        constexpr uint32_t idesc = idesc_bf16(kBN, BT, true, false);
+    } else if (warp == 1 && half == 0) {
+        constexpr uint32_t idesc = idesc_bf16(kTileN, BT, true, false);
         // descriptors of stage 0: a stage and a step of K move the start address (in 16 bytes)
         const uint64_t w_desc = smem_desc_sw128(smem_u32(smem), 64 * 128, 1024);
         const uint64_t x_desc = smem_desc_sw128(smem_u32(smem) + L::kWBytes, 16, 1024);
@@ -366,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true, there = false;
         for (; ok && walk.next(seg); ++n_seg) {
             const uint32_t b = n_seg & 1;
-            if (n_seg >= 2 && !warp_wait(false, &acc_empty[b], (n_seg / 2 - 1) & 1, abort_flag)) break;
+            if (n_seg >= 2 && !warp_wait<kPair>(false, &acc_empty[b], (n_seg / 2 - 1) & 1, abort_flag)) break;
             tc_fence_after();
             const uint32_t d = acc0 + b * BT;
             for (int kc = seg.k0; kc < seg.k1; ++kc) {
@@ -384,14 +452,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        mma_ss(d, dw + kk * (16 * 128 >> 4), dx + kk * (32 >> 4), idesc, kk > 0 || kc > seg.k0);
-                    mma_commit(bar);
-                    if (kc + 1 == seg.k1) mma_commit(&acc_full[b]);
+                        (kPair ? mma_ss_pair : mma_ss)(d, dw + kk * (16 * 128 >> 4), dx + kk * (32 >> 4), idesc,
+                                                       kk > 0 || kc > seg.k0);
+                    (kPair ? mma_commit_pair : mma_commit)(bar);
+                    if (kc + 1 == seg.k1) (kPair ? mma_commit_pair : mma_commit)(&acc_full[b]);
                 }
             }
         }
         if (!ok || *abort_flag) {  // let the MMAs in flight end before the memory they use is given up
-            if (elect_one()) mma_commit(drain);
+            if (elect_one()) (kPair ? mma_commit_pair : mma_commit)(drain);
             mbar_wait(drain, 0);
         }
     } else if (warp >= 2) {
@@ -401,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float *turn = reinterpret_cast<float *>(smem + L::kStages * L::kStage) + (warp - 2) * kStep * kPitch;
         for (uint32_t n_seg = 0; plan.cluster == 1 && walk.next(seg); ++n_seg) {
             const uint32_t b = n_seg & 1;
-            const int t0 = seg.tile % plan.tiles_m * BT, n0 = seg.tile / plan.tiles_m * kBN;
+            const int t0 = seg.tile % plan.tiles_m * BT, n0 = seg.tile / plan.tiles_m * kTileN + half * kBN;
             const bool cut = !plan.whole && (seg.k0 > 0 || seg.k1 < plan.nk);
             const int nt = min(BT, a.M - t0);
             const uint32_t acc = tmem + tmem_lane_base(q) + b * BT;
@@ -435,11 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[b]);
+            if (lane == 0) {
+                if (half == 0) mbar_arrive(&acc_empty[b]);
+                else mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[b]), 0));
+            }
             first_seg = false;
         }
     }
-    if (plan.cluster > 1) {
+    if (!kPair && plan.cluster > 1) {
         // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
         // have, takes the parts of the tokens this CTA finishes, one slot a rank.
         const int rank = blockIdx.x % plan.cluster, share = BT / plan.cluster;
@@ -491,9 +563,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // neither CTA's memory is used by the other any more
     if (warp == 1) {
         tc_fence_after();
-        tmem_free<L::kTmemCols>(tmem);
+        if (kPair) tmem_free_pair<L::kTmemCols>(tmem);
+        else tmem_free<L::kTmemCols>(tmem);
     }
 }
 
@@ -542,20 +616,20 @@ __global__ void __launch_bounds__(32 * kJoinTokens) linear_join(LinearArgs a, Pl
         make_uint2(pack_bf16x2(y[0] + res[0], y[1] + res[1]), pack_bf16x2(y[2] + res[2], y[3] + res[3]));
 }
 
-template <int BT>
+template <int BT, bool kPair = false>
 cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
     CUtensorMap tm_w, tm_x;
     const uint64_t wd[2] = {(uint64_t)a.N, (uint64_t)a.K}, ws[1] = {(uint64_t)a.N * 2};
     const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.M}, xs[1] = {(uint64_t)a.x_stride * 2};
-    const uint32_t wb[2] = {64, kBK}, xb[2] = {kBK, BT};
+    const uint32_t wb[2] = {64, kBK}, xb[2] = {kBK, kPair ? BT / 2 : BT};
     if (!encode_bf16_sw128(&tm_w, a.w, 2, wd, ws, wb) || !encode_bf16_sw128(&tm_x, a.x, 2, xd, xs, xb))
         return cudaErrorInvalidValue;
-    const int smem = Smem<BT>::kBytes;
+    const int smem = Smem<BT, kPair>::kBytes;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     static std::atomic<unsigned long long> ready{0};  // devices the kernel's shared memory is allowed on
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_tc<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(linear_tc<BT, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
@@ -566,11 +640,11 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.x = kPair ? 2 : p.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, linear_tc<BT>, tm_w, tm_x, a, p);
+    cfg.numAttrs = kPair || p.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_tc<BT, kPair>, tm_w, tm_x, a, p);
 }
 
 }  // namespace
@@ -588,7 +662,7 @@ cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st) {
         case 32: e = launch_bt<32>(a, p, st); break;
         case 64: e = launch_bt<64>(a, p, st); break;
         case 128: e = launch_bt<128>(a, p, st); break;
-        default: e = launch_bt<256>(a, p, st); break;
+        default: e = p.pair ? launch_bt<256, true>(a, p, st) : launch_bt<256>(a, p, st); break;
     }
     if (e != cudaSuccess || p.whole) return e;
     cudaLaunchConfig_t cfg = {};

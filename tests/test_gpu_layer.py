@@ -467,6 +467,10 @@ LINEAR_CASES = [
     (256, 128, 4096, False, "none", False, 0, 0, 0), (333, 1000, 1544, True, "gelu_tanh", True, 8, 8, 8),
     (1025, 72, 520, True, "silu", True, 0, 24, 0), (4096, 512, 2048, False, "none", True, 0, 0, 0),
     (5000, 136, 1160, True, "gelu", True, 0, 0, 0),
+    # pairs of CTAs: several rounds of tiles, the last ones cut by every edge; one round
+    (5000, 1032, 6000, True, "silu", True, 8, 8, 8), (700, 2056, 6024, False, "none", True, 0, 0, 0),
+    # whole tiles over a little more than a wave, cut into runs
+    (8, 1000, 20480, True, "relu", True, 0, 8, 0), (150, 2048, 19464, False, "none", True, 0, 0, 0),
 ]
 
 
