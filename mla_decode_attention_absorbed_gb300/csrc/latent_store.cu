@@ -2,8 +2,11 @@
 // rotation of the key, one rounding to the cache's format, written to the slots.
 //
 // One warp a token: a lane holds two 16-byte chunks of the latent (d_c <= 512) and
-// one pair of the key (d_rope <= 64), so the row is read once, the mean square is
-// one warp reduction, and nothing goes through shared memory.
+// two neighbouring values of the key (d_rope <= 64), so the row is read once, the mean
+// square is one warp reduction, and nothing goes through shared memory.  In the half
+// layout the two values belong to two pairs: lanes l and l + 16 hold values 2l, 2l + 1 of
+// the first and of the second half, trade one each, turn a pair each, and trade back.
+// A warp takes several tokens and has the next one's row under way.
 #include "layer.h"
 #include "rope.cuh"
 #include "sm100.cuh"
@@ -12,7 +15,7 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 4;  // warps a CTA
-constexpr int kCtasPerSm = 8;
+constexpr int kCtasPerSm = 7;  // as many as its registers allow: 15.9 us for 32768 rows of 576, 19.7 with 8
 
 // Two values as E4M3 codes (v0 in the low byte): nearest even, saturating at +-448.
 __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
@@ -24,26 +27,61 @@ __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
 // What a warp reads of one token before it can compute: the row, and where it goes.
 struct Row {
     uint4 c[2];   // 16-byte chunks lane and lane + 32 of the latent
-    uint32_t k;   // the lane's pair of the key, bf16 x 2
+    uint32_t k;   // the lane's two values of the key, bf16 x 2
     int slot;     // slots, else the sequence's length (which pos may need, too)
     int pos, len;
 };
+
+// The key's values at, at + 1 that a lane holds, and the pair it turns.
+template <bool kHalf>
+struct KeyLane {
+    int at, pair;
+    bool active;
+    __device__ __forceinline__ KeyLane(int lane, int pairs) {
+        const int l = lane & 15, upper = lane >> 4;
+        at = kHalf ? upper * pairs + 2 * l : 2 * lane;
+        pair = kHalf ? 2 * l + upper : lane;
+        active = kHalf ? 2 * l < pairs : lane < pairs;
+    }
+    // the lane's two values <-> the pair it turns
+    static __device__ __forceinline__ float2 trade(float2 k, int lane) {
+        if (!kHalf) return k;
+        const bool upper = lane & 16;
+        const float got = __shfl_xor_sync(~0u, upper ? k.x : k.y, 16);
+        return upper ? make_float2(got, k.y) : make_float2(k.x, got);
+    }
+};
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<unsigned long long *>(&c)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
 
 template <bool kHalf>
 __device__ __forceinline__ Row load_row(const StoreArgs &a, int t, int lane) {
     Row r;
     const __nv_bfloat16 *src = a.x + t * a.token_stride;
-    const int nc = a.d_c / 8, nf = a.d_rope / 2;
+    const int nc = a.d_c / 8;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         r.c[i] = make_uint4(0, 0, 0, 0);
         if (lane + 32 * i < nc) r.c[i] = *(reinterpret_cast<const uint4 *>(src) + lane + 32 * i);
     }
     r.k = 0;
-    if (lane < nf) {
-        const unsigned short *k = reinterpret_cast<const unsigned short *>(src + a.d_c);
-        r.k = kHalf ? k[lane] | (uint32_t)k[lane + nf] << 16 : *reinterpret_cast<const uint32_t *>(k + 2 * lane);
-    }
+    const KeyLane<kHalf> key(lane, a.d_rope / 2);
+    if (key.active) r.k = *reinterpret_cast<const uint32_t *>(src + a.d_c + key.at);
     const bool by_lens = !a.slots || (a.rotate && !a.positions);
     r.len = by_lens ? __ldg(a.cache.seq_lens + (a.s_q == 1 ? t : t / a.s_q)) : 0;
     r.slot = a.slots ? __ldg(a.slots + t) : 0;
@@ -91,25 +129,27 @@ __device__ __forceinline__ float2 unpack(uint32_t v) {
 template <bool kFp8, bool kHalf>
 __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant__ StoreArgs a) {
     const int lane = threadIdx.x % 32, nw = gridDim.x * kWarps;
-    const int nc = a.d_c / 8, nf = a.d_rope / 2;
+    const int nc = a.d_c / 8;
+    const KeyLane<kHalf> key(lane, a.d_rope / 2);
     int t = blockIdx.x * kWarps + threadIdx.x / 32;
     if (t >= a.tokens) return;
     Row row = load_row<kHalf>(a, t, lane);
-    float wt[2][8];
+    // what a value is multiplied by besides 1 / rms: its weight, and 1 / kv_scale
+    const float unit = kFp8 ? 1.f / a.cache.kv_scale : 1.f;
+    float2 wt[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
+        uint4 v = make_uint4(0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80);  // ones
         if (a.weight && lane + 32 * i < nc) v = __ldg(reinterpret_cast<const uint4 *>(a.weight) + lane + 32 * i);
         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 p = unpack(w4[e]);
-            wt[i][2 * e] = p.x;
-            wt[i][2 * e + 1] = p.y;
+            wt[i][e] = make_float2(unit * p.x, unit * p.y);
         }
     }
     const float part = 1.f / (float)a.d_c;
-    const unsigned long long turn = a.rotate && lane < nf ? a.plan.turn[lane] : 0;
+    const unsigned long long turn = a.rotate && key.active ? a.plan.turn[key.pair] : 0;
     while (true) {
         const int next = t + nw;
         const bool more = next < a.tokens;
@@ -117,50 +157,45 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
         if (more) row = load_row<kHalf>(a, next, lane);  // on its way while this row is computed
         const long long at = row_offset(a, r, t, lane);
         if (at >= 0) {
-            float f[2][8], sum = 0.f;
+            float2 f[2][4], sum2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t w4[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 p = unpack(w4[e]);
-                    f[i][2 * e] = p.x;
-                    f[i][2 * e + 1] = p.y;
-                    sum = fmaf(p.x, p.x, fmaf(p.y, p.y, sum));
+                    f[i][e] = unpack(w4[e]);
+                    sum2 = fma2(f[i][e], f[i][e], sum2);
                 }
             }
+            float2 inv = make_float2(1.f, 1.f);
             if (a.weight) {
+                float sum = sum2.x + sum2.y;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-                const float inv = rsqrtf(fmaf(sum, part, a.eps));
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[i][e] *= inv * wt[i][e];
+                inv.x = inv.y = rsqrtf(fmaf(sum, part, a.eps));
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[i][e] = mul2(f[i][e], mul2(inv, wt[i][e]));
             float2 k = unpack(r.k);
-            if (a.rotate) k = rope_turn(k.x, k.y, rope_cos_sin(turn, r.pos, a.plan.mscale, 1.f));
+            if (a.rotate) {
+                k = key.trade(k, lane);
+                k = rope_turn(k.x, k.y, rope_cos_sin(turn, r.pos, a.plan.mscale, 1.f));
+                k = key.trade(k, lane);
+            }
             if (kFp8) {
                 uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
-                const float s = a.cache.kv_scale;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int c = lane + 32 * i;
                     if (c < nc)
                         *(reinterpret_cast<uint2 *>(dst) + c) =
-                            make_uint2(e4m3x2(f[i][0] / s, f[i][1] / s) | e4m3x2(f[i][2] / s, f[i][3] / s) << 16,
-                                       e4m3x2(f[i][4] / s, f[i][5] / s) | e4m3x2(f[i][6] / s, f[i][7] / s) << 16);
+                            make_uint2(e4m3x2(f[i][0].x, f[i][0].y) | e4m3x2(f[i][1].x, f[i][1].y) << 16,
+                                       e4m3x2(f[i][2].x, f[i][2].y) | e4m3x2(f[i][3].x, f[i][3].y) << 16);
                 }
-                if (lane < nf) {
-                    const uint32_t code = e4m3x2(k.x / s, k.y / s);
-                    dst += a.d_c;
-                    if (kHalf) {
-                        dst[lane] = (uint8_t)code;
-                        dst[lane + nf] = (uint8_t)(code >> 8);
-                    } else {
-                        *reinterpret_cast<unsigned short *>(dst + 2 * lane) = (unsigned short)code;
-                    }
-                }
+                if (key.active)
+                    *reinterpret_cast<unsigned short *>(dst + a.d_c + key.at) = (unsigned short)e4m3x2(unit * k.x, unit * k.y);
             } else {
                 __nv_bfloat16 *dst = const_cast<__nv_bfloat16 *>(static_cast<const __nv_bfloat16 *>(a.cache.kv)) + at;
 #pragma unroll
@@ -168,18 +203,10 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
                     const int c = lane + 32 * i;
                     if (c < nc)
                         *(reinterpret_cast<uint4 *>(dst) + c) =
-                            make_uint4(sm100::pack_bf16x2(f[i][0], f[i][1]), sm100::pack_bf16x2(f[i][2], f[i][3]),
-                                       sm100::pack_bf16x2(f[i][4], f[i][5]), sm100::pack_bf16x2(f[i][6], f[i][7]));
+                            make_uint4(sm100::pack_bf16x2(f[i][0].x, f[i][0].y), sm100::pack_bf16x2(f[i][1].x, f[i][1].y),
+                                       sm100::pack_bf16x2(f[i][2].x, f[i][2].y), sm100::pack_bf16x2(f[i][3].x, f[i][3].y));
                 }
-                if (lane < nf) {
-                    dst += a.d_c;
-                    if (kHalf) {
-                        dst[lane] = __float2bfloat16_rn(k.x);
-                        dst[lane + nf] = __float2bfloat16_rn(k.y);
-                    } else {
-                        *reinterpret_cast<uint32_t *>(dst + 2 * lane) = sm100::pack_bf16x2(k.x, k.y);
-                    }
-                }
+                if (key.active) *reinterpret_cast<uint32_t *>(dst + a.d_c + key.at) = sm100::pack_bf16x2(k.x, k.y);
             }
         }
         if (!more) return;
