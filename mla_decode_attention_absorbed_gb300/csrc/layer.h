@@ -42,7 +42,8 @@ struct PagesArgs {
     int *state_out;
     const int *old_lens, *new_lens;
     int *seq_lens, *token_start, *positions, *slots, *status;
-    float inv_units;  // 1 / (page_size / 64)
+    unsigned div_magic;  // division by page_size / 64, see pages.cu
+    int div_shift;
 };
 cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t st);
 

@@ -209,7 +209,10 @@ MLA_API int mla_pages_update(const mla_page_pool *pool, const int *old_lens, con
         return MLA_ERR_UNSUPPORTED;
     mla::PagesArgs a{pool->B, pool->page_size, pool->max_pages, pool->num_pages, max_tokens, pool->block_table,
                      pool->free_ring, pool->state, pool->state_out, old_lens, new_lens, seq_lens, token_start,
-                     positions, slots, status, 64.f / (float)pool->page_size};
+                     positions, slots, status, 0, 25};
+    const unsigned long long units = (unsigned)pool->page_size / 64;
+    while ((1ull << (a.div_shift - 25)) < units) ++a.div_shift;
+    a.div_magic = (unsigned)(((1ull << a.div_shift) + units - 1) / units);
     return result(mla::launch_pages_update(a, as_stream(stream)));
 }
 

@@ -31,32 +31,45 @@ struct Request {
     Sums n;  // its own tokens, pages taken, pages given back
 };
 
-__device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
+// m / units for the pool's page size of 64 units tokens, m < 2^25: with l the bits of
+// units - 1, ceil(2^(25 + l) / units) is off by less than 1, that is by less than 2^-25 of a
+// quotient's step, so the product's integer part is the quotient.
+__device__ __forceinline__ int div_units(const PagesArgs &a, int m) {
+    return (int)((unsigned long long)(unsigned)m * a.div_magic >> a.div_shift);
+}
+
+__device__ __forceinline__ Request make_request(const PagesArgs &a, int old_len, int new_len) {
     Request r;
-    r.old_len = __ldg(a.old_lens + b);
-    r.new_len = __ldg(a.new_lens + b);
+    r.old_len = old_len;
+    r.new_len = new_len;
     const int most = a.max_pages * a.page_size;  // at most 2^30
-    // pages of n tokens: n / 64 is exact in fp32 up to 2^24, its quotient by the page's
-    // 64-token units within one of the fp32 product, which the remainder puts right
-    const int units = a.page_size >> 6;
-    const float inv = a.inv_units;
-    auto pages = [&](int n) {
-        const int m = (n + 63) >> 6;
-        int q = (int)((float)m * inv);
-        const int rest = m - q * units;
-        if (rest < 0) --q;
-        if (rest >= units) ++q;
-        return q * units < m ? q + 1 : q;
-    };
     r.valid = r.old_len >= 0 && r.new_len >= 0 && r.old_len <= most && r.new_len <= most;
     r.had = r.has = 0;
     r.n = Sums{0, 0, 0};
     if (r.valid) {
-        r.had = pages(r.old_len);
-        r.has = pages(r.new_len);
+        r.had = div_units(a, ((r.old_len + 63) >> 6) + (a.page_size >> 6) - 1);
+        r.has = div_units(a, ((r.new_len + 63) >> 6) + (a.page_size >> 6) - 1);
         r.n = Sums{max(r.new_len - r.old_len, 0), max(r.has - r.had, 0), max(r.had - r.has, 0)};
     }
     return r;
+}
+
+__device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
+    return make_request(a, __ldg(a.old_lens + b), __ldg(a.new_lens + b));
+}
+
+// f(b, request) of requests [b0, b1), four at a time where the lengths allow it.
+template <class F>
+__device__ __forceinline__ void each_request(const PagesArgs &a, int b0, int b1, bool aligned, F f) {
+    int b = b0;
+    for (; aligned && b + 4 <= b1; b += 4) {
+        const int4 o = __ldg(reinterpret_cast<const int4 *>(a.old_lens + b)), n = __ldg(reinterpret_cast<const int4 *>(a.new_lens + b));
+        f(b, make_request(a, o.x, n.x));
+        f(b + 1, make_request(a, o.y, n.y));
+        f(b + 2, make_request(a, o.z, n.z));
+        f(b + 3, make_request(a, o.w, n.w));
+    }
+    for (; b < b1; ++b) f(b, load_request(a, b));
 }
 
 struct Ring {
@@ -129,7 +142,7 @@ struct TokenRun {
         pos = slot = -1;
         if (!served(a, ring, r, add(before, r.n))) return;
         pos = r.old_len + (k - before.tokens);
-        const int col = pos / a.page_size, row = pos - col * a.page_size;
+        const int col = div_units(a, pos >> 6), row = pos - col * a.page_size;
         end = min(end, k + a.page_size - row);
         const int page = col < r.had ? a.table[(long long)b * a.max_pages + col]
                                      : __ldg(a.ring + ring_at(a, ring.head, before.taken + col - r.had));
@@ -138,7 +151,7 @@ struct TokenRun {
     }
 };
 
-__global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ PagesArgs a, int per) {
+__global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ PagesArgs a, int per, int lane_tokens) {
     __shared__ Sums first[kGroups];
     __shared__ Sums warp_sums[32];
     __shared__ Sums total_s;
@@ -149,7 +162,9 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
 
     // sums before every group
     Sums mine{0, 0, 0};
-    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine = add(mine, load_request(a, b).n);
+    const bool aligned = per % 4 == 0 && (((uintptr_t)a.old_lens | (uintptr_t)a.new_lens) & 15) == 0;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    each_request(a, b0, b1, aligned, [&](int, const Request &r) { mine = add(mine, r.n); });
     Sums run = mine;
     for (int o = 1; o < 32; o <<= 1) {
         Sums up{__shfl_up_sync(~0u, run.tokens, o), __shfl_up_sync(~0u, run.taken, o), __shfl_up_sync(~0u, run.given, o)};
@@ -168,6 +183,9 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
         if (lane == 31) total_s = w;
     }
     __syncthreads();
+    const Sums total = total_s;
+    // room for everybody: every valid request is served
+    const bool plenty = ring.ok && total.taken <= ring.count && total.tokens <= a.max_tokens;
     {
         // sums before this thread's group: before its warp, and before it within the warp
         Sums before = warp > 0 ? warp_sums[warp - 1] : Sums{0, 0, 0};
@@ -177,8 +195,7 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
         // the group's requests: lengths, starts, and what the whole batch takes
         const bool writes = tid % (int)gridDim.x == (int)blockIdx.x;
         int most = 0;
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-            const Request r = load_request(a, b);
+        if (writes || !plenty) each_request(a, b0, b1, aligned, [&](int b, const Request &r) {
             const Sums end = add(before, r.n);
             const bool fits = served(a, ring, r, end);
             if (fits && r.n.taken > 0) most = end.taken;
@@ -191,12 +208,11 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
                                                                                                  : MLA_ERR_SHAPE);
             }
             before = end;
-        }
+        });
         if (most > 0) atomicMax(&taken_s, most);
     }
     __syncthreads();
-    const Sums total = total_s;
-    const int taken = taken_s;  // served takers are the first ones: their sums do not exceed the ring's count
+    const int taken = plenty ? total.taken : taken_s;  // served takers are the first ones: their sums do not exceed the ring's count
     // pages given back that the ring has room for (all of them, in a consistent pool)
     const int given = ring.ok ? min(total.given, a.num_pages - ring.count) : 0;
     const int gsize = gridDim.x * blockDim.x, gid = blockIdx.x * blockDim.x + tid;
@@ -229,38 +245,40 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
         a.ring[ring_at(a, tail, k)] = a.table[(long long)b * a.max_pages + r.has + (k - before.given)];
     }
 
-    // Tokens, four neighbours a lane.  A lane keeps the run it is in: neighbouring tokens of
-    // one request in one page, whose positions and slots count up from the run's first.
+    // Tokens, `lane_tokens` neighbours a lane.  A lane keeps the run it is in: neighbouring tokens
+    // of one request in one page, whose positions and slots count up from the run's first.
     TokenRun run_of;
     run_of.b = -1;
     // A warp has a contiguous run of chunks, so that it walks on where it is.
     const int warps = gsize / 32;
     int w = gid / 32 + warps / 3;
     if (w >= warps) w -= warps;
-    const long long chunks = ((long long)a.max_tokens + 127) / 128;
+    const long long chunks = ((long long)a.max_tokens + 32 * lane_tokens - 1) / (32 * lane_tokens);
     const long long c1 = chunks * (w + 1) / warps;
-    const bool wide = (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15) == 0;
+    const bool wide = lane_tokens == 4 && (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15) == 0;
     for (long long c = chunks * w / warps; c < c1; ++c) {
-        const long long k0 = c * 128 + lane * 4;
-        int pos[4], slot[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int k = (int)k0 + e;
-            pos[e] = slot[e] = -1;
-            if (k >= total.tokens || k >= a.max_tokens) continue;
-            if (run_of.b < 0 || k >= run_of.end) run_of.locate(a, ring, first, groups, per, k);
-            if (run_of.pos >= 0) {
-                pos[e] = run_of.pos + (k - run_of.begin);
-                if (run_of.slot >= 0) slot[e] = run_of.slot + (k - run_of.begin);
+        const long long k0 = (c * 32 + lane) * lane_tokens, k1 = min(k0 + lane_tokens, (long long)a.max_tokens);
+#pragma unroll 1
+        for (int k = (int)k0, n; k < k1; k += n) {
+            if (k >= total.tokens) {
+                run_of = TokenRun{-1, k, kBig, -1, -1};
+            } else if (run_of.b < 0 || k >= run_of.end) {
+                run_of.locate(a, ring, first, groups, per, k);
             }
-        }
-        if (wide && k0 + 4 <= a.max_tokens) {
-            *reinterpret_cast<int4 *>(a.positions + k0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            *reinterpret_cast<int4 *>(a.slots + k0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-        } else {
-            for (int e = 0; e < 4 && k0 + e < a.max_tokens; ++e) {
-                a.positions[k0 + e] = pos[e];
-                a.slots[k0 + e] = slot[e];
+            n = min((int)k1, run_of.end) - k;
+            int pos = run_of.pos, slot = run_of.slot;
+            const int dp = pos >= 0 ? 1 : 0, ds = slot >= 0 ? 1 : 0;  // -1 stays
+            pos += dp * (k - run_of.begin);
+            slot += ds * (k - run_of.begin);
+            if (n == 4 && wide) {
+                *reinterpret_cast<int4 *>(a.positions + k) = make_int4(pos, pos + dp, pos + 2 * dp, pos + 3 * dp);
+                *reinterpret_cast<int4 *>(a.slots + k) = make_int4(slot, slot + ds, slot + 2 * ds, slot + 3 * ds);
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < n; ++e) {
+                    a.positions[k + e] = pos + e * dp;
+                    a.slots[k + e] = slot + e * ds;
+                }
             }
         }
     }
@@ -269,16 +287,19 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
 }  // namespace
 
 cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t st) {
-    const int per = a.B > 0 ? (a.B + kGroups - 1) / kGroups : 1;
+    // requests a group: one, or fours (loaded as 16 bytes)
+    const int per = a.B <= kGroups ? 1 : (a.B + 4 * kGroups - 1) / (4 * kGroups) * 4;
     const int groups = (a.B + per - 1) / per;
-    // enough threads for the groups' sums, and CTAs for the tokens (three at least: see the
-    // items' order)
+    // Enough threads for the groups' sums.  Few tokens: one a thread, on at least 12 CTAs, so
+    // that the items' loads run side by side (512 requests, 1,300 tokens: 10.8 us on one CTA,
+    // 8.4 on 3, 7.4 on 12).  Many: four a lane, stored as 16 bytes.
     int threads = groups > 0 ? (groups + 31) / 32 * 32 : 32;
     if (threads < 256 && a.max_tokens > threads) threads = 256;
-    const long long want = ((long long)a.max_tokens + 4 * threads - 1) / (4 * threads);
     const int sms = layer_num_sms();
-    const int grid = want < 3 ? 3 : want > sms ? sms : (int)want;
-    pages_update<<<grid, threads, 0, st>>>(a, per);
+    const int lane_tokens = a.max_tokens > sms * threads ? 4 : 1;
+    const long long want = ((long long)a.max_tokens + lane_tokens * threads - 1) / (lane_tokens * threads);
+    const int grid = want < 12 ? 12 : want > sms ? sms : (int)want;
+    pages_update<<<grid, threads, 0, st>>>(a, per, lane_tokens);
     return cudaGetLastError();
 }
 

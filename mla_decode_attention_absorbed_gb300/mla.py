@@ -545,7 +545,7 @@ class Pages:
         return cls(table, ring, page_size), torch.tensor([0, num_pages], dtype=torch.int32, device=device)
 
 
-@dataclass
+@dataclass(slots=True)
 class PagesStep:
     """What one ``pages_update`` gives: the batch's lengths, the ring's state, and for the new
     tokens where each request's begin, their positions and their slots."""
@@ -569,14 +569,23 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
     new = _dense(new_lens, "new_lens", torch.int32, dev, (B,))
     word = None if status is None else _dense(status, "status", torch.int32, dev)
     if out is None:
-        out = PagesStep(*(_empty_strided_cuda((n,), (1,), torch.int32) for n in (B, 2, B + 1, max_tokens, max_tokens)))
-        at = [t.data_ptr() for t in (out.seq_lens, out.ring_state, out.token_start, out.positions, out.slots)]
+        i32, one = torch.int32, (1,)
+        lens = _empty_strided_cuda((B,), one, i32)
+        state_out = _empty_strided_cuda((2,), one, i32)
+        start = _empty_strided_cuda((B + 1,), one, i32)
+        pos = _empty_strided_cuda((max_tokens,), one, i32)
+        slot = _empty_strided_cuda((max_tokens,), one, i32)
+        out = PagesStep(lens, state_out, start, pos, slot)
+        lens, state_out, start = lens.data_ptr(), state_out.data_ptr(), start.data_ptr()
+        pos, slot = pos.data_ptr(), slot.data_ptr()
     else:
-        at = [_dense(t, what, torch.int32, dev, (n,)) for t, n, what in (
-            (out.seq_lens, B, "seq_lens"), (out.ring_state, 2, "ring_state"), (out.token_start, B + 1, "token_start"),
-            (out.positions, max_tokens, "positions"), (out.slots, max_tokens, "slots"))]
-    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], table.data_ptr(), ring.data_ptr(), state, at[1])
-    _check(lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, at[0], at[2], at[3], at[4], word,
+        lens = _dense(out.seq_lens, "seq_lens", torch.int32, dev, (B,))
+        state_out = _dense(out.ring_state, "ring_state", torch.int32, dev, (2,))
+        start = _dense(out.token_start, "token_start", torch.int32, dev, (B + 1,))
+        pos = _dense(out.positions, "positions", torch.int32, dev, (max_tokens,))
+        slot = _dense(out.slots, "slots", torch.int32, dev, (max_tokens,))
+    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], table.data_ptr(), ring.data_ptr(), state, state_out)
+    _check(lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, lens, start, pos, slot, word,
                                 _raw_stream(dev, stream)), "mla_pages_update")
     return out
 
