@@ -512,8 +512,9 @@ MLA_API int mla_pages_update(const mla_page_pool *pool, const int *old_lens, con
  * [c | k] (d_c + d_rope values a token, row t at x + t*token_stride, t = b*s_q + i):
  *   c' = c / sqrt(mean(c^2) + eps) * norm_weight     (norm_weight NULL: c' = c)
  *   k' = k rotated by the token's position           (plan NULL: k' = k)
- * computed in fp32 and rounded once, to bf16 or to the E4M3 code of value /
- * kv_scale (nearest even, saturated to +-448; NaN stays NaN).  norm_weight bf16 [d_c].
+ * computed in fp32 and rounded once, to bf16 or to the E4M3 code of value times
+ * 1 / kv_scale in fp32 (nearest even, saturated to +-448; NaN stays NaN; kv_scale
+ * not below 2^-126, else MLA_ERR_UNSUPPORTED).  norm_weight bf16 [d_c].
  * Token t goes to row slots[t] of a paged pool (int32 [B][s_q], as
  * mla_pages_update gives them; a negative slot is skipped); slots NULL: to row
  * seq_lens[b] - s_q + i of sequence b, as mla_cache_append.  Two tokens of one call
@@ -553,8 +554,10 @@ MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *desc);
  *   out[m, n] = residual[m, n] + act(sum_k x[m, k] W[k, n] + bias[n])
  * fp32 accumulation and epilogue, one rounding to bf16.  x [M][K], w [K][N] dense,
  * bias [N] or NULL, residual [M][N] or NULL, out [M][N], all bf16.  out may be
- * residual itself.  Results do not depend on the timing of the GPU.  A bounded
- * device wait that runs out leaves NaN in the outputs it concerns. */
+ * residual itself (with its stride).  A workspace serves one call at a time: calls
+ * that may overlap on the GPU need one each.  Results do not depend on the timing
+ * of the GPU.  A bounded device wait that runs out leaves NaN in the outputs it
+ * concerns. */
 MLA_API int mla_linear(const mla_linear_desc *desc, const void *x, const void *w, const void *bias,
                        const void *residual, void *out, void *workspace, size_t ws_bytes, void *stream);
 

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[i][e] = mul2(f[i][e], mul2(inv, wt[i][e]));
+                for (int e = 0; e < 4; ++e) f[i][e] = mul2(mul2(f[i][e], inv), wt[i][e]);
             float2 k = unpack(r.k);
             if (a.rotate) {
                 k = key.trade(k, lane);

@@ -58,6 +58,7 @@ int check_store_cache(const mla_dims *d, const mla_cache *c) {
     if (c->kv_dtype != MLA_KV_BF16 && c->kv_dtype != MLA_KV_E4M3) return MLA_ERR_UNSUPPORTED;
     if (c->kv_dtype == MLA_KV_E4M3) {
         if (!(c->kv_scale > 0.f) || c->kv_scale > 3.0e38f) return MLA_ERR_SHAPE;
+        if (c->kv_scale < 1.1754944e-38f) return MLA_ERR_UNSUPPORTED;  // 1 / kv_scale has to be finite
         if (W % 16 || (!c->block_table && c->seq_stride % 16)) return MLA_ERR_ALIGN;
     }
     if (c->block_table) {
@@ -174,6 +175,11 @@ MLA_API int mla_rope(const mla_dims *dims, const mla_rope_plan *plan, const void
     if (!aligned(x, 16) || !aligned(rope_out, 16) || !aligned(pass_out, 16) || !aligned(positions, 4) ||
         !aligned(seq_lens, 4))
         return MLA_ERR_ALIGN;
+    // x may be turned in place where every value is written by the thread that read it
+    if (pass_out == x || pass_out == rope_out) return MLA_ERR_UNSUPPORTED;
+    if (rope_out == x && (pass_out || (dims->H > 1 && head_stride != width) ||
+                          ((long long)dims->B * dims->s_q > 1 && token_stride != dims->H * width)))
+        return MLA_ERR_UNSUPPORTED;
     mla::RopeArgs a;
     a.x = (const __nv_bfloat16 *)x;
     a.token_stride = token_stride;
@@ -284,6 +290,8 @@ MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, c
     if (!x || !w || !out) return MLA_ERR_NULL;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16))
         return MLA_ERR_ALIGN;
+    if (out == x || out == w || (out == residual && d->M > 1 && d->out_stride != d->residual_stride))
+        return MLA_ERR_UNSUPPORTED;
     mla::LinearArgs a;
     a.M = d->M;
     a.K = d->K;

@@ -62,9 +62,14 @@ __host__ __device__ __forceinline__ long long run_start(const Plan &p, int g) {
 //                       the weights for all CTAs at work, at 3500 bytes a cycle
 //   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
 //   a cluster's exchange  about 2000 cycles
-//   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back
+//   a chunk of a pair's tile  530 cycles
+//   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back at half
+//                       the card's rate
 // E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
-// tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters.
+// tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters;
+// 4096 x 7168 x 576: 40.9 us in pairs, 49.9 in runs; 4096 x 16384 x 7168: 510 us in pairs,
+// 587 in whole tiles of 128 x 256.  Over 23 shapes from 1 x 7168 x 576 up the choice was
+// within 6 % of the best plan timed, but for two below 8 us (11 %).
 Plan make_plan(int M, int K, int N, int sms) {
     Plan best{};
     double best_cost = 0.0;
@@ -121,7 +126,7 @@ Plan make_plan(int M, int K, int N, int sms) {
         if (tiles % p.grid == 0 || tiles >= 2 * sms) continue;
         p.whole = false;
         keep((double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk(p.grid) + epilogue + 6000.0 +
-             2.0 * (p.grid < tiles ? 2.0 * p.grid : p.grid + tiles) * kBN * bt * 4 / 3500.0);
+             4.0 * (p.grid < tiles ? 2.0 * p.grid : p.grid + tiles) * kBN * bt * 4 / 3500.0);
     }
     return best;
 }

@@ -31,7 +31,8 @@ __global__ void __launch_bounds__(kThreads)
     const int nf = a.d_rope / 2;
     auto position = [&](int t) {
         if (a.positions) return __ldg(a.positions + t);
-        return __ldg(a.seq_lens + t / a.s_q) - a.s_q + t % a.s_q;
+        const long long p = (long long)__ldg(a.seq_lens + t / a.s_q) - a.s_q + t % a.s_q;
+        return p < 0 ? -1 : (int)p;
     };
     for (int i = threadIdx.x; i < nt * nf; i += kThreads) {
         const int t = i / nf, f = i - t * nf;

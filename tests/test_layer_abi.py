@@ -68,7 +68,8 @@ def test_rope_refusals(lib):
     p = ctypes.byref(plan)
     W = 192
 
-    def call(d=None, plan=p, x=A, ts=16 * W, hs=W, pos=A, lens=NUL, q_nope=A, q_rope=A):
+    def call(d=None, plan=p, x=A, ts=16 * W, hs=W, pos=A, lens=NUL, q_nope=ctypes.c_void_p(0x60000),
+             q_rope=ctypes.c_void_p(0x70000)):
         d = dims() if d is None else d
         return lib.mla_rope(ctypes.byref(d), plan, x, ts, hs, pos, lens, q_nope, q_rope, 0, NUL)
 
@@ -82,6 +83,10 @@ def test_rope_refusals(lib):
     assert call(d=dims(d_nope=24)) == 6 and call(d=dims(d_nope=272)) == 6 and call(d=dims(B=65536)) == 6
     assert call(d=dims(B=65535, s_q=129)) == 6 and call(d=dims(B=-1)) == 2 and call(d=dims(s_q=0)) == 2
     assert call(d=dims(B=0), x=NUL) == 0  # nothing to do
+    B_ = ctypes.c_void_p(0x50000)
+    for over in (dict(x=A, q_nope=A, q_rope=B_), dict(x=B_, q_nope=A, q_rope=A), dict(x=A, q_nope=B_, q_rope=A),
+                 dict(x=A, q_nope=NUL, q_rope=A)):  # in place only where x is dense rows of d_rope
+        assert call(**over) == 6, over
     broken = mla.rope_plan(64)
     broken.d_rope = 80
     assert call(plan=ctypes.byref(broken)) == 6
@@ -145,6 +150,7 @@ def test_store_refusals(lib):
     assert call(d=dims(d_rope=80), plan=None) == 6 and call(d=dims(B=65536)) == 6
     assert call(c=cache(paged=False)) == 6  # slots are rows of a pool
     assert call(c=cache(page_size=32)) == 6 and call(c=cache(num_pages=1 << 25)) == 6 and call(c=cache(num_pages=0)) == 2
+    assert call(c=cache(fp8=True, scale=1e-39)) == 6
     assert call(c=cache(fp8=True, scale=0.0)) == 2 and call(c=cache(fp8=True, scale=float("nan"))) == 2
     bad = cache()
     bad.kv_dtype = 2
@@ -157,7 +163,7 @@ def test_linear_refusals(lib):
     def desc(M=4, K=64, N=128, act=0, xs=64, os=128, rs=128):
         return mla.LinearDesc(M, K, N, act, xs, os, rs)
 
-    def call(d=None, x=A, w=A, bias=NUL, residual=NUL, out=A, ws=A, nbytes=1 << 30):
+    def call(d=None, x=A, w=A, bias=NUL, residual=NUL, out=ctypes.c_void_p(0x60000), ws=A, nbytes=1 << 30):
         d = desc() if d is None else d
         return lib.mla_linear(ctypes.byref(d), x, w, bias, residual, out, ws, nbytes, NUL)
 
@@ -175,6 +181,9 @@ def test_linear_refusals(lib):
         assert call(desc(**bad)) == code, bad
         assert lib.mla_linear_workspace_size(ctypes.byref(desc(**bad))) == 0, bad
     assert call(desc(rs=120), residual=A) == 2 and call(desc(rs=132), residual=A) == 4
+    B_ = ctypes.c_void_p(0x50000)
+    assert call(x=A, w=B_, out=A) == 6 and call(x=B_, w=A, out=A) == 6  # out over an operand
+    assert call(desc(rs=136), x=B_, w=B_, residual=A, out=A) == 6  # residual in place, but with another stride
     need = lib.mla_linear_workspace_size(ctypes.byref(desc()))
     assert need > 0 and call(nbytes=need - 1) == 5
     assert call(desc(M=0), x=NUL) == 0  # nothing to do
