@@ -250,8 +250,8 @@ MLA_API size_t mla_cache_append_workspace_size(const mla_dims *dims, int d_model
  *   c[b,i,:] = sum_k x[b,i,k] * W_DKV[k,:]     (fp32 accumulate, bf16 in the cache)
  * and row L_b - s_q + i of sequence b (L_b = seq_lens[b], which already counts
  * the s_q new tokens) becomes [c[b,i,:] | k_rope[b,i,:]].  x [B][s_q][d_model],
- * w_dkv [d_model][d_c], k_rope [B][s_q][d_rope] (already rotated; the library
- * does no rotation).  The cache is described as for mla_decode_attn and its kv
+ * w_dkv [d_model][d_c], k_rope [B][s_q][d_rope] (already rotated: this call
+ * does no rotation, mla_rope and mla_latent_store do).  The cache is described as for mla_decode_attn and its kv
  * buffer is WRITTEN (it must be writable device memory); only the new rows
  * change.  An FP8 cache receives the E4M3 code of value / kv_scale, rounded to
  * nearest even and saturated to +-448, for every element of the row.  d_model must be a multiple of 8.  A length outside [s_q, capacity]
