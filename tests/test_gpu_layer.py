@@ -249,6 +249,31 @@ def test_pages_one_long_among_many():
     pages_check(table, ring, [11, len(ids) - n], old, new, 64, 210000, codes=set())
 
 
+@pytest.mark.parametrize("B,ps,max_pages,grow,short", [
+    (3, 64, 1100, 60000, -3), (3, 256, 300, 60000, 40), (2000, 192, 5, 400, -3), (2000, 64, 16, 400, 1500),
+    (4000, 64, 20, 129, -3), (900, 128, 40, 3000, 5000)])
+def test_pages_many_tokens(B, ps, max_pages, grow, short):
+    """Tokens by warps: long requests, short ones, both, some of them without pages; with room to spare, with too
+    little, and into arrays that start between two 16-byte boundaries."""
+    table, ring, state, old, new = pages_case(B, ps, max_pages, B + grow, grow, spare=-short)
+    if B == 4000:  # every other request grows by a token or not at all, in long stretches
+        new[500:2500] = torch.where(torch.arange(2000) % 3 == 0, old[500:2500] + 1, old[500:2500]).clamp(max=ps * max_pages)
+    n = int((new - old).clamp(min=0).sum())
+    assert n > 38912 * (4 if B > 992 else 1) * 0.5
+    room = max(n + 5, 152 * 1024 + 1)
+    codes = {layer.PAGE} if short > 0 else set()
+    out = pages_check(table, ring, state, old, new, ps, room, codes=codes)
+    if short < 0:
+        pages_check(table, ring, state, old, new, ps, n - 777 if n - 777 > 152 * 1024 else n, codes=None)
+    # into views that begin one element after an allocation
+    dev = lambda t: torch.as_tensor(t).to(I32).to(DEV)  # noqa: E731
+    buf = torch.full((2, room + 2), -9, dtype=I32, device=DEV)
+    views = mla.PagesStep(dev(old), dev(state), torch.empty(B + 1, dtype=I32, device=DEV), buf[0, 1:-1], buf[1, 1:-1])
+    mla.pages_update(mla.Pages(dev(table), dev(ring), ps), dev(state), dev(old), dev(new), room, out=views)
+    assert torch.equal(views.positions, out.positions) and torch.equal(views.slots, out.slots)
+    assert bool((buf[:, 0] == -9).all()) and bool((buf[:, -1] == -9).all())
+
+
 @pytest.mark.parametrize("B,short", [(2, 1), (40, 1), (40, 25), (3000, 700)])
 def test_pages_ring_runs_out(B, short):
     """Requests are served in order as long as pages last; those that need none always are."""
@@ -723,3 +748,103 @@ def test_calls_on_two_streams_at_once():
             assert torch.equal(got, alone[k])
         else:
             assert torch.equal(got.slots, alone[2].slots) and torch.equal(got.ring_state, alone[2].ring_state)
+
+
+# ------------------------------------------------------------------------------------- sizes at the ends of the ranges
+def test_offsets_past_32_bits():
+    """Rows whose element offsets pass 2^32: the last tokens of a rotation, the last slots of a pool, the last rows of a
+    product, each against the same call on those rows alone (whose results the other tests check)."""
+    torch.manual_seed(91)
+    # rotation: 100,000 tokens x 128 heads x 192 = 2.46e9 values in, as many out
+    T, H = 100000, 128
+    x = torch.empty(1, T, H, 192, dtype=BF16, device=DEV)
+    x[0, :3] = torch.randn(3, H, 192, device=DEV)
+    x[0, -3:] = torch.randn(3, H, 192, device=DEV)
+    plan = mla.rope_plan(64)
+    at = torch.arange(T, dtype=I32, device=DEV)
+    nope, turned = mla.rope(problem(1, H, T), plan, x, positions=at)
+    for rows in (slice(0, 3), slice(T - 3, T)):
+        n1, t1 = mla.rope(problem(1, H, 3), plan, x[:, rows], positions=at[rows].contiguous())
+        assert torch.equal(nope[:, rows], n1) and torch.equal(turned[:, rows], t1)
+    del x, nope, turned
+    # store: 150,000 pages of 64 rows of 576 values
+    pages, W = 150000, 576
+    kv = torch.empty(pages, 64, W, dtype=BF16, device=DEV)
+    kv[0].zero_()
+    kv[-2:].zero_()
+    rows = torch.randn(4, W, device=DEV).to(BF16)
+    slots = torch.tensor([pages * 64 - 1, 5, pages * 64 - 65, pages * 64 - 64], dtype=I32, device=DEV)
+    lens, table = torch.ones(4, dtype=I32, device=DEV), torch.zeros(4, 1, dtype=I32, device=DEV)
+    prob = problem(4, 16, 1)
+    kw = dict(plan=plan, positions=torch.arange(4, dtype=I32, device=DEV), norm_weight=torch.ones(512, dtype=BF16, device=DEV))
+    mla.latent_store(prob, rows, mla.make_cache(prob, kv, lens, table, 64), slots=slots, **kw)
+    small = torch.zeros(1, 64, W, dtype=BF16, device=DEV)
+    mla.latent_store(prob, rows, mla.make_cache(prob, small, lens, table, 64), slots=torch.arange(4, dtype=I32, device=DEV), **kw)
+    flat = kv.view(-1, W)
+    assert torch.equal(flat[slots.long()], small[0, :4])
+    around = torch.cat((flat[:64], flat[-128:])).float().abs().sum(1)
+    assert int((around > 0).sum()) == 4
+    del kv, flat, around
+    # product: 140,000 x 32,768 outputs = 4.6e9
+    M, K, N = 140000, 64, 32768
+    x, w = torch.randn(M, K, device=DEV).to(BF16), torch.randn(K, N, device=DEV).to(BF16)
+    y = mla.linear(x, w)
+    for rows in (slice(0, 300), slice(M - 300, M)):
+        assert torch.equal(y[rows], mla.linear(x[rows], w))
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 1 << 20, 8), (1, 8, 1 << 20), (65535 * 128, 8, 8), (2, 64, 8 * 131071)])
+def test_linear_longest_sides(M, K, N):
+    """Whole numbers, so that every sum is exact: the ends of each size's range."""
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    x = torch.randint(-1, 2, (M, K), generator=g, device=DEV).to(BF16)
+    w = torch.randint(-1, 2, (K, N), generator=g, device=DEV).to(BF16)
+    want = (x.double() @ w.double()).to(torch.float32).to(BF16)
+    assert torch.equal(mla.linear(x, w), want)
+
+
+def test_most_tokens_of_rope_and_store():
+    """65535 sequences of 128 tokens, the most a call takes, padding among them."""
+    B, s_q = 65535, 128
+    prob = problem(B, 1, s_q, d_c=64, d_rope=16, d_nope=16)
+    plan = mla.rope_plan(16, layout=mla.ROPE_HALF)
+    g = torch.Generator(device=DEV).manual_seed(71)
+    x = torch.randn(B, s_q, 1, 16, generator=g, device=DEV).to(BF16)
+    at = torch.randint(-3, 1000, (B, s_q), generator=g, device=DEV).to(I32)
+    out = torch.full_like(x, 9.0)
+    mla.rope(prob, plan, x, positions=at, q_rope=out)
+    assert bool((out[at < 0] == 9).all())
+    pick = torch.randint(0, B * s_q, (2000,), generator=g, device=DEV)
+    pick = torch.cat((pick, torch.tensor([0, B * s_q - 1], device=DEV)))
+    pick = pick[at.flatten()[pick] >= 0]
+    few = x.view(-1, 16)[pick]
+    want = layer.rotate(few.cpu(), at.flatten()[pick].cpu().long(), layer.frequencies(16), True)
+    close(out.view(-1, 16)[pick], want,
+          rope_tolerance(few.cpu(), at.flatten()[pick].cpu().long(), layer.frequencies(16), True, 1.0, want))
+    rows = torch.randn(B * s_q, 80, generator=g, device=DEV).to(BF16)
+    kv = torch.zeros(B * s_q // 64, 64, 80, dtype=BF16, device=DEV)
+    slots = torch.randperm(B * s_q, generator=g, device=DEV).to(I32)
+    lens, table = torch.full((B,), s_q, dtype=I32, device=DEV), torch.zeros(B, 2, dtype=I32, device=DEV)
+    mla.latent_store(prob, rows, mla.make_cache(prob, kv, lens, table, 64), slots=slots)  # neither norm nor rotation: a copy
+    assert torch.equal(kv.view(-1, 80)[slots.long()], rows)
+
+
+def test_one_workspace_in_two_graphs():
+    """Two captured products share a workspace: replayed one after another on a stream, each gives its own result."""
+    g = gen(81)
+    M, K, N = 8, 1000, 20480  # cut along K, its pieces in the workspace
+    w = randn(g, K, N, std=K ** -0.5).to(DEV)
+    xs = [randn(g, M, K).to(DEV) for _ in range(2)]
+    ws = torch.empty(mla.linear_workspace_size(M, K, N), dtype=torch.uint8, device=DEV)
+    assert ws.numel() > 256
+    want = [mla.linear(x, w) for x in xs]
+    graphs, outs = [], []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(mla.linear(x, w, workspace=ws))
+        graphs.append(graph)
+    for i in (0, 1, 1, 0, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
