@@ -184,6 +184,17 @@ class Problem:
     d_v: int
     scale: float
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_dims_kept", None)  # the structure below follows the fields
+
+    def dims_ref(self):
+        """A reference to ``dims()`` for ctypes, made once until a field changes."""
+        ref = self.__dict__.get("_dims_kept")
+        if ref is None:
+            ref = self.__dict__["_dims_kept"] = ctypes.byref(self.dims())
+        return ref
+
     def dims(self) -> Dims:
         return Dims(self.B, self.H, self.s_q, self.d_c, self.d_rope, self.d_nope, self.d_v, float(self.scale))
 
@@ -421,45 +432,56 @@ def read_status(workspace, stream=None) -> int:
 
 # ------------------------------------------------------------- the layer around the attention
 # These calls take a few microseconds on the GPU, so what a call costs on the host counts: every
-# property of a tensor is read once, and pointers and streams go to ctypes as plain integers.
-def _device(t, what: str) -> int:
-    """Index of t's device, which must be the current one."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"{what} must be on the current CUDA device")
-    return dev
-
-
-def _dense(t, what: str, dtype, dev: int, shape=None) -> int:
-    """Address of t, a dense tensor of this type (and shape) on device ``dev``."""
-    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what} must be a dense {dtype} tensor{'' if shape is None else f' {list(shape)}'} on device "
-                         f"{dev}, not {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
-
-def _per_token(t, what: str, dev: int, tokens: int) -> int | None:
-    """Address of t, int32 with one entry a token, or None."""
-    if t is None:
-        return None
-    if t.numel() != tokens:
-        raise ValueError(f"{what} must hold one entry a token ({tokens}), not {t.numel()}")
-    return _dense(t, what, torch.int32, dev)
-
-
-def _rows(t, what: str, dev: int, shape) -> int:
-    """Address of t, a bf16 matrix of this shape with contiguous rows (any stride between them)."""
-    if t.dtype != torch.bfloat16 or t.get_device() != dev or t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a torch.bfloat16 tensor {list(shape)} with contiguous rows on device {dev}, not "
-                         f"{t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
+# property of a tensor is read once, without further calls, and pointers and streams go to ctypes
+# as plain integers.
+_BF16, _I32 = torch.bfloat16, torch.int32
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 try:  # an allocation on the current device without the dispatcher: 1.3 us against torch.empty's 2.8 (Grace host)
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:
     def _empty_strided_cuda(shape, stride, dtype):
         return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
+
+def _device(t, what: str) -> int:
+    """Index of t's device, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    return dev
+
+
+def _refuse(t, what: str, need: str):
+    raise ValueError(f"{what} must be {need}, not {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _dense(t, what: str, dtype, dev: int, shape) -> int:
+    """Address of t, a dense tensor of this type and shape on device ``dev``."""
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+        _refuse(t, what, f"a dense {dtype} tensor {list(shape)} on device {dev}")
+    return t.data_ptr()
+
+
+def _per_token(t, what: str, dev: int, tokens: int) -> int:
+    """Address of t, int32 with one entry a token."""
+    if t.dtype != _I32 or t.get_device() != dev or not t.is_contiguous() or t.numel() != tokens:
+        _refuse(t, what, f"a dense int32 tensor with one entry a token ({tokens}) on device {dev}")
+    return t.data_ptr()
+
+
+def _word(t, dev: int) -> int:
+    """Address of a status word."""
+    if t.dtype != _I32 or t.get_device() != dev or t.numel() < 1:
+        _refuse(t, "status", f"an int32 tensor on device {dev}")
+    return t.data_ptr()
+
+
+def _rows(t, what: str, dev: int, M: int, N: int) -> int:
+    """Address of t, a bf16 matrix with contiguous rows (any stride between them)."""
+    if t.dtype != _BF16 or t.get_device() != dev or t.shape != (M, N) or (N > 1 and t.stride(1) != 1):
+        _refuse(t, what, f"a torch.bfloat16 tensor [{M}, {N}] with contiguous rows on device {dev}")
+    return t.data_ptr()
 
 
 def _raw_stream(dev: int, stream) -> int:
@@ -488,37 +510,38 @@ def rope(prob: Problem, plan: RopePlan, x, positions=None, seq_lens=None, q_nope
     """mla_rope: x [B, s_q, H, d_nope + d_rope] (rows of heads may lie inside wider ones) split
     and rotated, returns (q_nope, q_rope); x [B, s_q, H, d_rope] rotated, returns q_rope (which
     may be x itself).  Tokens are at ``positions`` [B, s_q], or the last of ``seq_lens`` [B]."""
-    lib = load()
+    lib = _lib or load()
     B, s_q, H, d_nope, d_rope = prob.B, prob.s_q, prob.H, prob.d_nope, prob.d_rope
-    dev = _device(x, "x")
-    split = x.shape == (B, s_q, H, d_nope + d_rope)
-    if x.dtype != torch.bfloat16 or not (split or x.shape == (B, s_q, H, d_rope)):
-        raise ValueError(f"x must be torch.bfloat16 [B, s_q, H, d_nope + d_rope or d_rope], not {x.dtype} {list(x.shape)}")
-    st = x.stride()
-    if st[3] != 1 or (B > 1 and s_q > 1 and st[0] != s_q * st[1]):
-        raise ValueError(f"x must have contiguous values and evenly spaced tokens, not the strides {st}")
-    width = d_nope + d_rope if split else d_rope
-    head_stride = st[2] if H > 1 else width
-    token_stride = st[1] if s_q > 1 else st[0] if B > 1 else (H - 1) * head_stride + width
-    pos = _per_token(positions, "positions", dev, B * s_q)
-    lens = None if seq_lens is None else _dense(seq_lens, "seq_lens", torch.int32, dev, (B,))
+    dev, shape = _device(x, "x"), x.shape
+    split = shape == (B, s_q, H, d_nope + d_rope)
+    if x.dtype != _BF16 or not (split or shape == (B, s_q, H, d_rope)):
+        _refuse(x, "x", "torch.bfloat16 [B, s_q, H, d_nope + d_rope or d_rope]")
+    s0, s1, head_stride, s3 = x.stride()
+    if s3 != 1 or (B > 1 and s_q > 1 and s0 != s_q * s1):
+        _refuse(x, "x", "of contiguous values and evenly spaced tokens")
+    if H == 1:
+        head_stride = shape[3]
+    token_stride = s1 if s_q > 1 else s0 if B > 1 else (H - 1) * head_stride + shape[3]
+    pos = None if positions is None else _per_token(positions, "positions", dev, B * s_q)
+    lens = None if seq_lens is None else _dense(seq_lens, "seq_lens", _I32, dev, (B,))
     nope = None
     if split:
         if q_nope is None:
-            q_nope = _empty_strided_cuda((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), torch.bfloat16)
+            q_nope = _empty_strided_cuda((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), _BF16)
             nope = q_nope.data_ptr()
         else:
-            nope = _dense(q_nope, "q_nope", torch.bfloat16, dev, (B, s_q, H, d_nope))
+            nope = _dense(q_nope, "q_nope", _BF16, dev, (B, s_q, H, d_nope))
     elif q_nope is not None:
         raise ValueError("rows of d_rope values have no part for q_nope")
     if q_rope is None:
-        q_rope = _empty_strided_cuda((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), torch.bfloat16)
+        q_rope = _empty_strided_cuda((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), _BF16)
         turned = q_rope.data_ptr()
     else:
-        turned = _dense(q_rope, "q_rope", torch.bfloat16, dev, (B, s_q, H, d_rope))
-    d = prob.dims()
-    _check(lib.mla_rope(ctypes.byref(d), ctypes.byref(plan), x.data_ptr(), token_stride, head_stride, pos, lens, nope,
-                        turned, int(transpose), _raw_stream(dev, stream)), "mla_rope")
+        turned = _dense(q_rope, "q_rope", _BF16, dev, (B, s_q, H, d_rope))
+    code = lib.mla_rope(prob.dims_ref(), ctypes.byref(plan), x.data_ptr(), token_stride, head_stride, pos, lens, nope,
+                        turned, int(transpose), _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_rope")
     return (q_nope, q_rope) if split else q_rope
 
 
@@ -532,10 +555,10 @@ class Pages:
 
     def __post_init__(self):
         dev = _device(self.block_table, "block_table")
-        _dense(self.block_table, "block_table", torch.int32, dev)
-        _dense(self.free_ring, "free_ring", torch.int32, dev)
         if self.block_table.dim() != 2 or self.free_ring.dim() != 1:
             raise ValueError("block_table must be [B, max_pages], free_ring [num_pages]")
+        _dense(self.block_table, "block_table", _I32, dev, self.block_table.shape)
+        _dense(self.free_ring, "free_ring", _I32, dev, self.free_ring.shape)
 
     @classmethod
     def empty(cls, B: int, max_pages: int, num_pages: int, page_size: int = 64, device="cuda"):
@@ -560,33 +583,35 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
                  status=None, stream=None) -> PagesStep:
     """mla_pages_update: every request from old_lens[b] to new_lens[b] tokens.  ``out`` (the
     result of an earlier call) is written over; its tensors must not be this call's inputs."""
-    lib = load()
+    lib = _lib or load()
     table, ring = pages.block_table, pages.free_ring
     dev = _device(table, "block_table")
     B, max_pages = table.shape
-    state = _dense(ring_state, "ring_state", torch.int32, dev, (2,))
-    old = _dense(old_lens, "old_lens", torch.int32, dev, (B,))
-    new = _dense(new_lens, "new_lens", torch.int32, dev, (B,))
-    word = None if status is None else _dense(status, "status", torch.int32, dev)
+    state = _dense(ring_state, "ring_state", _I32, dev, (2,))
+    old = _dense(old_lens, "old_lens", _I32, dev, (B,))
+    new = _dense(new_lens, "new_lens", _I32, dev, (B,))
+    word = None if status is None else _word(status, dev)
     if out is None:
-        i32, one = torch.int32, (1,)
-        lens = _empty_strided_cuda((B,), one, i32)
-        state_out = _empty_strided_cuda((2,), one, i32)
-        start = _empty_strided_cuda((B + 1,), one, i32)
-        pos = _empty_strided_cuda((max_tokens,), one, i32)
-        slot = _empty_strided_cuda((max_tokens,), one, i32)
+        one = (1,)
+        lens = _empty_strided_cuda((B,), one, _I32)
+        state_out = _empty_strided_cuda((2,), one, _I32)
+        start = _empty_strided_cuda((B + 1,), one, _I32)
+        pos = _empty_strided_cuda((max_tokens,), one, _I32)
+        slot = _empty_strided_cuda((max_tokens,), one, _I32)
         out = PagesStep(lens, state_out, start, pos, slot)
         lens, state_out, start = lens.data_ptr(), state_out.data_ptr(), start.data_ptr()
         pos, slot = pos.data_ptr(), slot.data_ptr()
     else:
-        lens = _dense(out.seq_lens, "seq_lens", torch.int32, dev, (B,))
-        state_out = _dense(out.ring_state, "ring_state", torch.int32, dev, (2,))
-        start = _dense(out.token_start, "token_start", torch.int32, dev, (B + 1,))
-        pos = _dense(out.positions, "positions", torch.int32, dev, (max_tokens,))
-        slot = _dense(out.slots, "slots", torch.int32, dev, (max_tokens,))
+        lens = _dense(out.seq_lens, "seq_lens", _I32, dev, (B,))
+        state_out = _dense(out.ring_state, "ring_state", _I32, dev, (2,))
+        start = _dense(out.token_start, "token_start", _I32, dev, (B + 1,))
+        pos = _dense(out.positions, "positions", _I32, dev, (max_tokens,))
+        slot = _dense(out.slots, "slots", _I32, dev, (max_tokens,))
     pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], table.data_ptr(), ring.data_ptr(), state, state_out)
-    _check(lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, lens, start, pos, slot, word,
-                                _raw_stream(dev, stream)), "mla_pages_update")
+    code = lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, lens, start, pos, slot, word,
+                                _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_pages_update")
     return out
 
 
@@ -594,18 +619,19 @@ def latent_store(prob: Problem, x, cache: Cache, plan: RopePlan | None = None, n
                  positions=None, slots=None, status=None, stream=None) -> None:
     """mla_latent_store: rows [c | k] of the new tokens (x [B * s_q, d_c + d_rope], inside wider
     rows or not) normalised, rotated and written to the cache, whose kv buffer is modified."""
-    lib = load()
+    lib = _lib or load()
     dev = _device(x, "x")
     tokens, width = prob.B * prob.s_q, prob.d_c + prob.d_rope
-    rows = _rows(x, "x", dev, (tokens, width))
-    weight = None if norm_weight is None else _dense(norm_weight, "norm_weight", torch.bfloat16, dev, (prob.d_c,))
-    pos = _per_token(positions, "positions", dev, tokens)
-    slot = _per_token(slots, "slots", dev, tokens)
-    word = None if status is None else _dense(status, "status", torch.int32, dev)
-    d = prob.dims()
-    _check(lib.mla_latent_store(ctypes.byref(d), None if plan is None else ctypes.byref(plan), rows,
+    rows = _rows(x, "x", dev, tokens, width)
+    weight = None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, dev, (prob.d_c,))
+    pos = None if positions is None else _per_token(positions, "positions", dev, tokens)
+    slot = None if slots is None else _per_token(slots, "slots", dev, tokens)
+    word = None if status is None else _word(status, dev)
+    code = lib.mla_latent_store(prob.dims_ref(), None if plan is None else ctypes.byref(plan), rows,
                                 x.stride(0) if tokens > 1 else width, weight, eps, pos, slot, ctypes.byref(cache), word,
-                                _raw_stream(dev, stream)), "mla_latent_store")
+                                _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_latent_store")
 
 
 def linear_workspace_size(M: int, K: int, N: int) -> int:
@@ -619,23 +645,26 @@ def linear_workspace_size(M: int, K: int, N: int) -> int:
 def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, workspace=None, stream=None):
     """mla_linear: residual + act(x . w + bias), x [M, K] and residual [M, N] with any row stride
     (multiples of 8), w [K, N] dense.  ``out`` may be ``residual``."""
-    lib = load()
+    lib = _lib or load()
     dev = _device(x, "x")
     if w.dim() != 2 or x.dim() != 2:
         raise ValueError("x must be [M, K], w [K, N]")
     K, N = w.shape
     M = x.shape[0]
-    rows, weight = _rows(x, "x", dev, (M, K)), _dense(w, "w", torch.bfloat16, dev)
-    b = None if bias is None else _dense(bias, "bias", torch.bfloat16, dev, (N,))
-    res = None if residual is None else _rows(residual, "residual", dev, (M, N))
+    rows = _rows(x, "x", dev, M, K)
+    if w.dtype != _BF16 or w.get_device() != dev or not w.is_contiguous():
+        _refuse(w, "w", f"a dense torch.bfloat16 tensor on device {dev}")
+    b = None if bias is None else _dense(bias, "bias", _BF16, dev, (N,))
+    res = None if residual is None else _rows(residual, "residual", dev, M, N)
     if out is None:
-        out = _empty_strided_cuda((M, N), (N, 1), torch.bfloat16)
-        to = out.data_ptr()
+        out = _empty_strided_cuda((M, N), (N, 1), _BF16)
+        to, out_stride = out.data_ptr(), N
     else:
-        to = _rows(out, "out", dev, (M, N))
-    one = M <= 1  # a single row has no stride
-    desc = LinearDesc(M, K, N, act, K if one else x.stride(0), N if one else out.stride(0),
-                      N if one or residual is None else residual.stride(0))
+        to, out_stride = _rows(out, "out", dev, M, N), out.stride(0)
+    if M > 1:
+        desc = LinearDesc(M, K, N, act, x.stride(0), out_stride, N if res is None else residual.stride(0))
+    else:  # a single row has no stride
+        desc = LinearDesc(M, K, N, act, K, N, N)
     at = ctypes.byref(desc)
     if workspace is None:
         nbytes, ws = lib.mla_linear_workspace_size(at), None
@@ -644,7 +673,9 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
             ws = workspace.data_ptr()
     else:
         nbytes, ws = workspace.numel(), workspace.data_ptr()
-    _check(lib.mla_linear(at, rows, weight, b, res, to, ws, nbytes, _raw_stream(dev, stream)), "mla_linear")
+    code = lib.mla_linear(at, rows, w.data_ptr(), b, res, to, ws, nbytes, _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_linear")
     return out
 
 
