@@ -25,7 +25,8 @@
 //
 // With many tokens a tile is 256 columns x 256 tokens on a pair of CTAs: one MMA of 256 x 256
 // x 16 over both, each holding half of both operands, so that an SM takes in 32 KB a chunk
-// instead of 48.  Measured (device time): 4096 x 16384 x 7168 in 507 us = 1,897 TFLOP/s =
+// instead of 48 (with the tokens as the MMA's rows, and rows written as they come or turned
+// over in bf16, 0 to 6 % slower).  Measured (device time): 4096 x 16384 x 7168 in 507 us = 1,897 TFLOP/s =
 // 0.98 of the measured bf16 rate (tiles of 128 x 256 on single CTAs: 560), bound by the tensor
 // cores; 64 x 16384 x 7168 in 39.7 us, 235 MB of weights at 5.9 TB/s = 0.88 of the measured copy
 // bandwidth, with 2 us of start and 4 of exchange and epilogue around the stream;
@@ -70,15 +71,15 @@ __host__ __device__ __forceinline__ long long run_start(const Plan &p, int g) {
 //                       600 at 256 (the MMAs alone: 512); or what it takes the card to bring
 //                       the weights for all CTAs at work, at 3500 bytes a cycle
 //   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
-//   a cluster's exchange  about 2000 cycles
+//   a cluster's exchange  about 1000 cycles and 30 a token
 //   a chunk of a pair's tile  530 cycles
 //   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back at half
 //                       the card's rate
 // E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
 // tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters;
 // 4096 x 7168 x 576: 40.9 us in pairs, 49.9 in runs; 4096 x 16384 x 7168: 510 us in pairs,
-// 587 in whole tiles of 128 x 256.  Over 23 shapes from 1 x 7168 x 576 up the choice was
-// within 6 % of the best plan timed, but for two below 8 us (11 %).
+// 587 in whole tiles of 128 x 256.  Over 32 shapes from 1 x 7168 x 576 up the choice was
+// within 12 % of the best plan timed, and within 4 % for all but five.
 Plan make_plan(int M, int K, int N, int sms) {
     Plan best{};
     double best_cost = 0.0;
@@ -115,7 +116,7 @@ Plan make_plan(int M, int K, int N, int sms) {
             p.grid = p.cluster > 1 ? (int)tiles * p.cluster : tiles < sms ? (int)tiles : sms;
             const double at_work = (double)(tiles < fit ? tiles : fit) * p.cluster;
             keep(waves * ((p.nk + p.cluster - 1) / p.cluster * chunk(at_work)) + epilogue +
-                 (p.cluster > 1 ? 2000.0 + (waves - 1) * (epilogue + 3000.0) : 0.0));
+                 (p.cluster > 1 ? 1000.0 + 30.0 * bt + (waves - 1) * (epilogue + 3000.0) : 0.0));
         }
         p.cluster = 1;
         if (bt == 256) {
@@ -152,13 +153,45 @@ struct Smem {
     static constexpr uint32_t kTmemCols = 2 * BT < 32 ? 32 : 2 * BT;
 };
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// v / (1 + 2^-x): v times the logistic function of x ln 2.
+__device__ __forceinline__ float times_logistic(float v, float x) { return v * rcp(1.f + ex2(-x)); }
+
+// v Phi(v), Phi the normal distribution.  With z = |v| / sqrt 2 and t = 1 / (1 + z / 2),
+//   Phi(-|v|) = erfc(z) / 2 = t 2^(Q(t) - z^2 log2 e),
+// Q a polynomial fitted to log2(erfc(z) exp(z^2) / (2 t)) on (0, 1] (worst error 3.4e-6): no
+// cancellation on either side, relative error of the whole at most 2^-17.3.  CUDA's erfcf in
+// its place took a 1588 x 400 x 6072 product with bias and residual from 29 us to 41.
+__device__ __forceinline__ float gelu(float v) {
+    const float t = rcp(fmaf(fabsf(v), 0.35355339f, 1.f));
+    float q = fmaf(t, -0.22946589f, 0.9304564f);
+    q = fmaf(t, q, -1.2151098f);
+    q = fmaf(t, q, 0.32995093f);
+    q = fmaf(t, q, 0.014981962f);
+    q = fmaf(t, q, 0.55273217f);
+    q = fmaf(t, q, 1.4422023f);
+    q = fmaf(t, q, -2.8257446f);
+    const float below = t * ex2(fmaf(v * v, -0.72134752f, q));
+    return v * (v < 0.f ? below : 1.f - below);
+}
+
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {
     if (kAct == MLA_ACT_RELU) return v < 0.f ? 0.f : v;  // NaN stays
-    if (kAct == MLA_ACT_SILU) return __fdividef(v, 1.f + __expf(-v));
-    // 1 + erf(z) = erfc(-z) and (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)): no cancellation where they are small
-    if (kAct == MLA_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678f);
-    if (kAct == MLA_ACT_GELU_TANH) return __fdividef(v, 1.f + __expf(-1.59576912f * (v + 0.044715f * v * v * v)));
+    if (kAct == MLA_ACT_SILU) return times_logistic(v, v * 1.442695041f);
+    if (kAct == MLA_ACT_GELU) return gelu(v);
+    // (1 + tanh z) / 2 is the logistic function of 2 z
+    if (kAct == MLA_ACT_GELU_TANH) return times_logistic(v, v * fmaf(v * v, 0.10294324f, 2.3022082f));
     return v;
 }
 template <int kAct, int N>

@@ -188,6 +188,9 @@ class Problem:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_dims_kept", None)  # the structure below follows the fields
 
+    def __getstate__(self):  # copies and pickles take the fields alone
+        return {f: v for f, v in self.__dict__.items() if f != "_dims_kept"}
+
     def dims_ref(self):
         """A reference to ``dims()`` for ctypes, made once until a field changes."""
         ref = self.__dict__.get("_dims_kept")

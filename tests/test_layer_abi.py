@@ -1,7 +1,9 @@
 """The operators around the attention (mla_rope, mla_pages_update, mla_latent_store, mla_linear): what they refuse on the
 host, before anything is launched, and the rotation's frequencies.  No GPU needed."""
+import copy
 import ctypes
 import math
+import pickle
 
 import pytest
 
@@ -21,6 +23,20 @@ def lib():
 
 def dims(B=4, H=16, s_q=1, d_c=512, d_rope=64, d_nope=128, d_v=128):
     return mla.Problem(B, H, s_q, d_c, d_rope, d_nope, d_v, 0.1).dims()
+
+
+def test_problem_keeps_its_structure_up_to_date():
+    """The ctypes structure made once per Problem follows its fields, and copies and pickles do without it."""
+    p = mla.Problem(4, 16, 1, 512, 64, 128, 128, 0.5)
+
+    def seen(q):
+        return ctypes.cast(q.dims_ref(), ctypes.POINTER(mla.Dims)).contents
+
+    assert seen(p).B == 4 and p.dims_ref() is p.dims_ref()
+    q, r, s = copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p))
+    p.B, q.H, r.scale = 7, 3, 0.25
+    assert (seen(p).B, seen(p).H) == (7, 16) and (seen(q).B, seen(q).H) == (4, 3) and seen(r).scale == 0.25
+    assert s == mla.Problem(4, 16, 1, 512, 64, 128, 128, 0.5) and seen(s).scale == 0.5
 
 
 # ------------------------------------------------------------------------------------------------------------- rope
