@@ -466,7 +466,7 @@ MLA_API int mla_rope(const mla_dims *dims, const mla_rope_plan *plan, const void
                      long long head_stride, const int *positions, const int *seq_lens, void *pass_out,
                      void *rope_out, int transpose, void *stream);
 
-/* The pages of a batch.  Free pages sit in a ring, taken at its head and given
+/* The pages of a batch, each held by one request.  Free pages sit in a ring, taken at its head and given
  * back at its tail, so that a page just given back is the last to be used again. */
 typedef struct {
     int B;               /* requests */
