@@ -54,8 +54,19 @@ struct LinearArgs {
     long long x_stride, out_stride, residual_stride;
     float *part;  // workspace: fp32 tiles of the pieces of tiles that are cut along K
 };
-size_t linear_workspace_bytes(int M, int K, int N);
-cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st);
+// How a product is cut (see linear.cu).
+struct LinearPlan {
+    int bt;                // tokens a tile
+    int tiles_m, tiles_n;  // tile t: tokens (t % tiles_m) * bt, columns (t / tiles_m) * 128 (pair: 256)
+    int nk;                // chunks a tile
+    int grid;
+    int cluster;           // CTAs that share a tile's K (1: none)
+    bool whole;            // whole tiles, CTA g the tiles g, g + grid, ...; else runs of chunks
+    bool pair;             // a tile is 256 columns, taken by a pair of CTAs
+};
+LinearPlan linear_plan(int M, int K, int N, int sms);
+size_t linear_workspace_bytes(const LinearPlan &p);
+cudaError_t launch_linear(const LinearArgs &a, const LinearPlan &p, cudaStream_t st);
 
 // SMs of the current device (work plans only), looked up once per device.
 int layer_num_sms();

@@ -275,18 +275,19 @@ MLA_API int mla_latent_store(const mla_dims *dims, const mla_rope_plan *plan, co
 
 MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *d) {
     if (check_linear(d, false)) return 0;
-    return d->M == 0 ? 256 : mla::linear_workspace_bytes(d->M, d->K, d->N);
+    return d->M == 0 ? 256 : mla::linear_workspace_bytes(mla::linear_plan(d->M, d->K, d->N, mla::layer_num_sms()));
 }
 
 MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, const void *bias, const void *residual,
                        void *out, void *workspace, size_t ws_bytes, void *stream) {
     int s = check_linear(d, residual != nullptr);
     if (s) return s;
-    const size_t need = mla_linear_workspace_size(d);
-    if (!workspace && need > 256) return MLA_ERR_NULL;
     if (!aligned(workspace, 16)) return MLA_ERR_ALIGN;
+    if (d->M == 0) return ws_bytes < 256 ? MLA_ERR_WORKSPACE : MLA_OK;
+    const mla::LinearPlan plan = mla::linear_plan(d->M, d->K, d->N, mla::layer_num_sms());
+    const size_t need = mla::linear_workspace_bytes(plan);
     if (ws_bytes < need) return MLA_ERR_WORKSPACE;
-    if (d->M == 0) return MLA_OK;
+    if (!workspace && need > 256) return MLA_ERR_NULL;
     if (!x || !w || !out) return MLA_ERR_NULL;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16))
         return MLA_ERR_ALIGN;
@@ -306,7 +307,7 @@ MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, c
     a.out_stride = d->out_stride;
     a.residual_stride = d->residual_stride;
     a.part = (float *)workspace;
-    return result(mla::launch_linear(a, as_stream(stream)));
+    return result(mla::launch_linear(a, plan, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -51,94 +51,10 @@ constexpr int kStep = 16;     // tokens an epilogue warp turns over at a time
 constexpr int kPitch = 36;  // floats between the tokens of a turned tile: conflict-free columns, 16-byte rows
 constexpr int kMinChunks = 4;  // chunks a CTA's run of a cut tile holds at least
 
-struct Plan {
-    int bt;                // tokens a tile
-    int tiles_m, tiles_n;  // tile t: tokens (t % tiles_m) * bt, columns (t / tiles_m) * 128
-    int nk;                // chunks a tile
-    int grid;
-    int cluster;           // CTAs that share a tile's K (1: none)
-    bool whole;            // whole tiles, CTA g the tiles g, g + grid, ...; else runs of chunks
-    bool pair;             // a tile is 256 columns, taken by a pair of CTAs
-};
+using Plan = LinearPlan;
 
 __host__ __device__ __forceinline__ long long run_start(const Plan &p, int g) {
     return (long long)p.tiles_m * p.tiles_n * p.nk * g / p.grid;
-}
-
-// The plan with the shortest estimate, in SM cycles.  What the parts were measured to take
-// (clock traces at M = 64, 333, 2048 and 4096, K = 1000 to 16384):
-//   a chunk of a tile   about 400 cycles for narrow tiles (waits and issue), 455 at 128 tokens,
-//                       600 at 256 (the MMAs alone: 512); or what it takes the card to bring
-//                       the weights for all CTAs at work, at 3500 bytes a cycle
-//   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
-//   a cluster's exchange  about 1000 cycles and 30 a token
-//   a chunk of a pair's tile  530 cycles
-//   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back at half
-//                       the card's rate
-// E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
-// tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters;
-// 4096 x 7168 x 576: 40.9 us in pairs, 49.9 in runs; 4096 x 16384 x 7168: 510 us in pairs,
-// 587 in whole tiles of 128 x 256.  Over 32 shapes from 1 x 7168 x 576 up the choice was
-// within 12 % of the best plan timed, and within 4 % for all but five.
-Plan make_plan(int M, int K, int N, int sms) {
-    Plan best{};
-    double best_cost = 0.0;
-    for (int bt = 16; bt <= 256; bt *= 2) {
-        if (bt > 16 && bt / 2 >= M) break;
-        Plan p;
-        p.bt = bt;
-        p.tiles_m = (M + bt - 1) / bt;
-        p.tiles_n = (N + kBN - 1) / kBN;
-        p.nk = (K + kBK - 1) / kBK;
-        const long long tiles = (long long)p.tiles_m * p.tiles_n;
-        if (tiles > (1ll << 28)) continue;
-        auto chunk = [&](double ctas) {
-            const double c = 390.0 + 0.5 * bt > 2.35 * bt ? 390.0 + 0.5 * bt : 2.35 * bt;
-            const double hbm = ctas / p.tiles_m * 16384 / 3500.0;
-            return c < hbm ? hbm : c;
-        };
-        auto keep = [&](double cost) {
-            if (best.bt == 0 || cost < best_cost) {
-                best = p;
-                best_cost = cost;
-            }
-        };
-        const double epilogue = 1000.0 + 36.0 * bt;
-        p.pair = false;
-        p.whole = true;
-        for (p.cluster = 1; p.cluster <= 8; p.cluster *= 2) {
-            if (p.cluster > 1 && (p.nk < 2 * p.cluster || tiles > sms)) break;
-            // clusters that fit the SMs: fewer than an even share, as a cluster stays within
-            // one of the groups the SMs are built in
-            const int fit = p.cluster == 1 ? sms : p.cluster == 2 ? sms / 2 - 4 : p.cluster == 4 ? sms / 4 - 4 : sms / 8 - 5;
-            if (fit < 1) break;
-            const long long waves = (tiles + fit - 1) / fit;
-            p.grid = p.cluster > 1 ? (int)tiles * p.cluster : tiles < sms ? (int)tiles : sms;
-            const double at_work = (double)(tiles < fit ? tiles : fit) * p.cluster;
-            keep(waves * ((p.nk + p.cluster - 1) / p.cluster * chunk(at_work)) + epilogue +
-                 (p.cluster > 1 ? 1000.0 + 30.0 * bt + (waves - 1) * (epilogue + 3000.0) : 0.0));
-        }
-        p.cluster = 1;
-        if (bt == 256) {
-            p.pair = true;
-            p.tiles_n = (N + 2 * kBN - 1) / (2 * kBN);
-            const long long pairs = (long long)p.tiles_m * p.tiles_n, fit = sms / 2;
-            p.grid = 2 * (int)(pairs < fit ? pairs : fit);
-            keep((pairs + fit - 1) / fit * (p.nk * 530.0) + epilogue + 1000.0);
-            p.pair = false;
-            p.tiles_n = (N + kBN - 1) / kBN;
-        }
-        const long long most = (tiles * p.nk + kMinChunks - 1) / kMinChunks;
-        p.grid = most < sms ? (int)most : sms;
-        // equal runs of chunks are whole tiles; and over several waves whole tiles in order of
-        // the tokens share their weights in L2, which runs of tiles of a CTA's own do not
-        // (4096 x 16384 x 7168: 611 us whole, 775 us in runs)
-        if (tiles % p.grid == 0 || tiles >= 2 * sms) continue;
-        p.whole = false;
-        keep((double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk(p.grid) + epilogue + 6000.0 +
-             4.0 * (p.grid < tiles ? 2.0 * p.grid : p.grid + tiles) * kBN * bt * 4 / 3500.0);
-    }
-    return best;
 }
 
 template <int BT, bool kPair>
@@ -696,13 +612,87 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
 
 }  // namespace
 
-size_t linear_workspace_bytes(int M, int K, int N) {
-    const Plan p = make_plan(M, K, N, layer_num_sms());
+// The plan with the shortest estimate, in SM cycles.  What the parts were measured to take
+// (clock traces at M = 64, 333, 2048 and 4096, K = 1000 to 16384):
+//   a chunk of a tile   about 400 cycles for narrow tiles (waits and issue), 455 at 128 tokens,
+//                       600 at 256 (the MMAs alone: 512); or what it takes the card to bring
+//                       the weights for all CTAs at work, at 3500 bytes a cycle
+//   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
+//   a cluster's exchange  about 1000 cycles and 30 a token
+//   a chunk of a pair's tile  530 cycles
+//   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back at half
+//                       the card's rate
+// E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
+// tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters;
+// 4096 x 7168 x 576: 40.9 us in pairs, 49.9 in runs; 4096 x 16384 x 7168: 510 us in pairs,
+// 587 in whole tiles of 128 x 256.  Over 32 shapes from 1 x 7168 x 576 up the choice was
+// within 12 % of the best plan timed, and within 4 % for all but five.
+LinearPlan linear_plan(int M, int K, int N, int sms) {
+    Plan best{};
+    double best_cost = 0.0;
+    for (int bt = 16; bt <= 256; bt *= 2) {
+        if (bt > 16 && bt / 2 >= M) break;
+        Plan p;
+        p.bt = bt;
+        p.tiles_m = (M + bt - 1) / bt;
+        p.tiles_n = (N + kBN - 1) / kBN;
+        p.nk = (K + kBK - 1) / kBK;
+        const long long tiles = (long long)p.tiles_m * p.tiles_n;
+        if (tiles > (1ll << 28)) continue;
+        auto chunk = [&](double ctas) {
+            const double c = 390.0 + 0.5 * bt > 2.35 * bt ? 390.0 + 0.5 * bt : 2.35 * bt;
+            const double hbm = ctas / p.tiles_m * 16384 / 3500.0;
+            return c < hbm ? hbm : c;
+        };
+        auto keep = [&](double cost) {
+            if (best.bt == 0 || cost < best_cost) {
+                best = p;
+                best_cost = cost;
+            }
+        };
+        const double epilogue = 1000.0 + 36.0 * bt;
+        p.pair = false;
+        p.whole = true;
+        for (p.cluster = 1; p.cluster <= 8; p.cluster *= 2) {
+            if (p.cluster > 1 && (p.nk < 2 * p.cluster || tiles > sms)) break;
+            // clusters that fit the SMs: fewer than an even share, as a cluster stays within
+            // one of the groups the SMs are built in
+            const int fit = p.cluster == 1 ? sms : p.cluster == 2 ? sms / 2 - 4 : p.cluster == 4 ? sms / 4 - 4 : sms / 8 - 5;
+            if (fit < 1) break;
+            const long long waves = (tiles + fit - 1) / fit;
+            p.grid = p.cluster > 1 ? (int)tiles * p.cluster : tiles < sms ? (int)tiles : sms;
+            const double at_work = (double)(tiles < fit ? tiles : fit) * p.cluster;
+            keep(waves * ((p.nk + p.cluster - 1) / p.cluster * chunk(at_work)) + epilogue +
+                 (p.cluster > 1 ? 1000.0 + 30.0 * bt + (waves - 1) * (epilogue + 3000.0) : 0.0));
+        }
+        p.cluster = 1;
+        if (bt == 256) {
+            p.pair = true;
+            p.tiles_n = (N + 2 * kBN - 1) / (2 * kBN);
+            const long long pairs = (long long)p.tiles_m * p.tiles_n, fit = sms / 2;
+            p.grid = 2 * (int)(pairs < fit ? pairs : fit);
+            keep((pairs + fit - 1) / fit * (p.nk * 530.0) + epilogue + 1000.0);
+            p.pair = false;
+            p.tiles_n = (N + kBN - 1) / kBN;
+        }
+        const long long most = (tiles * p.nk + kMinChunks - 1) / kMinChunks;
+        p.grid = most < sms ? (int)most : sms;
+        // equal runs of chunks are whole tiles; and over several waves whole tiles in order of
+        // the tokens share their weights in L2, which runs of tiles of a CTA's own do not
+        // (4096 x 16384 x 7168: 611 us whole, 775 us in runs)
+        if (tiles % p.grid == 0 || tiles >= 2 * sms) continue;
+        p.whole = false;
+        keep((double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk(p.grid) + epilogue + 6000.0 +
+             4.0 * (p.grid < tiles ? 2.0 * p.grid : p.grid + tiles) * kBN * bt * 4 / 3500.0);
+    }
+    return best;
+}
+
+size_t linear_workspace_bytes(const LinearPlan &p) {
     return p.whole ? 256 : 2ull * p.grid * kBN * p.bt * sizeof(float);
 }
 
-cudaError_t launch_linear(const LinearArgs &a, cudaStream_t st) {
-    const Plan p = make_plan(a.M, a.K, a.N, layer_num_sms());
+cudaError_t launch_linear(const LinearArgs &a, const LinearPlan &p, cudaStream_t st) {
     cudaError_t e;
     switch (p.bt) {
         case 16: e = launch_bt<16>(a, p, st); break;

@@ -438,6 +438,7 @@ def read_status(workspace, stream=None) -> int:
 # property of a tensor is read once, without further calls, and pointers and streams go to ctypes
 # as plain integers.
 _BF16, _I32 = torch.bfloat16, torch.int32
+_ERR_WORKSPACE = 5  # MLA_ERR_WORKSPACE
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 try:  # an allocation on the current device without the dispatcher: 1.3 us against torch.empty's 2.8 (Grace host)
@@ -668,15 +669,15 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
         desc = LinearDesc(M, K, N, act, x.stride(0), out_stride, N if res is None else residual.stride(0))
     else:  # a single row has no stride
         desc = LinearDesc(M, K, N, act, K, N, N)
-    at = ctypes.byref(desc)
-    if workspace is None:
-        nbytes, ws = lib.mla_linear_workspace_size(at), None
-        if nbytes > 256:  # below that none is used
+    at, weight, st = ctypes.byref(desc), w.data_ptr(), _raw_stream(dev, stream)
+    if workspace is not None:
+        code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), workspace.numel(), st)
+    else:  # most shapes need none
+        code = lib.mla_linear(at, rows, weight, b, res, to, None, 256, st)
+        if code == _ERR_WORKSPACE:
+            nbytes = lib.mla_linear_workspace_size(at)
             workspace = _empty_strided_cuda((nbytes,), (1,), torch.uint8)
-            ws = workspace.data_ptr()
-    else:
-        nbytes, ws = workspace.numel(), workspace.data_ptr()
-    code = lib.mla_linear(at, rows, w.data_ptr(), b, res, to, ws, nbytes, _raw_stream(dev, stream))
+            code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), nbytes, st)
     if code:
         raise MLAError(code, "mla_linear")
     return out
