@@ -9,9 +9,9 @@
 // K runs in chunks of 64 through a ring of TMA stages.  The work is tiles x chunks, cut
 // in one of three ways:
 //   whole    a CTA takes whole tiles;
-//   cluster  2, 4 or 8 CTAs of a cluster take a tile's K in equal parts, exchange their
-//            accumulators through distributed shared memory and finish a share of the
-//            tokens each;
+//   cluster  2, 4 or 8 CTAs (or pairs, see below) of a cluster take a tile's K in equal
+//            parts, exchange their accumulators through distributed shared memory and
+//            finish a share of the tokens each;
 //   runs     the tiles laid end to end are dealt out in equal runs of chunks, one a CTA:
 //            the end of one tile, whole ones, the start of another.  The pieces of a cut
 //            tile go to the workspace in fp32, and a second kernel joins them.
@@ -126,6 +126,13 @@ __device__ __forceinline__ void activate(int act, float (&v)[N]) {
     }
 }
 
+// Cluster plans: CTAs of a tile (a cluster), and which part of K this one's are.
+__device__ __forceinline__ int ctas_a_tile(const Plan &p) { return p.pair ? 2 * p.cluster : p.cluster; }
+__device__ __forceinline__ int part_of_k(const Plan &p) {
+    const int r = blockIdx.x % ctas_a_tile(p);
+    return p.pair ? r / 2 : r;
+}
+
 // One segment of a CTA's work: chunks [k0, k1) of a tile.
 struct Segment {
     int tile, k0, k1;
@@ -135,7 +142,7 @@ struct Walk {
     long long u, end;
     __device__ __forceinline__ Walk(const Plan &plan, int g) : p(plan) {
         if (p.cluster > 1) {
-            u = g / p.cluster;
+            u = g / ctas_a_tile(p);
             end = u + 1;
             return;
         }
@@ -145,7 +152,7 @@ struct Walk {
     __device__ __forceinline__ bool next(Segment &s) {
         if (u >= end) return false;
         if (p.cluster > 1) {
-            const int rank = blockIdx.x % p.cluster;
+            const int rank = part_of_k(p);
             s = Segment{(int)u, p.nk * rank / p.cluster, p.nk * (rank + 1) / p.cluster};
             u = end;
             return true;
@@ -286,12 +293,13 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives on `bar` of both CTAs when the MMAs issued so far have completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+// Arrives on `bar` of both CTAs (`pair`: their bits by rank in the cluster) when the MMAs
+// issued so far have completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint32_t pair) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)pair)
         : "memory");
 }
 
@@ -338,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a tile's columns, and this CTA's part of them (and of its tokens' copies) in a pair
     constexpr int kTileN = kPair ? 2 * kBN : kBN;
     const int half = kPair ? (int)(blockIdx.x & 1) : 0;
+    const uint32_t leader = kPair ? cluster_rank() & ~1u : 0, both = 3u << leader;
     Walk walk(plan, blockIdx.x);
     Segment seg;
 
@@ -346,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the loops in a single lane, a chunk took 583 cycles whatever its width, all of it
     // issue; the MMAs of the widest tile take 512.)
     if (warp == 0) {
-        const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), 0) : 0;
+        const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), leader) : 0;
         uint32_t s = 0, phase = 1, issued = 0;
         bool ok = true, free = mbar_test_wait(&empty[0], 1);
         while (ok && walk.next(seg)) {
@@ -417,13 +426,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < kBK / 16; ++kk)
                         (kPair ? mma_ss_pair : mma_ss)(d, dw + kk * (16 * 128 >> 4), dx + kk * (32 >> 4), idesc,
                                                        kk > 0 || kc > seg.k0);
-                    (kPair ? mma_commit_pair : mma_commit)(bar);
-                    if (kc + 1 == seg.k1) (kPair ? mma_commit_pair : mma_commit)(&acc_full[b]);
+                    if (kPair) mma_commit_pair(bar, both);
+                    else mma_commit(bar);
+                    if (kc + 1 == seg.k1) {
+                        if (kPair) mma_commit_pair(&acc_full[b], both);
+                        else mma_commit(&acc_full[b]);
+                    }
                 }
             }
         }
         if (!ok || *abort_flag) {  // let the MMAs in flight end before the memory they use is given up
-            if (elect_one()) (kPair ? mma_commit_pair : mma_commit)(drain);
+            if (elect_one()) {
+                if (kPair) mma_commit_pair(drain, both);
+                else mma_commit(drain);
+            }
             mbar_wait(drain, 0);
         }
     } else if (warp >= 2) {
@@ -469,16 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 if (half == 0) mbar_arrive(&acc_empty[b]);
-                else mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[b]), 0));
+                else mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[b]), leader));
             }
             first_seg = false;
         }
     }
-    if (!kPair && plan.cluster > 1) {
+    if (plan.cluster > 1) {
         // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
         // have, takes the parts of the tokens this CTA finishes, one slot a rank.
-        const int rank = blockIdx.x % plan.cluster, share = BT / plan.cluster;
-        const int tile = blockIdx.x / plan.cluster, t0 = tile % plan.tiles_m * BT, n0 = tile / plan.tiles_m * kBN;
+        const int rank = part_of_k(plan), share = BT / plan.cluster;
+        const int tile = blockIdx.x / ctas_a_tile(plan), t0 = tile % plan.tiles_m * BT;
+        const int n0 = tile / plan.tiles_m * kTileN + half * kBN;
         const int nt = min(BT, a.M - t0), i0 = threadIdx.x - 64;  // 16 threads a token, 8 columns each
         const int first = rank * share, last = min(nt, first + share);
         Finish fin(a, t0, warp >= 2 ? n0 + i0 % 16 * 8 : a.N);
@@ -500,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld16(tmem + tmem_lane_base(q) + c, r);
                 tmem_ld_wait();
                 const int to = c / share;
-                const uint32_t at = map_to_rank(slot + (uint32_t)(c - to * share) * (kBN * 4), to);
+                const uint32_t at = map_to_rank(slot + (uint32_t)(c - to * share) * (kBN * 4), kPair ? 2 * to + half : to);
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (e < step) st_cluster_f32(at + e * (kBN * 4), ok ? __uint_as_float(r[e]) : __int_as_float(0x7fc00000));
@@ -603,7 +620,7 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPair ? 2 : p.cluster;
+    attr[0].val.clusterDim.x = kPair ? 2 * p.cluster : p.cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kPair || p.cluster > 1 ? 1 : 0;
@@ -615,8 +632,8 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
 // The plan with the shortest estimate, in SM cycles.  What the parts were measured to take
 // (clock traces at M = 64, 333, 2048 and 4096, K = 1000 to 16384):
 //   a chunk of a tile   about 400 cycles for narrow tiles (waits and issue), 455 at 128 tokens,
-//                       600 at 256 (the MMAs alone: 512); or what it takes the card to bring
-//                       the weights for all CTAs at work, at 3500 bytes a cycle
+//                       600 at 256 (the MMAs alone: 512); all chunks together at least what
+//                       it takes the card to bring the weights, at 3500 bytes a cycle
 //   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
 //   a cluster's exchange  about 1000 cycles and 30 a token
 //   a chunk of a pair's tile  530 cycles
@@ -624,12 +641,14 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
 //                       the card's rate
 // E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
 // tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters;
-// 4096 x 7168 x 576: 40.9 us in pairs, 49.9 in runs; 4096 x 16384 x 7168: 510 us in pairs,
-// 587 in whole tiles of 128 x 256.  Over 32 shapes from 1 x 7168 x 576 up the choice was
-// within 12 % of the best plan timed, and within 4 % for all but five.
+// 256 x 16384 x 7168: 51.8 us in clusters of two pairs, 60.2 in clusters of two CTAs, 59.2 in
+// runs; 4096 x 7168 x 576: 40.9 us in pairs, 49.9 in runs; 4096 x 16384 x 7168: 482 to 510 us
+// in pairs, 587 in whole tiles of 128 x 256.  Over 35 shapes from 1 x 7168 x 576 up the choice
+// was within 12 % of the best plan timed, and within 5 % for all but four.
 LinearPlan linear_plan(int M, int K, int N, int sms) {
     Plan best{};
     double best_cost = 0.0;
+    const double weights = 2.0 * K * N / 3500.0;  // however they are dealt out
     for (int bt = 16; bt <= 256; bt *= 2) {
         if (bt > 16 && bt / 2 >= M) break;
         Plan p;
@@ -639,10 +658,14 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
         p.nk = (K + kBK - 1) / kBK;
         const long long tiles = (long long)p.tiles_m * p.tiles_n;
         if (tiles > (1ll << 28)) continue;
-        auto chunk = [&](double ctas) {
-            const double c = 390.0 + 0.5 * bt > 2.35 * bt ? 390.0 + 0.5 * bt : 2.35 * bt;
-            const double hbm = ctas / p.tiles_m * 16384 / 3500.0;
-            return c < hbm ? hbm : c;
+        const double chunk = 390.0 + 0.5 * bt > 2.35 * bt ? 390.0 + 0.5 * bt : 2.35 * bt;
+        // n tiles, `fit` at a time, each `cycles` long or what its share of the weights takes
+        auto waves_of = [&](long long n, long long fit, double cycles) {
+            auto wave = [&](long long at_work) {
+                const double w = weights * at_work / n;
+                return w > cycles ? w : cycles;
+            };
+            return n / fit * wave(fit) + (n % fit ? wave(n % fit) : 0.0);
         };
         auto keep = [&](double cost) {
             if (best.bt == 0 || cost < best_cost) {
@@ -661,17 +684,22 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
             if (fit < 1) break;
             const long long waves = (tiles + fit - 1) / fit;
             p.grid = p.cluster > 1 ? (int)tiles * p.cluster : tiles < sms ? (int)tiles : sms;
-            const double at_work = (double)(tiles < fit ? tiles : fit) * p.cluster;
-            keep(waves * ((p.nk + p.cluster - 1) / p.cluster * chunk(at_work)) + epilogue +
+            keep(waves_of(tiles, fit, (p.nk + p.cluster - 1) / p.cluster * chunk) + epilogue +
                  (p.cluster > 1 ? 1000.0 + 30.0 * bt + (waves - 1) * (epilogue + 3000.0) : 0.0));
         }
         p.cluster = 1;
         if (bt == 256) {
             p.pair = true;
             p.tiles_n = (N + 2 * kBN - 1) / (2 * kBN);
-            const long long pairs = (long long)p.tiles_m * p.tiles_n, fit = sms / 2;
-            p.grid = 2 * (int)(pairs < fit ? pairs : fit);
-            keep((pairs + fit - 1) / fit * (p.nk * 530.0) + epilogue + 1000.0);
+            const long long pairs = (long long)p.tiles_m * p.tiles_n;
+            for (p.cluster = 1; p.cluster <= 4; p.cluster *= 2) {
+                const int fit = p.cluster == 1 ? sms / 2 : p.cluster == 2 ? sms / 4 - 4 : sms / 8 - 5;
+                if (p.cluster > 1 && (p.nk < 2 * p.cluster || pairs > fit)) break;
+                p.grid = 2 * p.cluster * (int)(pairs < fit ? pairs : fit);
+                keep(waves_of(pairs, fit, (p.nk + p.cluster - 1) / p.cluster * 530.0) + epilogue + 1000.0 +
+                     (p.cluster > 1 ? 30.0 * bt : 0.0));
+            }
+            p.cluster = 1;
             p.pair = false;
             p.tiles_n = (N + kBN - 1) / kBN;
         }
@@ -682,8 +710,9 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
         // (4096 x 16384 x 7168: 611 us whole, 775 us in runs)
         if (tiles % p.grid == 0 || tiles >= 2 * sms) continue;
         p.whole = false;
-        keep((double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk(p.grid) + epilogue + 6000.0 +
-             4.0 * (p.grid < tiles ? 2.0 * p.grid : p.grid + tiles) * kBN * bt * 4 / 3500.0);
+        const double run = (double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk;
+        const double pieces = p.grid < tiles ? 2.0 * p.grid : p.grid + tiles;
+        keep((run > weights ? run : weights) + epilogue + 6000.0 + 4.0 * pieces * kBN * bt * 4 / 3500.0);
     }
     return best;
 }

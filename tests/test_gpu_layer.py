@@ -494,8 +494,10 @@ LINEAR_CASES = [
     (5000, 136, 1160, True, "gelu", True, 0, 0, 0),
     # pairs of CTAs: several rounds of tiles, the last ones cut by every edge; one round
     (5000, 1032, 6000, True, "silu", True, 8, 8, 8), (700, 2056, 6024, False, "none", True, 0, 0, 0),
-    # whole tiles over a little more than a wave, cut into runs
-    (8, 1000, 20480, True, "relu", True, 0, 8, 0), (150, 2048, 19464, False, "none", True, 0, 0, 0),
+    # clusters of two and of four pairs share K
+    (250, 8200, 7000, True, "gelu_tanh", True, 0, 8, 8), (1264, 6792, 416, False, "none", True, 8, 0, 0),
+    # tiles over a little more than a wave: whole, and cut into runs
+    (8, 1000, 20480, True, "relu", True, 0, 8, 0), (8, 4104, 20480, True, "silu", True, 8, 8, 0), (150, 2048, 19464, False, "none", True, 0, 0, 0),
 ]
 
 
@@ -552,7 +554,7 @@ def test_linear_in_place_on_the_residual_stream():
 
 def test_linear_repeats_bit_for_bit_with_a_dirty_workspace():
     g = gen(32)
-    for M, K, N in ((64, 16384, 1024), (333, 1000, 1544), (1, 8192, 264)):
+    for M, K, N in ((64, 16384, 1024), (333, 1000, 1544), (1, 8192, 264), (8, 4104, 20480)):
         x, w = randn(g, M, K).to(DEV), randn(g, K, N, std=K ** -0.5).to(DEV)
         ws = torch.full((mla.linear_workspace_size(M, K, N),), 0xFF, dtype=torch.uint8, device=DEV)
         a = mla.linear(x, w, workspace=ws)
@@ -832,7 +834,7 @@ def test_most_tokens_of_rope_and_store():
 def test_one_workspace_in_two_graphs():
     """Two captured products share a workspace: replayed one after another on a stream, each gives its own result."""
     g = gen(81)
-    M, K, N = 8, 1000, 20480  # cut along K, its pieces in the workspace
+    M, K, N = 8, 4104, 20480  # cut along K, its pieces in the workspace
     w = randn(g, K, N, std=K ** -0.5).to(DEV)
     xs = [randn(g, M, K).to(DEV) for _ in range(2)]
     ws = torch.empty(mla.linear_workspace_size(M, K, N), dtype=torch.uint8, device=DEV)

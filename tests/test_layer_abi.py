@@ -186,7 +186,7 @@ def test_linear_refusals(lib):
     assert lib.mla_linear(None, A, A, A, A, A, A, 0, NUL) == 1
     for name in ("x", "w", "out"):
         assert call(**{name: NUL}) == 1, name
-    runs = desc(M=8, K=1000, N=20480, xs=1000, os=20480)  # 160 tiles: cut along K, with pieces in the workspace
+    runs = desc(M=8, K=4104, N=20480, xs=4104, os=20480)  # 160 tiles: cut along K, with pieces in the workspace
     assert lib.mla_linear_workspace_size(ctypes.byref(runs)) > 256 and call(runs, ws=NUL) == 1
     for name in ("x", "w", "bias", "residual", "out", "ws"):
         assert call(**{name: ODD}) == 4, name
