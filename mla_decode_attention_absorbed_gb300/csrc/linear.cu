@@ -26,12 +26,13 @@
 // With many tokens a tile is 256 columns x 256 tokens on a pair of CTAs: one MMA of 256 x 256
 // x 16 over both, each holding half of both operands, so that an SM takes in 32 KB a chunk
 // instead of 48 (with the tokens as the MMA's rows, and rows written as they come or turned
-// over in bf16, 0 to 6 % slower).  Measured (device time): 4096 x 16384 x 7168 in 507 us = 1,897 TFLOP/s =
-// 0.98 of the measured bf16 rate (tiles of 128 x 256 on single CTAs: 560), bound by the tensor
-// cores; 64 x 16384 x 7168 in 39.7 us, 235 MB of weights at 5.9 TB/s = 0.88 of the measured copy
-// bandwidth, with 2 us of start and 4 of exchange and epilogue around the stream;
-// 333 x 1000 x 1544 in 7.6 us, a chain of latencies: 1.4 us to the first chunk, 16 chunks of
-// 0.21, 1.1 of epilogue.
+// over in bf16, 0 to 6 % slower).
+//
+// Measured (device time): 4096 x 16384 x 7168 in 507 us = 1,897 TFLOP/s = 0.98 of the measured
+// bf16 rate (tiles of 128 x 256 on single CTAs: 560), bound by the tensor cores; 64 x 16384 x
+// 7168 in 40 us, 235 MB of weights at 5.9 TB/s = 0.88 of the measured copy bandwidth, with 2 us
+// of start and 4 of exchange and epilogue around the stream; 333 x 1000 x 1544 in 7.6 us, a
+// chain of latencies: 1.4 us to the first chunk, 16 chunks of 0.21, 1.1 of epilogue.
 #include <atomic>
 
 #include "layer.h"

@@ -3,10 +3,11 @@
 //
 // Bound by memory: every value is read once and written once, 16 bytes an access; the
 // angles are worked out once a token (a CTA's, in shared memory) and serve all of its
-// heads.  8192 tokens x 128 heads x (128 + 64): 805 MB in 129.6 us = 6.21 TB/s = 0.915 of
-// the measured copy bandwidth with 128 rows a CTA (64 rows: 136.2, 256 rows: 131.6, loads
-// marked for early eviction: 133.7).  64 tokens x 128 heads take 3.3 us in groups of 16
-// rows (5.0 in groups of 128, on 64 of the 152 SMs): a launch and one memory round trip.
+// heads.  8192 tokens x 128 heads x (128 + 64): 805 MB in 118.1 us = 6.82 TB/s, the measured
+// copy bandwidth, with 128 rows a CTA and four copies under way a thread (one: 129.6, two:
+// 120.6, eight: 134.8, for their registers; with one, 64 rows a CTA: 136.2, 256: 131.6, loads
+// marked for early eviction: 133.7).  64 tokens x 128 heads take 3.1 us in groups of 16 rows
+// (5.0 in groups of 128, on 64 of the 152 SMs): a launch and one memory round trip.
 #include "layer.h"
 #include "rope.cuh"
 #include "sm100.cuh"
@@ -15,6 +16,7 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;
 constexpr int kMaxTokens = 64;  // tokens a CTA holds the angles of (16 KB)
 
 // i / d for i * d < 2^32 as one multiplication.
@@ -35,27 +37,44 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ int pos_s[kMaxTokens];
     const int t0 = blockIdx.x * tpb, h0 = blockIdx.y * hpb;
     const int nt = min(tpb, a.tokens - t0), nh = min(hpb, a.H - h0);
-    const int nf = a.d_rope / 2;
+    const int nf = a.d_rope / 2;  // at most 32
     auto position = [&](int t) {
         if (a.positions) return __ldg(a.positions + t);
         const long long p = (long long)__ldg(a.seq_lens + t / a.s_q) - a.s_q + t % a.s_q;
         return p < 0 ? -1 : (int)p;
     };
-    for (int i = threadIdx.x; i < nt * nf; i += kThreads) {
-        const int t = i / nf, f = i - t * nf;
-        const int pos = position(t0 + t);
-        cs[t * 32 + f] = rope_cos_sin(a.plan.turn[f], pos, a.plan.mscale, a.sign);
-        if (f == 0) pos_s[t] = pos;
+    // a warp takes every 8th token, a lane a pair; the positions of all of a warp's tokens are
+    // loaded at once (65536 keys of 64: 22.7 us one after another, 9.9 so)
+    constexpr int kW = kThreads / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (warp < nt) {
+        const int mine = warp + kW * lane < nt ? position(t0 + warp + kW * lane) : 0;
+        if (warp + kW * lane < nt) pos_s[warp + kW * lane] = mine;
+        const unsigned long long turn = lane < nf ? a.plan.turn[lane] : 0;
+        for (int t = warp, j = 0; t < nt; t += kW, ++j)
+            cs[t * 32 + lane] = rope_cos_sin(turn, __shfl_sync(~0u, mine, j), a.plan.mscale, a.sign);
     }
     __syncthreads();
     const int rows = nt * nh;
     const int cp = a.d_pass / 8, ir = a.d_rope / 16;
-    for (int i = threadIdx.x; i < rows * cp; i += kThreads) {
-        const int r = by_pass.div(i), c = i - r * cp;
-        const int t = by_heads.div(r), h = h0 + r - t * nh;
-        const uint4 v = *(reinterpret_cast<const uint4 *>(a.x + (t0 + t) * a.token_stride + h * a.head_stride) + c);
-        if (pos_s[t] >= 0)
-            *(reinterpret_cast<uint4 *>(a.pass_out + ((long long)(t0 + t) * a.H + h) * a.d_pass) + c) = v;
+    // kBatch loads before the first store, so that a thread has that many under way
+    for (int i0 = threadIdx.x; i0 < rows * cp; i0 += kBatch * kThreads) {
+        uint4 v[kBatch];
+        __nv_bfloat16 *dst[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * kThreads;
+            dst[j] = nullptr;
+            if (i < rows * cp) {
+                const int r = by_pass.div(i), c = i - r * cp;
+                const int t = by_heads.div(r), h = h0 + r - t * nh;
+                v[j] = *(reinterpret_cast<const uint4 *>(a.x + (t0 + t) * a.token_stride + h * a.head_stride) + c);
+                if (pos_s[t] >= 0) dst[j] = a.pass_out + ((long long)(t0 + t) * a.H + h) * a.d_pass + 8 * c;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (dst[j]) *reinterpret_cast<uint4 *>(dst[j]) = v[j];
     }
     // an item is 16 values, 8 pairs: two neighbouring 16-byte chunks, or one of each half
     const bool half = a.plan.layout == MLA_ROPE_HALF;
