@@ -638,8 +638,8 @@ cudaError_t launch_bt(const LinearArgs &a, const Plan &p, cudaStream_t st) {
 //   a tile's epilogue   1000 cycles and 36 a token; only the last one is not hidden
 //   a cluster's exchange  about 1000 cycles and 30 a token
 //   a chunk of a pair's tile  530 cycles
-//   the second kernel of runs  about 6000 cycles, and the pieces' bytes there and back at half
-//                       the card's rate
+//   the second kernel of runs  about 6000 cycles and 180 a piece of a tile, and the pieces'
+//                       bytes there and back at half the card's rate
 // E.g. 64 x 16384 x 7168: 40.3 us in clusters of 2, 43.7 in runs, 58.5 in whole tiles of 32
 // tokens; 333 x 1000 x 1544: 7.7 us in whole tiles of 32, 8.8 of 64, 12.7 in clusters;
 // 256 x 16384 x 7168: 51.8 us in clusters of two pairs, 60.2 in clusters of two CTAs, 59.2 in
@@ -679,9 +679,9 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
         p.whole = true;
         for (p.cluster = 1; p.cluster <= 8; p.cluster *= 2) {
             if (p.cluster > 1 && (p.nk < 2 * p.cluster || tiles > sms)) break;
-            // clusters that fit the SMs: fewer than an even share, as a cluster stays within
-            // one of the groups the SMs are built in
-            const int fit = p.cluster == 1 ? sms : p.cluster == 2 ? sms / 2 - 4 : p.cluster == 4 ? sms / 4 - 4 : sms / 8 - 5;
+            // clusters that fit the SMs: fewer than an even share (36 of 4, 15 of 8 on 152 SMs),
+            // as a cluster stays within one of the groups the SMs are built in
+            const int fit = p.cluster == 1 ? sms : p.cluster == 2 ? sms / 2 : p.cluster == 4 ? sms / 4 - 2 : sms / 8 - 4;
             if (fit < 1) break;
             const long long waves = (tiles + fit - 1) / fit;
             p.grid = p.cluster > 1 ? (int)tiles * p.cluster : tiles < sms ? (int)tiles : sms;
@@ -694,7 +694,7 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
             p.tiles_n = (N + 2 * kBN - 1) / (2 * kBN);
             const long long pairs = (long long)p.tiles_m * p.tiles_n;
             for (p.cluster = 1; p.cluster <= 4; p.cluster *= 2) {
-                const int fit = p.cluster == 1 ? sms / 2 : p.cluster == 2 ? sms / 4 - 4 : sms / 8 - 5;
+                const int fit = p.cluster == 1 ? sms / 2 : p.cluster == 2 ? sms / 4 - 2 : sms / 8 - 4;
                 if (p.cluster > 1 && (p.nk < 2 * p.cluster || pairs > fit)) break;
                 p.grid = 2 * p.cluster * (int)(pairs < fit ? pairs : fit);
                 keep(waves_of(pairs, fit, (p.nk + p.cluster - 1) / p.cluster * 530.0) + epilogue + 1000.0 +
@@ -713,7 +713,8 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
         p.whole = false;
         const double run = (double)((tiles * p.nk + p.grid - 1) / p.grid) * chunk;
         const double pieces = p.grid < tiles ? 2.0 * p.grid : p.grid + tiles;
-        keep((run > weights ? run : weights) + epilogue + 6000.0 + 4.0 * pieces * kBN * bt * 4 / 3500.0);
+        keep((run > weights ? run : weights) + epilogue + 6000.0 + 180.0 * p.grid / tiles +
+             4.0 * pieces * kBN * bt * 4 / 3500.0);
     }
     return best;
 }

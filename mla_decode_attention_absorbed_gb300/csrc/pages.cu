@@ -11,8 +11,8 @@
 //
 // A step of 64 requests takes 2.9 us and a turn of 512 (1,300 tokens) 4.0: a launch, the
 // lengths, the sums, and one round trip for the pages.  8,191 requests with 2.9 M tokens'
-// entries take 18.5 us against 3.5 for the 24 MB it writes: 5 us for the sums, that every CTA
-// repeats, the rest for finding requests and pages, a few one after another in every warp.
+// entries take 19 us against 3.5 for the 24 MB it writes: 5 us for the sums, that every CTA
+// repeats, the rest for finding requests and pages: bound by instructions.
 #include "layer.h"
 
 namespace mla {
@@ -132,58 +132,26 @@ __device__ __forceinline__ int page_at(const PagesArgs &a, const Ring &ring, con
     return -1;
 }
 
-// Position and slot of token k < total.tokens, by itself.
-__device__ __forceinline__ void one_token(const PagesArgs &a, const Ring &ring, const Sums *first, int groups, int per, int k) {
-    int b, pos = -1, slot = -1;
+// A thread's place among the tokens: a request, and in it tokens [begin, end) that lie in one
+// page (or the rest of a request that is not served, or what lies behind the last token:
+// pos -1).
+struct TokenRun {
+    int b, begin, end, pos, slot;
     Sums before;
-    const Request r = find_request<&Sums::tokens>(a, first, groups, per, k, b, before);
-    if (served(a, ring, r, add(before, r.n))) {
-        pos = r.old_len + (k - before.tokens);
-        const int col = div_units(a, pos >> 6), row = pos - col * a.page_size;
-        const int page = page_at(a, ring, r, before, b, col);
-        if (page >= 0) slot = page * a.page_size + row;
-    }
-    a.positions[k] = pos;
-    a.slots[k] = slot;
-}
-
-// A warp's tokens [k, end): quads of tokens a lane, f(token, pos, slot) giving each token's
-// values; quads that lie inside are stored as 16 bytes where `wide` allows.
-template <class F>
-__device__ __forceinline__ void store_tokens(const PagesArgs &a, int k, int end, int lane, bool wide, F f) {
-    const int quad0 = k & ~3;
-    for (int i = 0; quad0 + 128 * i < end; ++i) {  // whole warps go round: f may shuffle
-        const int t = quad0 + 128 * i + 4 * lane;
-        int pos[4], slot[4];
-        f(t, pos, slot);
-        if (wide && t >= k && t + 4 <= end) {
-            *reinterpret_cast<int4 *>(a.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            *reinterpret_cast<int4 *>(a.slots + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t + e >= k && t + e < end) {
-                    a.positions[t + e] = pos[e];
-                    a.slots[t + e] = slot[e];
-                }
-        }
-    }
-}
-
-// A warp's tokens [k, k1) of many: request after request, a request's pages loaded 32 at a
-// time, one a lane; where requests are shorter than a warp, 32 tokens each by itself.
-__device__ __forceinline__ void many_tokens(const PagesArgs &a, const Ring &ring, const Sums *first, int groups, int per,
-                                            const Sums &total, int k, int k1, int lane) {
-    const bool wide = (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15) == 0;
-    auto none = [](int, int (&pos)[4], int (&slot)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pos[e] = slot[e] = -1;
-    };
-    int b = -1;
     Request r;
-    Sums before;
-    while (k < min(k1, total.tokens)) {
-        // the request that holds k: one of the next few, else by bisection
+
+    __device__ __forceinline__ TokenRun() : b(-1), begin(0), end(0), pos(-1), slot(-1) {}
+
+    // moves on to the run of token k (not before the last one asked for)
+    __device__ __forceinline__ void to(const PagesArgs &a, const Ring &ring, const Sums *first, int groups, int per, int total,
+                                       int k) {
+        begin = k;
+        pos = slot = -1;
+        if (k >= total) {
+            end = kBig;
+            return;
+        }
+        // the same request, one of the next few, else by bisection
         for (int steps = 0; b >= 0 && sat_add(before.tokens, r.n.tokens) <= k; ++steps) {
             if (steps == 4 || b + 1 >= a.B) {
                 b = -1;
@@ -193,48 +161,17 @@ __device__ __forceinline__ void many_tokens(const PagesArgs &a, const Ring &ring
             }
         }
         if (b < 0) r = find_request<&Sums::tokens>(a, first, groups, per, k, b, before);
-        const int end = min(k1, sat_add(before.tokens, r.n.tokens));
-        if (end - k < 32 && end < k1) {
-            const int last = min(min(k1, total.tokens), k + 32);
-            if (k + lane < last) one_token(a, ring, first, groups, per, k + lane);
-            k = last;
-            __syncwarp();
-            continue;
-        }
-        if (!served(a, ring, r, add(before, r.n))) {
-            store_tokens(a, k, end, lane, wide, none);
-            k = end;
-            continue;
-        }
-        while (k < end) {
-            const int pos0 = r.old_len + (k - before.tokens);
-            const int col0 = div_units(a, pos0 >> 6), row0 = pos0 - col0 * a.page_size;
-            // tokens of the request in these 32 pages; page_size <= 2^30, so 64 bits for the bound
-            const int stop = (int)min((long long)end, k + 32ll * a.page_size - row0);
-            const int col1 = div_units(a, (pos0 + (stop - k) - 1) >> 6);
-            const int mine = col0 + lane <= col1 ? page_at(a, ring, r, before, b, col0 + lane) : -1;
-            const int k0 = k;
-            store_tokens(a, k, stop, lane, wide, [&](int t, int (&pos)[4], int (&slot)[4]) {
-                // rows counted from the first page's beginning; a quad lies in one page or two
-                const int from = max(t - k0, -3) + row0;
-                const int page = from < 0 ? 0 : min(div_units(a, from >> 6), 31);
-                const int id0 = __shfl_sync(~0u, mine, page), id1 = __shfl_sync(~0u, mine, min(page + 1, 31));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = from + e - page * a.page_size;
-                    const bool over = row >= a.page_size;
-                    const int id = over ? id1 : id0;
-                    pos[e] = pos0 + (t - k0) + e;
-                    slot[e] = id < 0 ? -1 : id * a.page_size + (over ? row - a.page_size : row);
-                }
-            });
-            k = stop;
-        }
+        end = sat_add(before.tokens, r.n.tokens);
+        if (!served(a, ring, r, add(before, r.n))) return;
+        pos = r.old_len + (k - before.tokens);
+        const int col = div_units(a, pos >> 6), row = pos - col * a.page_size;
+        end = min(end, k + a.page_size - row);
+        const int page = page_at(a, ring, r, before, b, col);
+        if (page >= 0) slot = page * a.page_size + row;
     }
-    if (k < k1) store_tokens(a, k, k1, lane, wide, none);
-}
+};
 
-__global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ PagesArgs a, int per, int many) {
+__global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ PagesArgs a, int per, int quads) {
     __shared__ Sums first[kGroups];
     __shared__ Sums warp_sums[32];
     __shared__ Sums total_s;
@@ -328,23 +265,41 @@ __global__ void __launch_bounds__(kGroups) pages_update(const __grid_constant__ 
         a.ring[ring_at(a, tail, k)] = a.table[(long long)b * a.max_pages + r.has + (k - before.given)];
     }
 
-    if (!many) {
-        const int third = gsize / 3;
-        for (int k = gid - third >= 0 ? gid - third : gid - third + gsize; k < a.max_tokens; k += gsize) {
-            if (k < total.tokens) {
-                one_token(a, ring, first, groups, per, k);
-            } else {
-                a.positions[k] = -1;
-                a.slots[k] = -1;
-            }
+    TokenRun run_of;
+    if (!quads) {
+        for (int k = gid - gsize / 3 >= 0 ? gid - gsize / 3 : gid - gsize / 3 + gsize; k < a.max_tokens; k += gsize) {
+            run_of.to(a, ring, first, groups, per, total.tokens, k);
+            a.positions[k] = run_of.pos;
+            a.slots[k] = run_of.slot;
         }
         return;
     }
-    // many tokens: a warp has a contiguous run of 128-token chunks
+    // Four neighbours a thread, a warp's in a contiguous run of 128-token chunks, so that a
+    // thread walks on where it is.
+    const bool wide = (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15) == 0;
     const int warps = gsize / 32, w = gid / 32;
-    const long long chunks = ((long long)a.max_tokens + 127) / 128;
-    many_tokens(a, ring, first, groups, per, total, (int)(chunks * w / warps * 128),
-                (int)min((long long)a.max_tokens, chunks * (w + 1) / warps * 128), lane);
+    const long long chunks = ((long long)a.max_tokens + 127) / 128, c1 = chunks * (w + 1) / warps;
+    for (long long c = chunks * w / warps; c < c1; ++c) {
+        const long long k0 = c * 128 + lane * 4;
+        const int k1 = (int)min(k0 + 4, (long long)a.max_tokens);
+#pragma unroll 1
+        for (int k = (int)k0, n; k < k1; k += n) {
+            if (k >= run_of.end) run_of.to(a, ring, first, groups, per, total.tokens, k);
+            n = min(k1, run_of.end) - k;
+            const int dp = run_of.pos >= 0 ? 1 : 0, ds = run_of.slot >= 0 ? 1 : 0;  // -1 stays
+            const int pos = run_of.pos + dp * (k - run_of.begin), slot = run_of.slot + ds * (k - run_of.begin);
+            if (n == 4 && wide) {
+                *reinterpret_cast<int4 *>(a.positions + k) = make_int4(pos, pos + dp, pos + 2 * dp, pos + 3 * dp);
+                *reinterpret_cast<int4 *>(a.slots + k) = make_int4(slot, slot + ds, slot + 2 * ds, slot + 3 * ds);
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < n; ++e) {
+                    a.positions[k + e] = pos + e * dp;
+                    a.slots[k + e] = slot + e * ds;
+                }
+            }
+        }
+    }
 }
 
 }  // namespace
@@ -355,14 +310,15 @@ cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t st) {
     const int groups = (a.B + per - 1) / per;
     // Enough threads for the groups' sums.  Few tokens: one a thread, on at least 12 CTAs, so
     // that the items' loads run side by side (512 requests, 1,300 tokens: 10.8 us on one CTA,
-    // 8.4 on 3, 7.4 on 12).  Many: by warps (see many_tokens).
+    // 8.4 on 3, 7.4 on 12).  Many, more than two rounds of that: four a thread (7,929 requests,
+    // 0.7 M tokens: 15.1 us, one a thread 21.0; 2,997 and 0.1 M: 9.2 us, one a thread 7.2).
     int threads = groups > 0 ? (groups + 31) / 32 * 32 : 32;
     if (threads < 256 && a.max_tokens > threads) threads = 256;
     const int sms = layer_num_sms();
-    const int many = a.max_tokens > sms * threads ? 1 : 0;
+    const int quads = a.max_tokens / 2 > sms * threads ? 1 : 0;
     const long long want = ((long long)a.max_tokens + threads - 1) / threads;
     const int grid = want < 12 ? 12 : want > sms ? sms : (int)want;
-    pages_update<<<grid, threads, 0, st>>>(a, per, many);
+    pages_update<<<grid, threads, 0, st>>>(a, per, quads);
     return cudaGetLastError();
 }
 
