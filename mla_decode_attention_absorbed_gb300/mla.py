@@ -437,6 +437,8 @@ def read_status(workspace, stream=None) -> int:
 # These calls take a few microseconds on the GPU, so what a call costs on the host counts: every
 # property of a tensor is read once, without further calls, and pointers and streams go to ctypes
 # as plain integers.
+# Tensors that a call with ``stream=`` makes belong to that stream, as if the call stood under
+# ``torch.cuda.stream(stream)``; inputs from another stream are the caller's to order.
 _BF16, _I32 = torch.bfloat16, torch.int32
 _ERR_WORKSPACE = 5  # MLA_ERR_WORKSPACE
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -489,7 +491,20 @@ def _rows(t, what: str, dev: int, M: int, N: int) -> int:
 
 
 def _raw_stream(dev: int, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream must be one of device {dev}, not of {stream.device}")
+    return stream.cuda_stream
+
+
+def _new(shape, stride, dtype, stream):
+    """A tensor for kernels on ``stream`` (None: the current one), from that stream's memory: what was freed there is
+    handed out again in the order of that stream's work alone."""
+    if stream is None:
+        return _empty_strided_cuda(shape, stride, dtype)
+    with torch.cuda.stream(stream):
+        return _empty_strided_cuda(shape, stride, dtype)
 
 
 def rope_plan(d_rope: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0, scaling: int = ROPE_PLAIN,
@@ -531,14 +546,14 @@ def rope(prob: Problem, plan: RopePlan, x, positions=None, seq_lens=None, q_nope
     nope = None
     if split:
         if q_nope is None:
-            q_nope = _empty_strided_cuda((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), _BF16)
+            q_nope = _new((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), _BF16, stream)
             nope = q_nope.data_ptr()
         else:
             nope = _dense(q_nope, "q_nope", _BF16, dev, (B, s_q, H, d_nope))
     elif q_nope is not None:
         raise ValueError("rows of d_rope values have no part for q_nope")
     if q_rope is None:
-        q_rope = _empty_strided_cuda((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), _BF16)
+        q_rope = _new((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), _BF16, stream)
         turned = q_rope.data_ptr()
     else:
         turned = _dense(q_rope, "q_rope", _BF16, dev, (B, s_q, H, d_rope))
@@ -597,11 +612,11 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
     word = None if status is None else _word(status, dev)
     if out is None:
         one = (1,)
-        lens = _empty_strided_cuda((B,), one, _I32)
-        state_out = _empty_strided_cuda((2,), one, _I32)
-        start = _empty_strided_cuda((B + 1,), one, _I32)
-        pos = _empty_strided_cuda((max_tokens,), one, _I32)
-        slot = _empty_strided_cuda((max_tokens,), one, _I32)
+        lens = _new((B,), one, _I32, stream)
+        state_out = _new((2,), one, _I32, stream)
+        start = _new((B + 1,), one, _I32, stream)
+        pos = _new((max_tokens,), one, _I32, stream)
+        slot = _new((max_tokens,), one, _I32, stream)
         out = PagesStep(lens, state_out, start, pos, slot)
         lens, state_out, start = lens.data_ptr(), state_out.data_ptr(), start.data_ptr()
         pos, slot = pos.data_ptr(), slot.data_ptr()
@@ -661,7 +676,7 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
     b = None if bias is None else _dense(bias, "bias", _BF16, dev, (N,))
     res = None if residual is None else _rows(residual, "residual", dev, M, N)
     if out is None:
-        out = _empty_strided_cuda((M, N), (N, 1), _BF16)
+        out = _new((M, N), (N, 1), _BF16, stream)
         to, out_stride = out.data_ptr(), N
     else:
         to, out_stride = _rows(out, "out", dev, M, N), out.stride(0)
@@ -676,7 +691,7 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
         code = lib.mla_linear(at, rows, weight, b, res, to, None, 256, st)
         if code == _ERR_WORKSPACE:
             nbytes = lib.mla_linear_workspace_size(at)
-            workspace = _empty_strided_cuda((nbytes,), (1,), torch.uint8)
+            workspace = _new((nbytes,), (1,), torch.uint8, stream)
             code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), nbytes, st)
     if code:
         raise MLAError(code, "mla_linear")

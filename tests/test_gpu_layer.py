@@ -850,3 +850,49 @@ def test_one_workspace_in_two_graphs():
         outs[i].zero_()
         graphs[i].replay()
         assert torch.equal(outs[i], want[i])
+
+
+# ------------------------------------------------------------------------------------------------- a stream as an argument
+def test_stream_argument_while_the_current_stream_allocates():
+    """linear(stream=s) of a shape that is cut into runs, held up on s, while the current stream takes and fills buffers
+    of the workspace's and of the output's size: neither side writes into the other's memory."""
+    g = gen(101)
+    M, K, N = 8, 4104, 20480
+    x, w = randn(g, M, K).to(DEV), randn(g, K, N, std=K ** -0.5).to(DEV)
+    nbytes = mla.linear_workspace_size(M, K, N)
+    assert nbytes > 256
+    want = mla.linear(x, w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        got = [mla.linear(x, w, stream=s) for _ in range(3)]
+        taken = [torch.full((n,), 0x7F, dtype=torch.uint8, device=DEV) for n in (nbytes, nbytes, 2 * M * N)]
+        for _ in range(20):
+            for t in taken:
+                t.fill_(0x7F)
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for y in got)
+        assert all(bool((t == 0x7F).all()) for t in taken)
+        del got, taken
+
+
+def test_tensors_made_for_a_stream_belong_to_it():
+    """Outputs that rope, pages_update and linear make under stream= come from that stream's memory."""
+    s = torch.cuda.Stream()
+    prob, plan = problem(2, 4, 1, d_rope=32, d_nope=64), mla.rope_plan(32)
+    q = torch.zeros(2, 1, 4, 96, dtype=BF16, device=DEV)
+    lens = torch.ones(2, dtype=I32, device=DEV)
+    pages, state = mla.Pages.empty(2, 4, 8)
+    x, w = torch.zeros(4, 64, dtype=BF16, device=DEV), torch.zeros(64, 128, dtype=BF16, device=DEV)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    made = [*mla.rope(prob, plan, q, seq_lens=lens, stream=s), mla.linear(x, w, stream=s)]
+    up = mla.pages_update(pages, state, lens, lens + 1, 2, stream=s)
+    made += [up.seq_lens, up.ring_state, up.token_start, up.positions, up.slots]
+    torch.cuda.synchronize()
+    segments = torch.cuda.memory_snapshot()
+    for t in made:
+        at = [seg for seg in segments if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]]
+        assert len(at) == 1 and at[0]["stream"] == s.cuda_stream

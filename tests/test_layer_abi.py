@@ -211,3 +211,13 @@ def test_linear_workspace_stays_bounded(lib):
         for K in (8, 64, 1000, 16384):
             for N in (8, 136, 7168, 65536):
                 assert 0 < mla.linear_workspace_size(M, K, N) <= 2 * 152 * 128 * 256 * 4, (M, K, N)
+
+
+# ---------------------------------------------------------------------------------------------------------- python
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device_index, device, cuda_stream = 1, "cuda:1", 0x1234
+
+    assert mla._raw_stream(1, Stream()) == 0x1234
+    with pytest.raises(ValueError):
+        mla._raw_stream(0, Stream())
