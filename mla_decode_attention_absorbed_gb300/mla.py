@@ -175,6 +175,7 @@ def _stream(stream=None):
 @dataclass
 class Problem:
     """Sizes of one decode step (mirrors ``mla_dims``)."""
+    __slots__ = ("__dict__", "__weakref__", "_kept")  # _kept: what dims_ref() made, beside the fields
     B: int
     H: int
     s_q: int
@@ -184,19 +185,17 @@ class Problem:
     d_v: int
     scale: float
 
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        self.__dict__.pop("_dims_kept", None)  # the structure below follows the fields
-
     def __getstate__(self):  # copies and pickles take the fields alone
-        return {f: v for f, v in self.__dict__.items() if f != "_dims_kept"}
+        return dict(self.__dict__)
 
     def dims_ref(self):
         """A reference to ``dims()`` for ctypes, made once until a field changes."""
-        ref = self.__dict__.get("_dims_kept")
-        if ref is None:
-            ref = self.__dict__["_dims_kept"] = ctypes.byref(self.dims())
-        return ref
+        kept = getattr(self, "_kept", None)
+        if kept is None or kept[0] != self.__dict__:
+            # made from one snapshot and kept with it: a field set meanwhile shows at the next call
+            seen = dict(self.__dict__)
+            kept = self._kept = seen, ctypes.byref(Dims(*[float(seen[n]) if n == "scale" else seen[n] for n, _ in Dims._fields_]))
+        return kept[1]
 
     def dims(self) -> Dims:
         return Dims(self.B, self.H, self.s_q, self.d_c, self.d_rope, self.d_nope, self.d_v, float(self.scale))

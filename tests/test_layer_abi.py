@@ -2,8 +2,10 @@
 host, before anything is launched, and the rotation's frequencies.  No GPU needed."""
 import copy
 import ctypes
+import dataclasses
 import math
 import pickle
+import weakref
 
 import pytest
 
@@ -37,6 +39,33 @@ def test_problem_keeps_its_structure_up_to_date():
     p.B, q.H, r.scale = 7, 3, 0.25
     assert (seen(p).B, seen(p).H) == (7, 16) and (seen(q).B, seen(q).H) == (4, 3) and seen(r).scale == 0.25
     assert s == mla.Problem(4, 16, 1, 512, 64, 128, 128, 0.5) and seen(s).scale == 0.5
+
+
+def test_problem_holds_its_fields_alone():
+    """What dims_ref() keeps is no field: vars() and copies by them are the sizes, before and after a call."""
+    p = mla.Problem(4, 16, 1, 512, 64, 128, 128, 0.5)
+    fields = dict(B=4, H=16, s_q=1, d_c=512, d_rope=64, d_nope=128, d_v=128, scale=0.5)
+    assert vars(p) == fields and p.dims_ref() is not None and vars(p) == fields
+    assert mla.Problem(**vars(p)) == p and dataclasses.replace(p, B=2).dims().B == 2 and weakref.ref(p)() is p
+    vars(p)["B"] = 3
+    assert ctypes.cast(p.dims_ref(), ctypes.POINTER(mla.Dims)).contents.B == 3
+
+
+def test_problem_field_set_while_another_thread_makes_the_structure(monkeypatch):
+    """A field set between the structure's making and its keeping (as by another thread): the next call sees it."""
+    p = mla.Problem(4, 16, 1, 512, 64, 128, 128, 0.5)
+    make = mla.Dims
+
+    class Interrupted(make):
+        def __init__(self, *values):
+            super().__init__(*values)
+            if p.B == 4:
+                p.B = 7
+
+    with monkeypatch.context() as m:
+        m.setattr(mla, "Dims", Interrupted)
+        p.dims_ref()
+    assert ctypes.cast(p.dims_ref(), ctypes.POINTER(make)).contents.B == 7
 
 
 # ------------------------------------------------------------------------------------------------------------- rope
