@@ -685,7 +685,9 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
         desc = LinearDesc(M, K, N, act, K, N, N)
     at, weight, st = ctypes.byref(desc), w.data_ptr(), _raw_stream(dev, stream)
     if workspace is not None:
-        code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), workspace.numel(), st)
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(workspace, "workspace", f"dense memory on device {dev}")
+        code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), workspace.nbytes, st)
     else:  # most shapes need none
         code = lib.mla_linear(at, rows, weight, b, res, to, None, 256, st)
         if code == _ERR_WORKSPACE:

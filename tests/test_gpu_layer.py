@@ -896,3 +896,20 @@ def test_tensors_made_for_a_stream_belong_to_it():
     for t in made:
         at = [seg for seg in segments if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]]
         assert len(at) == 1 and at[0]["stream"] == s.cuda_stream
+
+
+# ------------------------------------------------------------------------------------------------------ more refusals
+def test_linear_refuses_a_workspace_it_cannot_use():
+    """On the host or strided it is refused before anything is launched; its size counts in bytes, whatever its type."""
+    g = gen(111)
+    M, K, N = 8, 4104, 20480
+    x, w = randn(g, M, K).to(DEV), randn(g, K, N, std=K ** -0.5).to(DEV)
+    need = mla.linear_workspace_size(M, K, N)
+    for bad in (torch.empty(need, dtype=torch.uint8), torch.empty(2 * need, dtype=torch.uint8, device=DEV)[::2],
+                torch.empty(2, need, dtype=torch.uint8, device=DEV).t()):
+        with pytest.raises(ValueError):
+            mla.linear(x, w, workspace=bad)
+    words = torch.empty((need + 3) // 4, dtype=torch.float32, device=DEV)
+    assert torch.equal(mla.linear(x, w, workspace=words), mla.linear(x, w))
+    with pytest.raises(mla.MLAError):
+        mla.linear(x, w, workspace=words[:-64])

@@ -8,6 +8,7 @@ import pickle
 import weakref
 
 import pytest
+import torch
 
 from mla_decode_attention_absorbed_gb300 import build, mla
 from oracle import layer
@@ -250,3 +251,30 @@ def test_a_stream_of_another_device_is_refused():
     assert mla._raw_stream(1, Stream()) == 0x1234
     with pytest.raises(ValueError):
         mla._raw_stream(0, Stream())
+
+
+class OnDevice:
+    """A CPU tensor that says it lies on a device: for checks that end before a pointer is used."""
+
+    def __init__(self, t, dev=0):
+        self.t, self.dev = t, dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.dev
+
+
+@pytest.fixture
+def device0(monkeypatch):
+    monkeypatch.setattr(mla, "_current_device", lambda: 0)
+    monkeypatch.setattr(mla, "_raw_stream", lambda dev, stream: 0)
+
+
+def test_linear_checks_its_workspace(lib, device0):
+    x, w, out = (OnDevice(torch.zeros(*n, dtype=torch.bfloat16)) for n in ((8, 64), (64, 128), (8, 128)))
+    for ws in (OnDevice(torch.zeros(512, dtype=torch.uint8), -1), OnDevice(torch.zeros(512, dtype=torch.uint8), 1),
+               OnDevice(torch.zeros(1024, dtype=torch.uint8)[::2])):
+        with pytest.raises(ValueError, match="workspace"):
+            mla.linear(x, w, out=out, workspace=ws)
