@@ -604,7 +604,11 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
     lib = _lib or load()
     table, ring = pages.block_table, pages.free_ring
     dev = _device(table, "block_table")
+    # the fields may have been assigned since the batch was made
+    if table.dim() != 2 or ring.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages], free_ring [num_pages]")
     B, max_pages = table.shape
+    to_table, to_ring = _dense(table, "block_table", _I32, dev, table.shape), _dense(ring, "free_ring", _I32, dev, ring.shape)
     state = _dense(ring_state, "ring_state", _I32, dev, (2,))
     old = _dense(old_lens, "old_lens", _I32, dev, (B,))
     new = _dense(new_lens, "new_lens", _I32, dev, (B,))
@@ -625,7 +629,7 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
         start = _dense(out.token_start, "token_start", _I32, dev, (B + 1,))
         pos = _dense(out.positions, "positions", _I32, dev, (max_tokens,))
         slot = _dense(out.slots, "slots", _I32, dev, (max_tokens,))
-    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], table.data_ptr(), ring.data_ptr(), state, state_out)
+    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], to_table, to_ring, state, state_out)
     code = lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, lens, start, pos, slot, word,
                                 _raw_stream(dev, stream))
     if code:

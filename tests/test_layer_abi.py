@@ -278,3 +278,18 @@ def test_linear_checks_its_workspace(lib, device0):
                OnDevice(torch.zeros(1024, dtype=torch.uint8)[::2])):
         with pytest.raises(ValueError, match="workspace"):
             mla.linear(x, w, out=out, workspace=ws)
+
+
+def test_pages_update_checks_fields_assigned_later(lib, device0):
+    i32 = lambda *n: OnDevice(torch.zeros(*n, dtype=torch.int32))  # noqa: E731
+    table, ring, lens = i32(2, 4), i32(8), i32(2)
+    bad = [("free_ring", r) for r in (OnDevice(ring.t.long()), OnDevice(ring.t, -1), OnDevice(ring.t, 1),
+                                      OnDevice(torch.zeros(16, dtype=torch.int32)[::2]), i32(2, 4))]
+    bad += [("block_table", t) for t in (OnDevice(table.t.long()), OnDevice(table.t, -1), i32(8),
+                                         OnDevice(torch.zeros(4, 2, dtype=torch.int32).t()))]
+    out = mla.PagesStep(i32(2), i32(2), i32(3), i32(4), i32(4))
+    for name, value in bad:
+        pages = mla.Pages(table, ring, 64)
+        setattr(pages, name, value)
+        with pytest.raises(ValueError):
+            mla.pages_update(pages, i32(2), lens, i32(2), 4, out=out)
