@@ -315,11 +315,12 @@ MLA_API int mla_decode_attn_noalloc(const mla_dims *dims, const void *q_cat, con
 /* Diagnostics (the pages have no counterpart): the bound, in nanoseconds, of
  * every wait for work inside the attention kernels launched from now on by this
  * process (mla_decode_attn, mla_decode_step, the sparse, prefill and no-alloc
- * entry points).  A wait that runs out records MLA_ERR_TIMEOUT in the status
- * word; the kernel then drains the copies and MMAs it has in flight (those waits
- * keep the default bound) and returns, outputs undefined.  0 restores the
- * default, 2 s.  For tests of the timeout path and for diagnosing a stalled GPU;
- * not for production use.  Always returns MLA_OK. */
+ * entry points) and mla_linear.  A wait that runs out records MLA_ERR_TIMEOUT in
+ * the status word; the kernel then drains the copies and MMAs it has in flight
+ * (those waits keep the default bound) and returns, outputs undefined (those of
+ * mla_linear NaN or right).  0 restores the default, 2 s.  For tests of the timeout
+ * path and for diagnosing a stalled GPU; not for production use.  Always returns
+ * MLA_OK. */
 MLA_API int mla_set_wait_limit_ns(unsigned long long ns);
 
 /* One whole absorbed decode step: mla_absorb_q -> mla_decode_attn ->
@@ -557,9 +558,14 @@ MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *desc);
  * residual itself (with its stride).  A workspace serves one call at a time: calls
  * that may overlap on the GPU need one each.  Results do not depend on the timing
  * of the GPU.  A bounded device wait that runs out leaves NaN in the outputs it
- * concerns. */
+ * concerns; mla_linear_status records it, too. */
 MLA_API int mla_linear(const mla_linear_desc *desc, const void *x, const void *w, const void *bias,
                        const void *residual, void *out, void *workspace, size_t ws_bytes, void *stream);
+
+/* The same with this section's status word: MLA_ERR_TIMEOUT where a wait ran out. */
+MLA_API int mla_linear_status(const mla_linear_desc *desc, const void *x, const void *w, const void *bias,
+                              const void *residual, void *out, void *workspace, size_t ws_bytes, int *status,
+                              void *stream);
 
 #ifdef __cplusplus
 }

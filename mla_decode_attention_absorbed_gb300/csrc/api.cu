@@ -13,8 +13,7 @@ namespace {
 
 constexpr int kAbiVersion = 2;
 constexpr int kMaxSplits = 64;
-// Bound of the attention kernels' waits for work, set by mla_set_wait_limit_ns
-// (0: the kernels' default).
+// Bound of the kernels' waits for work, set by mla_set_wait_limit_ns (0: their default).
 std::atomic<unsigned long long> g_wait_ns{0};
 
 // SMs of the current device (split planning only), looked up once per device
@@ -408,6 +407,12 @@ size_t naive_cuda_core_bytes(const mla_dims *d, const mla_cache *c) {
 }
 
 }  // namespace
+
+namespace mla {
+
+unsigned long long wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+
+}  // namespace mla
 
 extern "C" {
 

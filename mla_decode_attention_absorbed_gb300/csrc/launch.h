@@ -7,6 +7,9 @@
 
 namespace mla {
 
+// Bound of the kernels' waits for work as mla_set_wait_limit_ns left it (0: their default).
+unsigned long long wait_limit_ns();
+
 // trigger: let the next grid (launched programmatically) start its CTAs at once;
 // wait_prev: this grid is launched programmatically after the attention and
 // reads o_lat only once that grid has completed.

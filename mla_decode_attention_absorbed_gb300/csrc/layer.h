@@ -53,6 +53,8 @@ struct LinearArgs {
     __nv_bfloat16 *out;
     long long x_stride, out_stride, residual_stride;
     float *part;  // workspace: fp32 tiles of the pieces of tiles that are cut along K
+    int *status;
+    unsigned long long wait_ns;  // bound of the waits for work
 };
 // How a product is cut (see linear.cu).
 struct LinearPlan {

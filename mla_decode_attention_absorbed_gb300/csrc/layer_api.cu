@@ -6,6 +6,7 @@
 
 #include <atomic>
 
+#include "launch.h"
 #include "layer.h"
 
 namespace mla {
@@ -27,6 +28,7 @@ namespace {
 
 constexpr int kMaxTokens = 65535 * 128;
 constexpr int kMaxWidth = 1 << 20;
+constexpr unsigned long long kWaitNs = 2000000000ull;  // bound of mla_linear's waits for work unless one is set
 
 bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -280,6 +282,12 @@ MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *d) {
 
 MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, const void *bias, const void *residual,
                        void *out, void *workspace, size_t ws_bytes, void *stream) {
+    return mla_linear_status(d, x, w, bias, residual, out, workspace, ws_bytes, nullptr, stream);
+}
+
+MLA_API int mla_linear_status(const mla_linear_desc *d, const void *x, const void *w, const void *bias,
+                              const void *residual, void *out, void *workspace, size_t ws_bytes, int *status,
+                              void *stream) {
     int s = check_linear(d, residual != nullptr);
     if (s) return s;
     if (!aligned(workspace, 16)) return MLA_ERR_ALIGN;
@@ -289,7 +297,8 @@ MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, c
     if (ws_bytes < need) return MLA_ERR_WORKSPACE;
     if (!workspace && need > 256) return MLA_ERR_NULL;
     if (!x || !w || !out) return MLA_ERR_NULL;
-    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16))
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16) ||
+        !aligned(status, 4))
         return MLA_ERR_ALIGN;
     if (out == x || out == w || (out == residual && d->M > 1 && d->out_stride != d->residual_stride))
         return MLA_ERR_UNSUPPORTED;
@@ -307,6 +316,9 @@ MLA_API int mla_linear(const mla_linear_desc *d, const void *x, const void *w, c
     a.out_stride = d->out_stride;
     a.residual_stride = d->residual_stride;
     a.part = (float *)workspace;
+    a.status = status;
+    const unsigned long long ns = mla::wait_limit_ns();
+    a.wait_ns = ns == 0 ? kWaitNs : ns < (1ull << 61) ? ns : 1ull << 61;  // twice that are cycles
     return result(mla::launch_linear(a, plan, as_stream(stream)));
 }
 

@@ -226,30 +226,29 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Bounded wait that also ends when another warp of the CTA gave up.
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    const long long c0 = clock64();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 15u) == 0 && (*abort_flag || wait_expired(t0, c0))) {
-            *abort_flag = 1;
-            return false;
-        }
+// The waits for work, which end after ns nanoseconds (cycles: twice that) or when another
+// warp of the CTA gave up.  A wait that runs out raises the CTA's flag; its other waits for
+// work then end too, what was not computed is written as NaN, and the CTA leaves by the same
+// barriers as always.  Copies and MMAs in flight are waited for whatever happened (mbar_wait,
+// 2 s): nothing may land in memory that the next CTA holds.
+struct Patience {
+    uint64_t ns;
+    volatile int *abort_flag;
+    __device__ __forceinline__ bool over(uint64_t t0, long long c0) const {
+        return *abort_flag || globaltimer_ns() - t0 > ns || clock64() - c0 > (long long)(2 * ns);
     }
-}
+};
 
-// The same for a whole warp, unless it is `over` already: every lane gets the same answer.
+// For a whole warp, unless it is `done` already: every lane gets the same answer.
 template <bool kCluster = false>
-__device__ __forceinline__ bool warp_wait(bool over, uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    if (__all_sync(~0u, over)) return true;
+__device__ __forceinline__ bool warp_wait(bool done, uint64_t *bar, uint32_t parity, const Patience &p) {
+    if (__all_sync(~0u, done)) return true;
     const uint64_t t0 = globaltimer_ns();
     const long long c0 = clock64();
-    for (uint32_t it = 1;; ++it) {
+    for (uint32_t it = 0;; ++it) {
         if (__all_sync(~0u, kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
-        if ((it & 15u) == 0 && __any_sync(~0u, *abort_flag || wait_expired(t0, c0))) {
-            *abort_flag = 1;
+        if ((it & 15u) == 0 && __any_sync(~0u, p.over(t0, c0))) {
+            *p.abort_flag = 1;
             return false;
         }
     }
@@ -304,6 +303,33 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar, uint32_t pair) {
         : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Counts `bytes` on this CTA's barrier as a copy would.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
+// After a pair gave up: the leader's load warp issued `mine` stages, the other's `theirs`, and
+// every stage counts the bytes of both on the leader's barrier.  The leader counts what the
+// other did not issue, arms the stages that only the other issued, and so sees the last
+// copies of both land.  The two are at most a ring apart: a stage is issued again only
+// after its last chunk, both halves of it, was multiplied.
+template <int kStages, uint32_t kBytes>
+__device__ __forceinline__ bool settle_pair(uint64_t *full, uint32_t mine, uint32_t theirs) {
+    if (elect_one()) {
+        for (uint32_t i = theirs; i < mine; ++i) mbar_complete_tx(&full[i % kStages], kBytes);
+        for (uint32_t i = mine; i < theirs; ++i) mbar_arrive_expect_tx(&full[i % kStages], kBytes);
+    }
+    __syncwarp();
+    const uint32_t last = max(mine, theirs);
+    bool ok = true;
+    for (uint32_t i = last > kStages ? last - kStages : 0; i < last; ++i)
+        ok &= mbar_wait(&full[i % kStages], (i / kStages) & 1);
+    return ok;
+}
+
 template <int BT, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, LinearArgs a, Plan plan) {
@@ -317,6 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    // a pair's: whether some pair of the cluster gave up, and the stages the other CTA issued
+    volatile int *gave_up = abort_flag + 1;
+    volatile uint32_t *peer_issued = reinterpret_cast<volatile uint32_t *>(gave_up + 1);
+    const Patience patience{a.wait_ns, abort_flag};
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     pdl_launch_dependents();
 
@@ -330,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&acc_empty[i], kPair ? 2 * kEpiWarps : kEpiWarps);
         }
         mbar_init(drain, 1);
-        *abort_flag = 0;
+        *abort_flag = *gave_up = 0;
+        *peer_issued = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
@@ -350,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t leader = kPair ? cluster_rank() & ~1u : 0, both = 3u << leader;
     Walk walk(plan, blockIdx.x);
     Segment seg;
+    uint32_t issued = 0;  // the load warp's stages
 
     // The loads' and the MMAs' loops are run by whole warps on values that are the same in
     // every lane, and one elected lane issues: the operands stay in uniform registers.  (With
@@ -357,14 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // issue; the MMAs of the widest tile take 512.)
     if (warp == 0) {
         const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), leader) : 0;
-        uint32_t s = 0, phase = 1, issued = 0;
+        uint32_t s = 0, phase = 1;
         bool ok = true, free = mbar_test_wait(&empty[0], 1);
         while (ok && walk.next(seg)) {
             const int t0 = seg.tile % plan.tiles_m * BT + half * (BT / 2);
             const int n0 = seg.tile / plan.tiles_m * kTileN + half * kBN;
             for (int kc = seg.k0; kc < seg.k1; ++kc) {
                 // the first round's waits are for the phase before the barriers' first: over at once
-                if (!warp_wait(free, &empty[s], phase, abort_flag)) {
+                if (!warp_wait(free, &empty[s], phase, patience)) {
                     ok = false;
                     break;
                 }
@@ -392,11 +424,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++issued;
             }
         }
-        // given up: the copies in flight still land in this CTA's shared memory (a pair's are
-        // counted by the leader)
-        if (!ok && half == 0)
-            for (uint32_t i = issued > L::kStages ? issued - L::kStages : 0; i < issued; ++i)
-                mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1);
+        // The copies in flight land in this CTA's shared memory.  A pair's are counted by the
+        // leader, both halves of a stage together; where it does not see them all, the
+        // cluster's CTAs settle it after their next barrier.
+        const uint32_t tail = issued > L::kStages ? issued - L::kStages : 0;
+        if (!kPair) {
+            for (uint32_t i = tail; i < issued; ++i) ok &= mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1);
+            if (!ok) *abort_flag = 1;
+        } else if (half == 0) {
+            for (uint32_t i = tail; i < issued; ++i)
+                ok = ok && warp_wait(false, &full[i % L::kStages], (i / L::kStages) & 1, patience);
+            if (!ok && lane < 2 * plan.cluster) st_cluster_u32(map_to_rank(smem_u32((const void *)gave_up), lane), 1);
+        } else if (lane == 0) {
+            st_cluster_u32(map_to_rank(smem_u32((const void *)peer_issued), leader), issued);
+        }
+        __syncwarp();
     } else if (warp == 1 && half == 0) {
         constexpr uint32_t idesc = idesc_bf16(kTileN, BT, true, false);
         // descriptors of stage 0: a stage and a step of K move the start address (in 16 bytes)
@@ -407,11 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true, there = false;
         for (; ok && walk.next(seg); ++n_seg) {
             const uint32_t b = n_seg & 1;
-            if (n_seg >= 2 && !warp_wait<kPair>(false, &acc_empty[b], (n_seg / 2 - 1) & 1, abort_flag)) break;
+            if (n_seg >= 2 && !warp_wait<kPair>(false, &acc_empty[b], (n_seg / 2 - 1) & 1, patience)) break;
             tc_fence_after();
             const uint32_t d = acc0 + b * BT;
             for (int kc = seg.k0; kc < seg.k1; ++kc) {
-                if (!warp_wait(there, &full[s], phase, abort_flag)) {
+                if (!warp_wait(there, &full[s], phase, patience)) {
                     ok = false;
                     break;
                 }
@@ -436,13 +478,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (!ok || *abort_flag) {  // let the MMAs in flight end before the memory they use is given up
-            if (elect_one()) {
-                if (kPair) mma_commit_pair(drain, both);
-                else mma_commit(drain);
-            }
-            mbar_wait(drain, 0);
+        // the MMAs end before the memory they use is given up or put to another use
+        __syncwarp();
+        if (elect_one()) {
+            if (kPair) mma_commit_pair(drain, both);
+            else mma_commit(drain);
         }
+        if (!mbar_wait(drain, 0)) *abort_flag = 1;
+        __syncwarp();
     } else if (warp >= 2) {
         const int q = warp & 3, c0 = (warp - 2) / 4 * kStep;  // its rows, and its first tokens
         bool ok = true;
@@ -456,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t acc = tmem + tmem_lane_base(q) + b * BT;
             Finish fin(a, t0, n0 + q * 32 + lane % 4 * 8);
             if (!cut) fin.load_residual(a, c0 + lane / 4, nt);
-            ok = ok && wait_or_abort(&acc_full[b], (n_seg / 2) & 1, abort_flag);
-            __syncwarp();
+            ok = ok && warp_wait(false, &acc_full[b], (n_seg / 2) & 1, patience);
             tc_fence_after();
             float *part = a.part + (2ll * blockIdx.x + (first_seg ? 0 : 1)) * (kBN * BT) + q * 32 + lane;
             for (int c = c0; c < nt; c += 2 * kStep) {
@@ -484,7 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
+            // a warp that gave up holds the accumulator: its arrivals, which wait for nothing, would
+            // stand for those of a warp that still reads
+            if (lane == 0 && ok) {
                 if (half == 0) mbar_arrive(&acc_empty[b]);
                 else mbar_arrive_remote(map_to_rank(smem_u32(&acc_empty[b]), leader));
             }
@@ -503,10 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (warp >= 2) {
             fin.load_half(a, first + i0 / 16, last);
-            ok = wait_or_abort(&acc_full[0], 0, abort_flag);
+            ok = warp_wait(false, &acc_full[0], 0, patience);
         }
         __syncwarp();
         cluster_sync();
+        if (kPair && *gave_up) {  // the same for every CTA of the cluster
+            if (warp == 0 && half == 0 && !settle_pair<L::kStages, L::kStage>(full, issued, *peer_issued)) *abort_flag = 1;
+            __syncwarp();
+            cluster_sync();
+        }
         if (warp >= 2) {
             tc_fence_after();
             const int q = warp & 3;
@@ -544,7 +593,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (kPair) cluster_sync();  // neither CTA's memory is used by the other any more
+    if (threadIdx.x == 0 && *abort_flag) set_status(a.status, MLA_ERR_TIMEOUT);
+    if (kPair) {
+        // the MMAs' last arrivals on this CTA's barriers
+        if (half == 1 && warp == 1) mbar_wait(drain, 0);
+        __syncwarp();
+        cluster_sync();  // neither CTA's memory is used by the other any more
+        if (plan.cluster == 1 && *gave_up) {
+            if (warp == 0 && half == 0) settle_pair<L::kStages, L::kStage>(full, issued, *peer_issued);
+            __syncwarp();
+            cluster_sync();
+        }
+    }
     if (warp == 1) {
         tc_fence_after();
         if (kPair) tmem_free_pair<L::kTmemCols>(tmem);

@@ -47,7 +47,7 @@ EXPORTS = ("mla_status_string", "mla_abi_version", "mla_absorb_q", "mla_decode_w
            "mla_cache_append", "mla_decode_sparse_workspace_size", "mla_decode_attn_sparse", "mla_prefill_crossover",
            "mla_prefill_expand_workspace_size", "mla_prefill_expand", "mla_prefill_workspace_size", "mla_prefill",
            "mla_decode_step", "mla_set_wait_limit_ns", "mla_rope_init", "mla_rope", "mla_pages_update",
-           "mla_latent_store", "mla_linear_workspace_size", "mla_linear")
+           "mla_latent_store", "mla_linear_workspace_size", "mla_linear", "mla_linear_status")
 PATH_ABSORB, PATH_EXPAND = 0, 1
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
@@ -149,6 +149,8 @@ def load(path: str | None = None):
     lib.mla_linear_workspace_size.restype = SZ
     lib.mla_linear.argtypes = [pl, P, P, P, P, P, P, SZ, P]
     lib.mla_linear.restype = I
+    lib.mla_linear_status.argtypes = [pl, P, P, P, P, P, P, SZ, P, P]
+    lib.mla_linear_status.restype = I
     if path is None:
         _lib = lib
     return lib
@@ -421,8 +423,8 @@ def decode_attn_noalloc(prob: Problem, q_cat, cache: Cache, o_lat, lse, num_spli
 
 
 def set_wait_limit_ns(ns: int) -> None:
-    """mla_set_wait_limit_ns: the bound of the attention kernels' waits for work
-    (0: the default 2 s).  For tests of the timeout path."""
+    """mla_set_wait_limit_ns: the bound of the attention kernels' and of linear's waits for
+    work (0: the default 2 s).  For tests of the timeout path."""
     _check(load().mla_set_wait_limit_ns(int(ns)), "mla_set_wait_limit_ns")
 
 
@@ -664,9 +666,10 @@ def linear_workspace_size(M: int, K: int, N: int) -> int:
     return int(n)
 
 
-def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, workspace=None, stream=None):
+def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, workspace=None, stream=None, status=None):
     """mla_linear: residual + act(x . w + bias), x [M, K] and residual [M, N] with any row stride
-    (multiples of 8), w [K, N] dense.  ``out`` may be ``residual``."""
+    (multiples of 8), w [K, N] dense.  ``out`` may be ``residual``; ``status`` (an int32 word)
+    takes MLA_ERR_TIMEOUT where a wait on the device ran out."""
     lib = _lib or load()
     dev = _device(x, "x")
     if w.dim() != 2 or x.dim() != 2:
@@ -678,6 +681,7 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
         _refuse(w, "w", f"a dense torch.bfloat16 tensor on device {dev}")
     b = None if bias is None else _dense(bias, "bias", _BF16, dev, (N,))
     res = None if residual is None else _rows(residual, "residual", dev, M, N)
+    word = None if status is None else _word(status, dev)
     if out is None:
         out = _new((M, N), (N, 1), _BF16, stream)
         to, out_stride = out.data_ptr(), N
@@ -691,13 +695,13 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             _refuse(workspace, "workspace", f"dense memory on device {dev}")
-        code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), workspace.nbytes, st)
+        code = lib.mla_linear_status(at, rows, weight, b, res, to, workspace.data_ptr(), workspace.nbytes, word, st)
     else:  # most shapes need none
-        code = lib.mla_linear(at, rows, weight, b, res, to, None, 256, st)
+        code = lib.mla_linear_status(at, rows, weight, b, res, to, None, 256, word, st)
         if code == _ERR_WORKSPACE:
             nbytes = lib.mla_linear_workspace_size(at)
             workspace = _new((nbytes,), (1,), torch.uint8, stream)
-            code = lib.mla_linear(at, rows, weight, b, res, to, workspace.data_ptr(), nbytes, st)
+            code = lib.mla_linear_status(at, rows, weight, b, res, to, workspace.data_ptr(), nbytes, word, st)
     if code:
         raise MLAError(code, "mla_linear")
     return out

@@ -913,3 +913,42 @@ def test_linear_refuses_a_workspace_it_cannot_use():
     assert torch.equal(mla.linear(x, w, workspace=words), mla.linear(x, w))
     with pytest.raises(mla.MLAError):
         mla.linear(x, w, workspace=words[:-64])
+
+
+# -------------------------------------------------------------------------------------------- waits that run out
+TIMEOUT_CASES = [
+    # M, K, N: whole tiles, clusters, runs, pairs in several rounds, clusters of two and of four pairs
+    (333, 1000, 1544), (64, 16384, 1024), (3, 65536, 136), (8, 4104, 20480), (5000, 1032, 6000), (250, 8200, 7000),
+    (1264, 6792, 416), (2000, 16384, 256),
+]
+
+
+@pytest.mark.parametrize("M,K,N", TIMEOUT_CASES)
+def test_linear_wait_timeout_reported_and_recovered(M, K, N):
+    """With a short bound on the waits for work, some of them run out, at once or on the way: the call ends, the status
+    word says so, every output is NaN or what it should be (whole numbers: exact sums), and calls after it are clean."""
+    g = gen(M + K + N + 7)
+    x, w = (torch.randint(-3, 4, n, generator=g).to(BF16).to(DEV) for n in ((M, K), (K, N)))
+    status = torch.zeros(1, dtype=I32, device=DEV)
+    want = mla.linear(x, w, status=status)
+    assert int(status) == 0
+    assert torch.equal(want, (x.float().double() @ w.float().double()).float().to(BF16))
+    seen = []
+    try:
+        for ns in (1, 1, 300, 1000, 3000, 4000, 5000, 6500, 8000, 10000):
+            mla.set_wait_limit_ns(ns)
+            status.zero_()
+            out = torch.full((M, N), 7.25, dtype=BF16, device=DEV)  # no sum of whole numbers
+            mla.linear(x, w, out=out, status=status)
+            torch.cuda.synchronize()
+            bad = torch.isnan(out)
+            assert torch.equal(out[~bad], want[~bad]), ns
+            assert int(status) in (0, 8) and (int(status) == 8 or not bool(bad.any())), ns
+            seen.append((int(status), int(bad.sum())))
+    finally:
+        mla.set_wait_limit_ns(0)
+    print(seen)
+    assert (8 in [c for c, _ in seen]) and any(n for _, n in seen), seen  # MLA_ERR_TIMEOUT
+    for _ in range(2):
+        status.zero_()
+        assert torch.equal(mla.linear(x, w, status=status), want) and int(status) == 0

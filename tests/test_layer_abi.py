@@ -293,3 +293,13 @@ def test_pages_update_checks_fields_assigned_later(lib, device0):
         setattr(pages, name, value)
         with pytest.raises(ValueError):
             mla.pages_update(pages, i32(2), lens, i32(2), 4, out=out)
+
+
+def test_linear_status_is_checked_like_the_rest(lib, device0):
+    d, out = mla.LinearDesc(4, 64, 128, 0, 64, 128, 128), ctypes.c_void_p(0x60000)
+    assert lib.mla_linear_status(ctypes.byref(d), A, A, NUL, NUL, out, A, 1 << 30, ODD4, NUL) == 4
+    assert lib.mla_linear_status(None, A, A, NUL, NUL, out, A, 1 << 30, A, NUL) == 1
+    x, w, y = (OnDevice(torch.zeros(*n, dtype=torch.bfloat16)) for n in ((8, 64), (64, 128), (8, 128)))
+    for word in (OnDevice(torch.zeros(1, dtype=torch.int64)), OnDevice(torch.zeros(1, dtype=torch.int32), -1)):
+        with pytest.raises(ValueError, match="status"):
+            mla.linear(x, w, out=y, status=word)
