@@ -138,8 +138,10 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
     int t = blockIdx.x * kWarps + threadIdx.x / 32;
     if (t >= a.tokens) return;
     Row row = load_row<kHalf>(a, t, lane);
-    // what a value is multiplied by besides 1 / rms: its weight, and 1 / kv_scale
+    // FP8: value times 1 / kv_scale, last and by itself: the scale may be as small as 2^-126, and
+    // taken together with a weight past 4 its inverse would be infinite, a latent of 0 NaN
     const float unit = kFp8 ? 1.f / a.cache.kv_scale : 1.f;
+    const float2 unit2 = make_float2(unit, unit);
     float2 wt[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -148,8 +150,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
         const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float2 p = unpack(w4[e]);
-            wt[i][e] = make_float2(unit * p.x, unit * p.y);
+            wt[i][e] = unpack(w4[e]);
         }
     }
     const float part = 1.f / (float)a.d_c;
@@ -181,7 +182,10 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[i][e] = mul2(mul2(f[i][e], inv), wt[i][e]);
+                for (int e = 0; e < 4; ++e) {
+                    f[i][e] = mul2(mul2(f[i][e], inv), wt[i][e]);
+                    if (kFp8) f[i][e] = mul2(f[i][e], unit2);
+                }
             float2 k = unpack(r.k);
             if (a.rotate) {
                 k = key.trade(k, lane);

@@ -480,6 +480,31 @@ def test_latent_store_special_values():
         assert bool((got[3, :d_c] == 0).all()) and float(got[3, d_c]) == (448.0 if fp8 else float(x[3, 0]))
 
 
+def test_latent_store_fp8_smallest_scale():
+    """kv_scale 2^-126, whose inverse is 2^126, with weights that times it pass fp32: zeros stay zeros (a row of them, and
+    beside other values), what is not zero saturates with its sign, and values of the scale's own size are held as such."""
+    d_c, d_rope = 64, 16
+    x = torch.zeros(3, d_c + d_rope, dtype=BF16)
+    x[1, :4] = torch.tensor([1.0, -2.0, 0.0, 0.5])
+    x[2, :4] = torch.tensor([2.0 ** -126, -3 * 2.0 ** -126, 0.0, 2.0 ** -125])
+    x[:, d_c:d_c + 2] = torch.tensor([2.0 ** -124, -1.0])
+    weight = torch.full((d_c,), 4.0)
+    weight[1], weight[5] = 1e30, -8.0
+    want = torch.zeros(3, d_c + d_rope)
+    want[:, d_c:d_c + 2] = torch.tensor([4.0, -448.0])
+    prob = problem(3, 16, 1, d_c=d_c, d_rope=d_rope)
+    lens, table = torch.ones(3, dtype=I32, device=DEV), torch.zeros(3, 1, dtype=I32, device=DEV)
+    for norm in (weight.to(BF16).to(DEV), None):
+        kv = torch.full((1, 64, d_c + d_rope), 0x55, dtype=torch.uint8, device=DEV)
+        cache = mla.make_cache(prob, kv, lens, table, 64, kv_scale=2.0 ** -126)
+        mla.latent_store(prob, x.to(DEV), cache, norm_weight=norm, eps=1e-6, slots=torch.arange(3, dtype=I32, device=DEV))
+        got = kv.view(torch.float8_e4m3fn).cpu().float()[0, :3]
+        want[1, :4] = torch.tensor([448.0, -448.0, 0.0, 448.0])
+        # without a norm the row's own values; with one they are 1000 times that (1 / sqrt(eps)) and their weight
+        want[2, :4] = torch.tensor([1.0, -3.0, 0.0, 2.0]) if norm is None else torch.tensor([448.0, -448.0, 0.0, 448.0])
+        assert torch.equal(got, want)
+
+
 # ----------------------------------------------------------------------------------------------------------- linear
 LINEAR_CASES = [
     # M, K, N, bias, act, residual, paddings of x, out and residual rows
