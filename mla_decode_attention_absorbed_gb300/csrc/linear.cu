@@ -81,34 +81,44 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// v / (1 + 2^-x): v times the logistic function of x ln 2.
-__device__ __forceinline__ float times_logistic(float v, float x) { return v * rcp(1.f + ex2(-x)); }
+// The activations hold their relative error down to the smallest normal numbers: where they
+// fall off, the power of two is taken as h^2 with h = 2^(half the exponent), and the value is
+// multiplied by h twice, so that nothing on the way leaves the range of fp32.  (With 2^x in
+// one piece SiLU was -0 below -87.3 and GELU below -13.1, where bf16 still holds the result.)
 
-// v Phi(v), Phi the normal distribution.  With z = |v| / sqrt 2 and t = 1 / (1 + z / 2),
+// v / (1 + 2^(-2 x)): v times the logistic function of 2 x ln 2.
+__device__ __forceinline__ float times_logistic(float v, float x) {
+    const float h = ex2(-fabsf(x)), s = v * rcp(fmaf(h, h, 1.f));
+    return x < 0.f ? s * h * h : s;
+}
+
+// v Phi(v), Phi the normal distribution.  With z = |v| / sqrt 2 and t = 1 / (1 + z / 2) (the
+// change of variable that Press et al., Numerical Recipes, use for erfc),
 //   Phi(-|v|) = erfc(z) / 2 = t 2^(Q(t) - z^2 log2 e),
-// Q a polynomial fitted to log2(erfc(z) exp(z^2) / (2 t)) on (0, 1] (worst error 3.4e-6): no
-// cancellation on either side, relative error of the whole at most 2^-17.3.  CUDA's erfcf in
-// its place took a 1588 x 400 x 6072 product with bias and residual from 29 us to 41.
+// Q a polynomial fitted to log2(erfc(z) exp(z^2) / (2 t)) on (0, 1] (worst error 3.5e-6), here
+// halved: no cancellation on either side.  Relative error at most 2^-17.3 from v = -10 up and
+// 2^-16.7 below, where the rounding of an exponent near -120 counts.  CUDA's erfcf in its
+// place took a 1588 x 400 x 6072 product with bias and residual from 29 us to 41.
 __device__ __forceinline__ float gelu(float v) {
     const float t = rcp(fmaf(fabsf(v), 0.35355339f, 1.f));
-    float q = fmaf(t, -0.22946589f, 0.9304564f);
-    q = fmaf(t, q, -1.2151098f);
-    q = fmaf(t, q, 0.32995093f);
-    q = fmaf(t, q, 0.014981962f);
-    q = fmaf(t, q, 0.55273217f);
-    q = fmaf(t, q, 1.4422023f);
-    q = fmaf(t, q, -2.8257446f);
-    const float below = t * ex2(fmaf(v * v, -0.72134752f, q));
-    return v * (v < 0.f ? below : 1.f - below);
+    float q = fmaf(t, 0.5f * -0.22946589f, 0.5f * 0.9304564f);
+    q = fmaf(t, q, 0.5f * -1.2151098f);
+    q = fmaf(t, q, 0.5f * 0.32995093f);
+    q = fmaf(t, q, 0.5f * 0.014981962f);
+    q = fmaf(t, q, 0.5f * 0.55273217f);
+    q = fmaf(t, q, 0.5f * 1.4422023f);
+    q = fmaf(t, q, 0.5f * -2.8257446f);
+    const float h = ex2(fmaf(v * v, 0.5f * -0.72134752f, q)), th = t * h;
+    return v < 0.f ? v * th * h : v * fmaf(-th, h, 1.f);
 }
 
 template <int kAct>
 __device__ __forceinline__ float activate(float v) {
     if (kAct == MLA_ACT_RELU) return v < 0.f ? 0.f : v;  // NaN stays
-    if (kAct == MLA_ACT_SILU) return times_logistic(v, v * 1.442695041f);
+    if (kAct == MLA_ACT_SILU) return times_logistic(v, v * 0.72134752f);  // 2^-17.1
     if (kAct == MLA_ACT_GELU) return gelu(v);
-    // (1 + tanh z) / 2 is the logistic function of 2 z
-    if (kAct == MLA_ACT_GELU_TANH) return times_logistic(v, v * fmaf(v * v, 0.10294324f, 2.3022082f));
+    // (1 + tanh z) / 2 is the logistic function of 2 z; 2^-16.3
+    if (kAct == MLA_ACT_GELU_TANH) return times_logistic(v, v * fmaf(v * v, 0.05147162f, 1.1511041f));
     return v;
 }
 template <int kAct, int N>

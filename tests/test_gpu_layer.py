@@ -977,3 +977,35 @@ def test_linear_wait_timeout_reported_and_recovered(M, K, N):
     for _ in range(2):
         status.zero_()
         assert torch.equal(mla.linear(x, w, status=status), want) and int(status) == 0
+
+
+# ----------------------------------------------------------------------------------------- activations over their range
+def exact_activation(act, v):
+    """In 64 bits without cancellation: v Phi(v) by erfc, the others by the logistic function of z."""
+    if act == "gelu":
+        return 0.5 * v * torch.special.erfc(-v / math.sqrt(2))
+    z = v if act == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)
+    e = torch.exp(-z.abs())
+    return torch.where(z < 0, v * e, v) / (1 + e)
+
+
+@pytest.mark.parametrize("act,least", [("silu", -94.0), ("gelu", -13.75), ("gelu_tanh", -10.5)])
+def test_linear_activations_to_the_end_of_bf16(act, least):
+    """One non-zero weight of 1, so that the activation gets x itself, from where its result leaves bf16 to 14.  A result
+    rounds once, half a step of 2^-8 of it (2^-134 among the subnormals) beside 2^-16 for the activation in fp32 (an
+    exponent near -126 rounds to 2^-18, ln 2 of which is 2^-18.5, three times; tanh's cube twice that).  With the rounded
+    result taken off again by the residual, what is left is that error in fp32 and half a step of a remainder that is
+    itself at most half a step: 2^-16 twice."""
+    v = torch.cat((torch.linspace(least, 0, 6000), torch.linspace(0, 14, 3000), -torch.logspace(-30, 1, 3000))).to(BF16)
+    v = torch.unique(v.float()).to(BF16)
+    M, N = v.numel(), 8
+    x, w = torch.zeros(M, 8, dtype=BF16), torch.zeros(8, N, dtype=BF16)
+    x[:, 3], w[3] = v, 1.0
+    want = exact_activation(act, v.double())[:, None].expand(M, N)
+    got = mla.linear(x.to(DEV), w.to(DEV), act=ACTS[act])
+    close(got, want, want.abs() * (2.0 ** -8 + 2.0 ** -16) + 2.0 ** -134)
+    tail = (want.abs() > 2.0 ** -126) & (want < 0)
+    assert bool((got.cpu()[tail] < 0).all()) and int(tail.sum()) > 1000
+    taken = -want.to(BF16)
+    left = mla.linear(x.to(DEV), w.to(DEV), act=ACTS[act], residual=taken.contiguous().to(DEV))
+    close(left, want + taken.double(), want.abs() * 2.0 ** -15 + 2.0 ** -133)
