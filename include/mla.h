@@ -546,6 +546,19 @@ typedef struct {
     long long residual_stride; /* (not read without a residual) */
 } mla_linear_desc;
 
+/* How mla_linear cuts a product on the current device (for tests and measurements).
+ * Tile by tile, or in runs of tiles' chunks; a tile's K in k_parts equal parts. */
+typedef struct {
+    int tile_rows;    /* rows of x a tile */
+    int tile_columns; /* columns of w a tile (256: taken by a pair of CTAs) */
+    int k_parts;      /* CTAs, or pairs of them, that share a tile's K */
+    int runs;         /* 1: equal runs of 64-wide chunks of K, cut where they end */
+    int ctas;
+} mla_linear_cut;
+
+/* Host only.  MLA_ERR_SHAPE for M = 0, else the errors of mla_linear. */
+MLA_API int mla_linear_query_cut(const mla_linear_desc *desc, mla_linear_cut *cut);
+
 /* Bytes of workspace mla_linear needs (0 for invalid arguments).  Up to 256 bytes
  * none is used, and workspace may be NULL. */
 MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *desc);

@@ -275,6 +275,16 @@ MLA_API int mla_latent_store(const mla_dims *dims, const mla_rope_plan *plan, co
     return result(mla::launch_latent_store(a, as_stream(stream)));
 }
 
+MLA_API int mla_linear_query_cut(const mla_linear_desc *d, mla_linear_cut *cut) {
+    const int s = check_linear(d, false);
+    if (s) return s;
+    if (!cut) return MLA_ERR_NULL;
+    if (d->M == 0) return MLA_ERR_SHAPE;
+    const mla::LinearPlan p = mla::linear_plan(d->M, d->K, d->N, mla::layer_num_sms());
+    *cut = mla_linear_cut{p.bt, p.pair ? 256 : 128, p.cluster, !p.whole, p.grid};
+    return MLA_OK;
+}
+
 MLA_API size_t mla_linear_workspace_size(const mla_linear_desc *d) {
     if (check_linear(d, false)) return 0;
     return d->M == 0 ? 256 : mla::linear_workspace_bytes(mla::linear_plan(d->M, d->K, d->N, mla::layer_num_sms()));

@@ -47,7 +47,8 @@ EXPORTS = ("mla_status_string", "mla_abi_version", "mla_absorb_q", "mla_decode_w
            "mla_cache_append", "mla_decode_sparse_workspace_size", "mla_decode_attn_sparse", "mla_prefill_crossover",
            "mla_prefill_expand_workspace_size", "mla_prefill_expand", "mla_prefill_workspace_size", "mla_prefill",
            "mla_decode_step", "mla_set_wait_limit_ns", "mla_rope_init", "mla_rope", "mla_pages_update",
-           "mla_latent_store", "mla_linear_workspace_size", "mla_linear", "mla_linear_status")
+           "mla_latent_store", "mla_linear_workspace_size", "mla_linear", "mla_linear_status",
+           "mla_linear_query_cut")
 PATH_ABSORB, PATH_EXPAND = 0, 1
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
@@ -76,6 +77,10 @@ class LinearDesc(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int), ("act", ctypes.c_int),
                 ("x_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong),
                 ("residual_stride", ctypes.c_longlong)]
+
+
+class LinearCut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("tile_rows", "tile_columns", "k_parts", "runs", "ctas")]
 
 
 def lib_path() -> str:
@@ -151,6 +156,8 @@ def load(path: str | None = None):
     lib.mla_linear.restype = I
     lib.mla_linear_status.argtypes = [pl, P, P, P, P, P, P, SZ, P, P]
     lib.mla_linear_status.restype = I
+    lib.mla_linear_query_cut.argtypes = [pl, ctypes.POINTER(LinearCut)]
+    lib.mla_linear_query_cut.restype = I
     if path is None:
         _lib = lib
     return lib
@@ -664,6 +671,13 @@ def linear_workspace_size(M: int, K: int, N: int) -> int:
     if n == 0:
         raise ValueError("mla_linear_workspace_size rejected the arguments")
     return int(n)
+
+
+def linear_cut(M: int, K: int, N: int) -> LinearCut:
+    """mla_linear_query_cut: how a product of these sizes is cut on the current device (host only)."""
+    desc, cut = LinearDesc(M, K, N, ACT_NONE, K, N, N), LinearCut()
+    _check(load().mla_linear_query_cut(ctypes.byref(desc), ctypes.byref(cut)), "mla_linear_query_cut")
+    return cut
 
 
 def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, workspace=None, stream=None, status=None):

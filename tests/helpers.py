@@ -100,3 +100,20 @@ def sample_rows(cfg: MLAConfig, n: int, seed: int = 1):
     rows = set(g.choice(total, size=min(n, total), replace=False).tolist())
     rows |= {0, total - 1}
     return sorted(rows)
+
+
+# A product for every way mla_linear cuts one on a GPU of 152 SMs, (rows a tile, columns a tile, parts of K, runs) to
+# (M, K, N), each with rows, K and columns that end inside a tile.
+LINEAR_FORMS = {
+    (16, 128, 1, 0): (3, 136, 136), (16, 128, 2, 0): (3, 456, 4680), (16, 128, 4, 0): (3, 456, 136),
+    (16, 128, 8, 0): (3, 976, 136), (16, 128, 1, 1): (3, 1520, 19856),
+    (32, 128, 1, 0): (1256, 136, 136), (32, 128, 2, 0): (619, 840, 136), (32, 128, 4, 0): (293, 648, 136),
+    (32, 128, 8, 0): (114, 1288, 136), (32, 128, 1, 1): (17, 2016, 19512),
+    (64, 128, 1, 0): (2460, 136, 136), (64, 128, 2, 0): (1241, 1352, 136), (64, 128, 4, 0): (43, 16320, 3224),
+    (64, 128, 8, 0): (293, 2888, 136), (64, 128, 1, 1): (141, 17712, 944),
+    (128, 128, 1, 0): (5178, 328, 136), (128, 128, 2, 0): (323, 2544, 1952), (128, 128, 4, 0): (1241, 2792, 144),
+    (128, 128, 8, 0): (583, 5624, 136), (128, 128, 1, 1): (794, 18704, 1400),
+    (256, 128, 1, 0): (565, 480, 12816), (256, 128, 2, 0): (1001, 14000, 2368), (256, 128, 4, 0): (1276, 12360, 880),
+    (256, 128, 8, 0): (1237, 14288, 136), (256, 128, 1, 1): (2869, 13720, 864),
+    (256, 256, 1, 0): (5234, 904, 392), (256, 256, 2, 0): (3310, 4648, 280), (256, 256, 4, 0): (1604, 5968, 272),
+}

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import oracle
-from helpers import within_tolerance
+from helpers import LINEAR_FORMS, within_tolerance
 from mla_decode_attention_absorbed_gb300 import build, mla
 from oracle import layer
 
@@ -1009,3 +1009,28 @@ def test_linear_activations_to_the_end_of_bf16(act, least):
     taken = -want.to(BF16)
     left = mla.linear(x.to(DEV), w.to(DEV), act=ACTS[act], residual=taken.contiguous().to(DEV))
     close(left, want + taken.double(), want.abs() * 2.0 ** -15 + 2.0 ** -133)
+
+
+# ------------------------------------------------------------------------------------------------- every form of a product
+@pytest.mark.parametrize("form", LINEAR_FORMS, ids=lambda f: "x".join(map(str, f)))
+def test_linear_every_form(form):
+    """Each way a product is cut, with ends inside tiles: small whole numbers, whose sums are exact in fp32, so that only
+    the epilogue rounds and the result is bit-equal; rows in wider ones, bias and residual; and again, bit for bit."""
+    M, K, N = LINEAR_FORMS[form]
+    cut = mla.linear_cut(M, K, N)
+    assert (cut.tile_rows, cut.tile_columns, cut.k_parts, cut.runs) == form
+    g = torch.Generator(device=DEV).manual_seed(sum(form) + M)
+    x = torch.randint(-4, 5, (M, K + 8), generator=g, device=DEV).to(BF16)[:, :K]
+    w = torch.randint(-4, 5, (K, N), generator=g, device=DEV).to(BF16)
+    b, r = torch.randn(N, generator=g, device=DEV).to(BF16), torch.randn(M, N + 16, generator=g, device=DEV).to(BF16)[:, :N]
+    full = (x.double() @ w.double()).float()  # exact
+    status = torch.zeros(1, dtype=I32, device=DEV)
+    assert torch.equal(mla.linear(x, w, status=status), full.to(BF16))
+    out = torch.full((M, N + 8), 9.0, dtype=BF16, device=DEV)
+    for _ in range(2):
+        mla.linear(x, w, bias=b, residual=r, act=mla.ACT_RELU, out=out[:, :N], status=status)
+        assert torch.equal(out[:, :N], ((full + b.float()).clamp(min=0) + r.float()).to(BF16))
+        assert bool((out[:, N:] == 9).all())
+    stream = r.clone(memory_format=torch.contiguous_format)  # in place on the residual
+    mla.linear(x, w, bias=b, residual=stream, act=mla.ACT_RELU, out=stream, status=status)
+    assert torch.equal(stream, out[:, :N]) and int(status) == 0

@@ -5,11 +5,13 @@ import ctypes
 import dataclasses
 import math
 import pickle
+import random
 import weakref
 
 import pytest
 import torch
 
+from helpers import LINEAR_FORMS
 from mla_decode_attention_absorbed_gb300 import build, mla
 from oracle import layer
 
@@ -303,3 +305,31 @@ def test_linear_status_is_checked_like_the_rest(lib, device0):
     for word in (OnDevice(torch.zeros(1, dtype=torch.int64)), OnDevice(torch.zeros(1, dtype=torch.int32), -1)):
         with pytest.raises(ValueError, match="status"):
             mla.linear(x, w, out=y, status=word)
+
+
+# ------------------------------------------------------------------------------------------------- how products are cut
+@pytest.mark.parametrize("form", LINEAR_FORMS)
+def test_linear_forms_are_reached(lib, form):
+    """The shapes that the GPU tests compare, form by form, are still cut that way (without a GPU the plan is that of 152
+    SMs); together they hold every form there is."""
+    cut = mla.linear_cut(*LINEAR_FORMS[form])
+    assert (cut.tile_rows, cut.tile_columns, cut.k_parts, cut.runs) == form and 1 <= cut.ctas <= 152
+
+
+def test_linear_forms_are_all_there(lib):
+    rng = random.Random(5)
+    seen = set()
+    for _ in range(20000):
+        M, K, N = int(math.exp(rng.uniform(0, 9))), 8 * int(math.exp(rng.uniform(0, 7.8))), 8 * int(math.exp(rng.uniform(0, 8)))
+        cut = mla.linear_cut(M, K, N)
+        seen.add((cut.tile_rows, cut.tile_columns, cut.k_parts, cut.runs))
+        assert (mla.linear_workspace_size(M, K, N) > 256) == bool(cut.runs)
+    assert seen <= set(LINEAR_FORMS)
+
+
+def test_linear_cut_refusals(lib):
+    cut = mla.LinearCut()
+    assert lib.mla_linear_query_cut(None, ctypes.byref(cut)) == 1
+    assert lib.mla_linear_query_cut(ctypes.byref(mla.LinearDesc(4, 64, 128, 0, 64, 128, 128)), None) == 1
+    for M, K, N, code in ((0, 64, 128, 2), (-1, 64, 128, 2), (4, 60, 128, 4), (4, 64, 1 << 21, 6)):
+        assert lib.mla_linear_query_cut(ctypes.byref(mla.LinearDesc(M, K, N, 0, 64, N, N)), ctypes.byref(cut)) == code
