@@ -4,6 +4,7 @@ page tables, the latent store, the matrix product with its epilogue, and a run o
 Tolerances count roundings.  A bf16 result is off by at most half a step, 2^-8 of its value (E4M3: 2^-4, and 2^-10 in
 units of the code among its subnormals); what is computed before that in fp32 adds a few times 2^-24 of the terms."""
 import math
+import threading
 
 import pytest
 import torch
@@ -1034,3 +1035,50 @@ def test_linear_every_form(form):
     stream = r.clone(memory_format=torch.contiguous_format)  # in place on the residual
     mla.linear(x, w, bias=b, residual=stream, act=mla.ACT_RELU, out=stream, status=status)
     assert torch.equal(stream, out[:, :N]) and int(status) == 0
+
+
+def test_calls_from_several_threads():
+    """Four threads, each on a stream of its own given as an argument, through one Problem, plan and set of weights: every
+    result is what the call gives alone."""
+    g = gen(121)
+    prob, plan = problem(6, 16, 2, d_c=128, d_rope=32, d_nope=64), mla.rope_plan(32)
+    q, at = randn(g, 6, 2, 16, 96).to(DEV), torch.arange(12, dtype=I32, device=DEV).view(6, 2)
+    x, w = randn(g, 8, 4104).to(DEV), randn(g, 4104, 20480, std=1 / 64).to(DEV)
+    x2, w2 = randn(g, 300, 520).to(DEV), randn(g, 520, 1032, std=1 / 23).to(DEV)
+    rows, norm = randn(g, 12, 160).to(DEV), randn(g, 128).to(DEV)
+    lens, table = torch.full((6,), 40, dtype=I32, device=DEV), torch.arange(6, dtype=I32, device=DEV).view(6, 1)
+    slots = (torch.arange(12, dtype=I32, device=DEV) * 29).contiguous()
+
+    def calls(stream):
+        with torch.cuda.stream(stream):
+            kv = torch.zeros(6, 64, 160, dtype=BF16, device=DEV)
+            pages, state = mla.Pages.empty(6, 4, 24)
+            old = torch.zeros(6, dtype=I32, device=DEV)
+            torch.cuda.current_stream().synchronize()
+        prob.scale = prob.scale  # fields set and structures made at the same time
+        n, r = mla.rope(prob, plan, q, positions=at, stream=stream)
+        y, y2 = mla.linear(x, w, stream=stream), mla.linear(x2, w2, act=mla.ACT_GELU, stream=stream)
+        mla.latent_store(prob, rows, mla.make_cache(prob, kv, lens, table, 64), plan=plan, norm_weight=norm, positions=at,
+                         slots=slots, stream=stream)
+        up = mla.pages_update(pages, state, old, lens, 240, stream=stream)
+        return n, r, y, y2, kv, up.slots, up.positions, up.ring_state, pages.block_table
+
+    alone = calls(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            kept = [calls(s) for _ in range(15)]
+            s.synchronize()
+            wrong.extend(k for got in kept for k, (a, b) in enumerate(zip(got, alone)) if not torch.equal(a, b))
+        except Exception as e:  # noqa: BLE001 - shown by the assertion below
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
