@@ -506,13 +506,16 @@ def _raw_stream(dev: int, stream) -> int:
     return stream.cuda_stream
 
 
-def _new(shape, stride, dtype, stream):
-    """A tensor for kernels on ``stream`` (None: the current one), from that stream's memory: what was freed there is
-    handed out again in the order of that stream's work alone."""
+def _allocator(stream):
+    """What makes tensors (shape, stride, dtype) for kernels on ``stream`` (None: the current one), from that stream's
+    memory: what was freed there is handed out again in the order of that stream's work alone."""
     if stream is None:
-        return _empty_strided_cuda(shape, stride, dtype)
-    with torch.cuda.stream(stream):
-        return _empty_strided_cuda(shape, stride, dtype)
+        return _empty_strided_cuda
+
+    def new(shape, stride, dtype):
+        with torch.cuda.stream(stream):
+            return _empty_strided_cuda(shape, stride, dtype)
+    return new
 
 
 def rope_plan(d_rope: int, layout: int = ROPE_INTERLEAVED, base: float = 10000.0, scaling: int = ROPE_PLAIN,
@@ -551,17 +554,17 @@ def rope(prob: Problem, plan: RopePlan, x, positions=None, seq_lens=None, q_nope
     token_stride = s1 if s_q > 1 else s0 if B > 1 else (H - 1) * head_stride + shape[3]
     pos = None if positions is None else _per_token(positions, "positions", dev, B * s_q)
     lens = None if seq_lens is None else _dense(seq_lens, "seq_lens", _I32, dev, (B,))
-    nope = None
+    nope, new = None, _allocator(stream)
     if split:
         if q_nope is None:
-            q_nope = _new((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), _BF16, stream)
+            q_nope = new((B, s_q, H, d_nope), (s_q * H * d_nope, H * d_nope, d_nope, 1), _BF16)
             nope = q_nope.data_ptr()
         else:
             nope = _dense(q_nope, "q_nope", _BF16, dev, (B, s_q, H, d_nope))
     elif q_nope is not None:
         raise ValueError("rows of d_rope values have no part for q_nope")
     if q_rope is None:
-        q_rope = _new((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), _BF16, stream)
+        q_rope = new((B, s_q, H, d_rope), (s_q * H * d_rope, H * d_rope, d_rope, 1), _BF16)
         turned = q_rope.data_ptr()
     else:
         turned = _dense(q_rope, "q_rope", _BF16, dev, (B, s_q, H, d_rope))
@@ -616,19 +619,22 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
     # the fields may have been assigned since the batch was made
     if table.dim() != 2 or ring.dim() != 1:
         raise ValueError("block_table must be [B, max_pages], free_ring [num_pages]")
+    if table.dtype != _I32 or not table.is_contiguous():
+        _refuse(table, "block_table", f"a dense int32 tensor on device {dev}")
+    if ring.dtype != _I32 or ring.get_device() != dev or not ring.is_contiguous():
+        _refuse(ring, "free_ring", f"a dense int32 tensor on device {dev}")
     B, max_pages = table.shape
-    to_table, to_ring = _dense(table, "block_table", _I32, dev, table.shape), _dense(ring, "free_ring", _I32, dev, ring.shape)
     state = _dense(ring_state, "ring_state", _I32, dev, (2,))
     old = _dense(old_lens, "old_lens", _I32, dev, (B,))
     new = _dense(new_lens, "new_lens", _I32, dev, (B,))
     word = None if status is None else _word(status, dev)
     if out is None:
-        one = (1,)
-        lens = _new((B,), one, _I32, stream)
-        state_out = _new((2,), one, _I32, stream)
-        start = _new((B + 1,), one, _I32, stream)
-        pos = _new((max_tokens,), one, _I32, stream)
-        slot = _new((max_tokens,), one, _I32, stream)
+        one, make = (1,), _allocator(stream)
+        lens = make((B,), one, _I32)
+        state_out = make((2,), one, _I32)
+        start = make((B + 1,), one, _I32)
+        pos = make((max_tokens,), one, _I32)
+        slot = make((max_tokens,), one, _I32)
         out = PagesStep(lens, state_out, start, pos, slot)
         lens, state_out, start = lens.data_ptr(), state_out.data_ptr(), start.data_ptr()
         pos, slot = pos.data_ptr(), slot.data_ptr()
@@ -638,7 +644,7 @@ def pages_update(pages: Pages, ring_state, old_lens, new_lens, max_tokens: int, 
         start = _dense(out.token_start, "token_start", _I32, dev, (B + 1,))
         pos = _dense(out.positions, "positions", _I32, dev, (max_tokens,))
         slot = _dense(out.slots, "slots", _I32, dev, (max_tokens,))
-    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], to_table, to_ring, state, state_out)
+    pool = PagePool(B, pages.page_size, max_pages, ring.shape[0], table.data_ptr(), ring.data_ptr(), state, state_out)
     code = lib.mla_pages_update(ctypes.byref(pool), old, new, max_tokens, lens, start, pos, slot, word,
                                 _raw_stream(dev, stream))
     if code:
@@ -697,7 +703,7 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
     res = None if residual is None else _rows(residual, "residual", dev, M, N)
     word = None if status is None else _word(status, dev)
     if out is None:
-        out = _new((M, N), (N, 1), _BF16, stream)
+        out = _allocator(stream)((M, N), (N, 1), _BF16)
         to, out_stride = out.data_ptr(), N
     else:
         to, out_stride = _rows(out, "out", dev, M, N), out.stride(0)
@@ -714,7 +720,7 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
         code = lib.mla_linear_status(at, rows, weight, b, res, to, None, 256, word, st)
         if code == _ERR_WORKSPACE:
             nbytes = lib.mla_linear_workspace_size(at)
-            workspace = _new((nbytes,), (1,), torch.uint8, stream)
+            workspace = _allocator(stream)((nbytes,), (1,), torch.uint8)
             code = lib.mla_linear_status(at, rows, weight, b, res, to, workspace.data_ptr(), nbytes, word, st)
     if code:
         raise MLAError(code, "mla_linear")
