@@ -8,9 +8,12 @@
 // the first and of the second half, trade one each, turn a pair each, and trade back.
 // A warp takes several tokens and has the next one's row under way.
 //
-// Bound by memory: 32768 rows of 576 values, 75.7 MB in 14.2 us = 5.3 TB/s = 0.79 of the
-// measured copy bandwidth, launch included (one warp a token without the loop: 19.7; two
-// bytes a lane for the key's halves: 15.9).  64 rows: 2.3 us, a launch and a round trip.
+// Bound by the rows' way through L2 with two of them under way a warp, not by HBM: of 32768
+// rows of 576 values DRAM reads the 38 MB that come in, what is written stays in L2.  In turn
+// over four sets of buffers (bf16, FP8; floors 11.1 and 8.3 us): 13.8 and 12.3 us with slots,
+// 14.5 and 14.7 into a contiguous cache by the lengths, 15.7 and 16.0 into a paged one, where a
+// row waits for its length and then for its page; the half layout 0.4 more.  On one set, in L2,
+// 10.9 and 11.7.  64 rows: 2.3 us, a launch and a round trip.
 #include "layer.h"
 #include "rope.cuh"
 #include "sm100.cuh"
@@ -19,7 +22,9 @@ namespace mla {
 namespace {
 
 constexpr int kWarps = 4;  // warps a CTA
-constexpr int kCtasPerSm = 7;  // as many as its registers allow: 15.9 us for 32768 rows of 576, 19.7 with 8
+// As many as the 72 registers of each variant allow: 32768 rows in L2 10.9 us, with 6 11.1, with
+// 8 11.9 (a second wave for the eighth), with 12 11.3, one warp a token without the loop 14.3.
+constexpr int kCtasPerSm = 7;
 
 // Two values as E4M3 codes (v0 in the low byte): nearest even, saturating at +-448.
 __device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {

@@ -28,11 +28,14 @@
 // instead of 48 (with the tokens as the MMA's rows, and rows written as they come or turned
 // over in bf16, 0 to 6 % slower).
 //
-// Measured (device time): 4096 x 16384 x 7168 in 507 us = 1,897 TFLOP/s = 0.98 of the measured
-// bf16 rate (tiles of 128 x 256 on single CTAs: 560), bound by the tensor cores; 64 x 16384 x
-// 7168 in 40 us, 235 MB of weights at 5.9 TB/s = 0.88 of the measured copy bandwidth, with 2 us
-// of start and 4 of exchange and epilogue around the stream; 333 x 1000 x 1544 in 7.6 us, a
-// chain of latencies: 1.4 us to the first chunk, 16 chunks of 0.21, 1.1 of epilogue.
+// Measured (device time): 4096 x 16384 x 7168 in 494 to 508 us for a dozen calls = 1,894 to 1,948
+// TFLOP/s, the measured bf16 rate (tiles of 128 x 256 on single CTAs: 560), bound by the tensor
+// cores, and in a long run of calls, as a prompt's layers make them, in 541 to 576 us = 1,670 to
+// 1,780 TFLOP/s, bound by the power limit, under which a library product sustains 1,713; 64 x
+// 16384 x 7168 in 39 to 40 us, 235 MB of weights at 5.9 TB/s = 0.88 of the measured copy
+// bandwidth, with 2 us of start and 4 of exchange and epilogue around the stream; 333 x 1000 x
+// 1544 in 7.4 us, a chain of latencies: 1.4 us to the first chunk, 16 chunks of 0.21, 1.1 of
+// epilogue.
 #include <atomic>
 
 #include "layer.h"
@@ -750,8 +753,10 @@ LinearPlan linear_plan(int M, int K, int N, int sms) {
         p.whole = true;
         for (p.cluster = 1; p.cluster <= 8; p.cluster *= 2) {
             if (p.cluster > 1 && (p.nk < 2 * p.cluster || tiles > sms)) break;
-            // clusters that fit the SMs: fewer than an even share (36 of 4, 15 of 8 on 152 SMs),
-            // as a cluster stays within one of the groups the SMs are built in
+            // clusters that fit the SMs: fewer than an even share, as a cluster stays within one of
+            // the groups the SMs are built in.  36 of 4 and 15 of 8 are what the occupancy query
+            // answers for 152 SMs; a device with other groups would get a worse estimate here,
+            // never a wrong result: clusters that do not fit wait for their turn
             const int fit = p.cluster == 1 ? sms : p.cluster == 2 ? sms / 2 : p.cluster == 4 ? sms / 4 - 2 : sms / 8 - 4;
             if (fit < 1) break;
             const long long waves = (tiles + fit - 1) / fit;
