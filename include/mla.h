@@ -32,6 +32,10 @@
  *   mla_latent_store the new tokens' latents normalised, their keys rotated, the
  *                    rows written to the cache's slots (bf16 or FP8)
  *   mla_linear       out = residual + act(x . W + bias)
+ *   mla_latent_load  cached rows, of whole histories or listed tokens, back as bf16
+ *   mla_quantize     activations (after their RMS norm) and weights as E4M3 codes
+ *                    with a scale for each block of 128
+ *   mla_linear_fp8   mla_linear of such codes
  * The latent cache is bf16 or FP8 (E4M3 codes with one scale per cache), see
  * mla_cache.
  *
@@ -103,9 +107,15 @@ typedef struct {
 /* Element formats of the latent cache (mla_cache.kv_dtype). */
 typedef enum {
     MLA_KV_BF16 = 0,  /* bf16 values */
-    MLA_KV_E4M3 = 1   /* OCP FP8 E4M3 codes (1 sign, 4 exponent bits with bias 7,
+    MLA_KV_E4M3 = 1,  /* OCP FP8 E4M3 codes (1 sign, 4 exponent bits with bias 7,
                          3 mantissa bits, no infinities, S.1111.111 = NaN); the
                          value is kv_scale * code */
+    MLA_KV_E4M3_BLOCKS = 3 /* (2 is no format) rows of mla_latent_row_bytes: d_c E4M3 codes of the
+                         latent, 4 fp32 scales, d_rope bf16 values of the key.  Value
+                         i of the latent is scale[i / 128] * code; scales of no value
+                         are 0.  kv_scale is not read, and seq_stride counts bytes.
+                         Taken by mla_latent_store and mla_latent_load alone: the
+                         attention reads what the latter gives */
 } mla_kv_dtype;
 
 /* The latent cache: one row [c_kv (d_c) | k_rope (d_rope)] per cached token,
@@ -515,7 +525,8 @@ MLA_API int mla_pages_update(const mla_page_pool *pool, const int *old_lens, con
  *   k' = k rotated by the token's position           (plan NULL: k' = k)
  * computed in fp32 and rounded once, to bf16 or to the E4M3 code of value times
  * 1 / kv_scale in fp32 (nearest even, saturated to +-448; NaN stays NaN; kv_scale
- * not below 2^-126, else MLA_ERR_UNSUPPORTED).  norm_weight bf16 [d_c].
+ * not below 2^-126, else MLA_ERR_UNSUPPORTED).  A cache of MLA_KV_E4M3_BLOCKS takes c'
+ * in blocks of 128 (the last may be 64) as mla_quantize does, and k' in bf16.  norm_weight bf16 [d_c].
  * Token t goes to row slots[t] of a paged pool (int32 [B][s_q], as
  * mla_pages_update gives them; a negative slot is skipped); slots NULL: to row
  * seq_lens[b] - s_q + i of sequence b, as mla_cache_append.  Two tokens of one call
@@ -579,6 +590,75 @@ MLA_API int mla_linear(const mla_linear_desc *desc, const void *x, const void *w
 MLA_API int mla_linear_status(const mla_linear_desc *desc, const void *x, const void *w, const void *bias,
                               const void *residual, void *out, void *workspace, size_t ws_bytes, int *status,
                               void *stream);
+
+/* Bytes of a row of an MLA_KV_E4M3_BLOCKS cache, d_c + 16 + 2 d_rope (656 at
+ * DeepSeek-V3 widths); 0 for widths mla_latent_store does not take. */
+MLA_API long long mla_latent_row_bytes(const mla_dims *dims);
+
+/* Cached rows back as bf16: for each sequence b and i < rows, with p =
+ * positions[b*rows + i], or i where positions is NULL,
+ *   out[b*out_stride + i*(d_c + d_rope) ...] = row of token p of sequence b
+ * (an FP8 value is scale * code in fp32, rounded once).  A row whose p is outside [0,
+ * seq_lens[b]) stays as it was, so that a list may be padded with -1.  out is then a
+ * contiguous bf16 cache of `rows` tokens a sequence (seq_stride = out_stride), which
+ * every entry point takes: whole histories for mla_prefill_expand, the tokens of a
+ * selector for mla_decode_attn (with the number of them as lengths).  The cache is of
+ * any mla_kv_dtype; of dims, B, d_c (a multiple of 64 up to 512) and d_rope (of 16 up to
+ * 64, or 0) are read.  out bf16, out_stride a multiple of 8.
+ * Recorded in status, the rows left as they were: MLA_ERR_SEQLEN (a length outside [0,
+ * capacity]), MLA_ERR_PAGE (a page outside the pool). */
+MLA_API int mla_latent_load(const mla_dims *dims, const mla_cache *cache, int rows, const int *positions, void *out,
+                            long long out_stride, int *status, void *stream);
+
+typedef struct {
+    int M;                  /* rows, at most 65535 * 128 */
+    int K;                  /* values a row, a multiple of 16 up to 2^20 */
+    int block_rows;         /* rows a scale stands for: 1 (activations) or 128 (weights) */
+    long long x_stride;     /* elements between rows of x, a multiple of 8, >= K */
+    long long code_stride;  /* bytes between rows of codes, a multiple of 16, >= K */
+    long long scale_stride; /* block_rows 1: floats between blocks of K, >= M;
+                               128: floats between blocks of rows, >= ceil(K / 128) */
+} mla_quantize_desc;
+
+/* bf16 values as E4M3 codes with one fp32 scale a block of block_rows rows x 128
+ * values (blocks at the ends may be smaller).  With y = x, or, given norm_weight
+ * (bf16 [K], block_rows 1 only), y[m, k] = x[m, k] / sqrt(mean_k(x^2) + eps) *
+ * norm_weight[k], in fp32, and A the largest |y| of the block, at least 2^-100:
+ *   scale = A / 448,   code = E4M3(y * (448 / A))      (nearest even, saturated)
+ * A NaN has the code NaN and leaves the other values of its block as they are; an infinity makes the
+ * scale of its block infinite (its values and the products they enter are then NaN).
+ * codes [M][K]; scales: block_rows 1: [ceil(K/128)][M], 128: [ceil(M/128)][ceil(K/128)],
+ * as mla_linear_fp8 takes them. */
+MLA_API int mla_quantize(const mla_quantize_desc *desc, const void *x, const void *norm_weight, float eps, void *codes,
+                         float *scales, void *stream);
+
+typedef struct {
+    int M;                     /* rows of x (tokens), at most 65535 * 128 */
+    int K;                     /* contraction width, a multiple of 16 up to 2^20 */
+    int N;                     /* output width, a multiple of 8 up to 2^20 */
+    int act;                   /* mla_act */
+    long long x_stride;        /* bytes between rows of x, a multiple of 16, >= K */
+    long long x_scale_stride;  /* floats between blocks of K in x_scale, >= M */
+    long long out_stride;      /* elements between rows of out and residual: */
+    long long residual_stride; /* multiples of 8, >= N (not read without a residual) */
+} mla_linear_fp8_desc;
+
+/* mla_linear of E4M3 codes with scales by blocks of 128, as mla_quantize gives them:
+ *   out[m, n] = residual[m, n] + act(sum_k x'[m, k] w'[n, k] + bias[n])
+ *   x'[m, k] = x_scale[k/128][m] * x[m, k],  w'[n, k] = w_scale[n/128][k/128] * w[n, k]
+ * The codes' products are summed block by block of K in fp32, and the scaled blocks
+ * in fp32 in the order of K (x_scale * w_scale of a block has to be finite); epilogue as
+ * mla_linear, one rounding to bf16.  x [M][K] and w [N][K] (dense; the rows are
+ * output columns) are codes, x_scale fp32 [ceil(K/128)][M], w_scale fp32 [ceil(N/128)]
+ * [ceil(K/128)]; bias [N], residual and out [M][N] bf16, as for mla_linear.  No
+ * workspace.  Results do not depend on the timing of the GPU.  A bounded device wait that runs
+ * out leaves NaN in the outputs it concerns and MLA_ERR_TIMEOUT in status. */
+MLA_API int mla_linear_fp8(const mla_linear_fp8_desc *desc, const void *x, const float *x_scale, const void *w,
+                           const float *w_scale, const void *bias, const void *residual, void *out, int *status,
+                           void *stream);
+
+/* How mla_linear_fp8 cuts a product on the current device.  Host only. */
+MLA_API int mla_linear_fp8_query_cut(const mla_linear_fp8_desc *desc, mla_linear_cut *cut);
 
 #ifdef __cplusplus
 }

@@ -14,24 +14,19 @@
 // 14.5 and 14.7 into a contiguous cache by the lengths, 15.7 and 16.0 into a paged one, where a
 // row waits for its length and then for its page; the half layout 0.4 more.  On one set, in L2,
 // 10.9 and 11.7.  64 rows: 2.3 us, a launch and a round trip.
-#include "layer.h"
+#include "quantize.cuh"
 #include "rope.cuh"
-#include "sm100.cuh"
 
 namespace mla {
 namespace {
+
+using quant::e4m3x2;
+using quant::unpack;
 
 constexpr int kWarps = 4;  // warps a CTA
 // As many as the 72 registers of each variant allow: 32768 rows in L2 10.9 us, with 6 11.1, with
 // 8 11.9 (a second wave for the eighth), with 12 11.3, one warp a token without the loop 14.3.
 constexpr int kCtasPerSm = 7;
-
-// Two values as E4M3 codes (v0 in the low byte): nearest even, saturating at +-448.
-__device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v1), "f"(v0));
-    return r;
-}
 
 // What a warp reads of one token before it can compute: the row, and where it goes.
 struct Row {
@@ -98,10 +93,12 @@ __device__ __forceinline__ Row load_row(const StoreArgs &a, int t, int lane) {
     return r;
 }
 
-// Element offset in the cache of token t's row, or -1: skipped, or recorded in status.
+// Offset in the cache of token t's row (elements; bytes in a cache of blocks), or -1: skipped, or
+// recorded in status.
+template <int kDtype>
 __device__ __forceinline__ long long row_offset(const StoreArgs &a, Row &r, int t, int lane) {
     const AttnParams &c = a.cache;
-    const long long W = a.d_c + a.d_rope;
+    const long long W = kDtype == MLA_KV_E4M3_BLOCKS ? a.d_c + quant::kScaleBytes + 2 * a.d_rope : a.d_c + a.d_rope;
     int error = 0;
     long long at = -1;
     if (a.slots && r.slot < 0) return -1;
@@ -131,12 +128,9 @@ __device__ __forceinline__ long long row_offset(const StoreArgs &a, Row &r, int 
     return at;
 }
 
-__device__ __forceinline__ float2 unpack(uint32_t v) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
-}
-
-template <bool kFp8, bool kHalf>
+template <int kDtype, bool kHalf>
 __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant__ StoreArgs a) {
+    constexpr bool kFp8 = kDtype == MLA_KV_E4M3;
     const int lane = threadIdx.x % 32, nw = gridDim.x * kWarps;
     const int nc = a.d_c / 8;
     const KeyLane<kHalf> key(lane, a.d_rope / 2);
@@ -165,7 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
         const bool more = next < a.tokens;
         Row r = row;
         if (more) row = load_row<kHalf>(a, next, lane);  // on its way while this row is computed
-        const long long at = row_offset(a, r, t, lane);
+        const long long at = row_offset<kDtype>(a, r, t, lane);
         if (at >= 0) {
             float2 f[2][4], sum2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -197,7 +191,21 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
                 k = rope_turn(k.x, k.y, rope_cos_sin(turn, r.pos, a.plan.mscale, 1.f));
                 k = key.trade(k, lane);
             }
-            if (kFp8) {
+            if (kDtype == MLA_KV_E4M3_BLOCKS) {
+                // 16 lanes hold a block of the latent; the key keeps bf16
+                uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float v[8] = {f[i][0].x, f[i][0].y, f[i][1].x, f[i][1].y, f[i][2].x, f[i][2].y, f[i][3].x, f[i][3].y};
+                    const float top = fmaxf(quant::top16(quant::top8(v)), quant::kLeast);
+                    const int c = lane + 32 * i;
+                    if (c < nc) *(reinterpret_cast<uint2 *>(dst) + c) = quant::codes8(v, __fdiv_rn(quant::kTop, top));
+                    if ((lane & 15) == 0)
+                        *(reinterpret_cast<float *>(dst + a.d_c) + c / 16) = c < nc ? __fdiv_rn(top, quant::kTop) : 0.f;
+                }
+                if (key.active)
+                    *reinterpret_cast<uint32_t *>(dst + a.d_c + quant::kScaleBytes + 2 * key.at) = sm100::pack_bf16x2(k.x, k.y);
+            } else if (kFp8) {
                 uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -233,13 +241,13 @@ cudaError_t launch_latent_store(const StoreArgs &a, cudaStream_t st) {
     int grid = (a.tokens + kWarps - 1) / kWarps;
     if (grid > layer_num_sms() * kCtasPerSm) grid = layer_num_sms() * kCtasPerSm;
     const bool half = a.rotate && a.plan.layout == MLA_ROPE_HALF;
-    if (a.cache.kv_fp8) {
-        if (half) latent_rows<true, true><<<grid, 32 * kWarps, 0, st>>>(a);
-        else latent_rows<true, false><<<grid, 32 * kWarps, 0, st>>>(a);
-    } else {
-        if (half) latent_rows<false, true><<<grid, 32 * kWarps, 0, st>>>(a);
-        else latent_rows<false, false><<<grid, 32 * kWarps, 0, st>>>(a);
-    }
+    auto launch = [&](auto with_half, auto without) {
+        if (half) with_half<<<grid, 32 * kWarps, 0, st>>>(a);
+        else without<<<grid, 32 * kWarps, 0, st>>>(a);
+    };
+    if (a.dtype == MLA_KV_E4M3_BLOCKS) launch(latent_rows<MLA_KV_E4M3_BLOCKS, true>, latent_rows<MLA_KV_E4M3_BLOCKS, false>);
+    else if (a.dtype == MLA_KV_E4M3) launch(latent_rows<MLA_KV_E4M3, true>, latent_rows<MLA_KV_E4M3, false>);
+    else launch(latent_rows<MLA_KV_BF16, true>, latent_rows<MLA_KV_BF16, false>);
     return cudaGetLastError();
 }
 

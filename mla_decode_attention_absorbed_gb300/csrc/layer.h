@@ -29,11 +29,37 @@ struct StoreArgs {
     float eps;
     int rotate;
     const int *positions, *slots;
+    int dtype;         // mla_kv_dtype
     AttnParams cache;  // the cache's fields and the lengths
     int *status;
     mla_rope_plan plan;
 };
 cudaError_t launch_latent_store(const StoreArgs &a, cudaStream_t st);
+
+struct LoadArgs {
+    int rows, d_c, width;  // rows a sequence; width: d_c + d_rope
+    int dtype;             // mla_kv_dtype
+    const int *positions;  // [B][rows], or NULL: row i is token i
+    __nv_bfloat16 *out;
+    long long out_stride;  // elements between sequences
+    long long row_bytes, seq_bytes;
+    AttnParams cache;  // the cache's fields and the lengths
+    int *status;
+};
+cudaError_t launch_latent_load(const LoadArgs &a, cudaStream_t st);
+
+struct QuantizeArgs {
+    int M, K, block_rows;
+    const __nv_bfloat16 *x;
+    long long x_stride;
+    const __nv_bfloat16 *weight;  // NULL: no norm
+    float eps;
+    uint8_t *codes;
+    long long code_stride;
+    float *scales;
+    long long scale_stride;
+};
+cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t st);
 
 struct PagesArgs {
     int B, page_size, max_pages, num_pages, max_tokens;
@@ -69,6 +95,23 @@ struct LinearPlan {
 LinearPlan linear_plan(int M, int K, int N, int sms);
 size_t linear_workspace_bytes(const LinearPlan &p);
 cudaError_t launch_linear(const LinearArgs &a, const LinearPlan &p, cudaStream_t st);
+
+// x and w hold codes
+struct LinearFp8Args : LinearArgs {
+    const float *x_scale, *w_scale;  // [K / 128][x_scale_stride], [N / 128][K / 128]
+    long long x_scale_stride;
+};
+// How a product of codes is cut (see linear_fp8.cu).
+struct LinearFp8Plan {
+    int columns;           // of a tile a CTA accumulates, for 128 tokens
+    int tiles_m, tiles_n;  // tile t: tokens t % tiles_m, columns t / tiles_m
+    int nk;                // blocks of K
+    int grid;
+    int cluster;           // CTAs, or pairs of them, that share a tile's K (1: none)
+    bool pair;             // a tile is 256 tokens x 256 columns, taken by a pair of CTAs
+};
+LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms);
+cudaError_t launch_linear_fp8(const LinearFp8Args &a, const LinearFp8Plan &p, cudaStream_t st);
 
 // SMs of the current device (work plans only), looked up once per device.
 int layer_num_sms();

@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kMaxTokens = 65535 * 128;
 constexpr int kMaxWidth = 1 << 20;
-constexpr unsigned long long kWaitNs = 2000000000ull;  // bound of mla_linear's waits for work unless one is set
+constexpr unsigned long long kWaitNs = 2000000000ull;  // bound of the products' waits for work unless one is set
 
 bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -50,14 +50,23 @@ bool good_plan(const mla_rope_plan *p) {
            (p->layout == MLA_ROPE_INTERLEAVED || p->layout == MLA_ROPE_HALF);
 }
 
-// A cache that rows are written to.
+// Widths of the latent rows the store and the load take.
+int check_widths(const mla_dims *d) {
+    if (d->d_c < 1 || d->d_rope < 0) return MLA_ERR_SHAPE;
+    if (d->d_c % 64 || d->d_c > 512 || d->d_rope % 16 || d->d_rope > 64) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+// A cache that rows are written to or read back from.
 int check_store_cache(const mla_dims *d, const mla_cache *c) {
     if (!c) return MLA_ERR_NULL;
     if (d->B == 0) return MLA_OK;
     if (!c->kv || !c->seq_lens) return MLA_ERR_NULL;
     if (!aligned(c->kv, 16) || !aligned(c->seq_lens, 4)) return MLA_ERR_ALIGN;
-    const long long W = d->d_c + d->d_rope;
-    if (c->kv_dtype != MLA_KV_BF16 && c->kv_dtype != MLA_KV_E4M3) return MLA_ERR_UNSUPPORTED;
+    const bool blocks = c->kv_dtype == MLA_KV_E4M3_BLOCKS;
+    const long long W = blocks ? mla_latent_row_bytes(d) : d->d_c + d->d_rope;  // of a row, in units of seq_stride
+    if (c->kv_dtype != MLA_KV_BF16 && c->kv_dtype != MLA_KV_E4M3 && !blocks) return MLA_ERR_UNSUPPORTED;
+    if (blocks && !c->block_table && c->seq_stride % 16) return MLA_ERR_ALIGN;
     if (c->kv_dtype == MLA_KV_E4M3) {
         if (!(c->kv_scale > 0.f) || c->kv_scale > 3.0e38f) return MLA_ERR_SHAPE;
         if (c->kv_scale < 1.1754944e-38f) return MLA_ERR_UNSUPPORTED;  // 1 / kv_scale has to be finite
@@ -76,6 +85,21 @@ int check_store_cache(const mla_dims *d, const mla_cache *c) {
     return MLA_OK;
 }
 
+void fill_cache(const mla_dims &d, const mla_cache &c, mla::AttnParams &p) {
+    p.B = d.B;
+    p.s_q = d.s_q;
+    p.kv = c.kv;
+    p.kv_fp8 = c.kv_dtype == MLA_KV_E4M3;
+    p.kv_scale = p.kv_fp8 ? c.kv_scale : 1.f;
+    p.seq_stride = c.seq_stride;
+    p.capacity = c.block_table ? c.max_pages * c.page_size : c.capacity;
+    p.block_table = c.block_table;
+    p.max_pages = c.max_pages;
+    p.page_size = c.page_size;
+    p.num_pages = c.num_pages;
+    p.seq_lens = c.seq_lens;
+}
+
 int check_pool(const mla_page_pool *p, int max_tokens) {
     if (!p) return MLA_ERR_NULL;
     if (p->B < 0 || p->page_size < 1 || p->max_pages < 1 || p->num_pages < 1 || max_tokens < 0) return MLA_ERR_SHAPE;
@@ -83,6 +107,38 @@ int check_pool(const mla_page_pool *p, int max_tokens) {
     if ((long long)p->max_pages * p->page_size > (1ll << 30)) return MLA_ERR_UNSUPPORTED;
     if ((long long)p->num_pages * p->page_size > 0x7fffffffll) return MLA_ERR_UNSUPPORTED;
     return MLA_OK;
+}
+
+int check_quantize(const mla_quantize_desc *d) {
+    if (!d) return MLA_ERR_NULL;
+    if (d->M < 0 || d->K < 1) return MLA_ERR_SHAPE;
+    if (d->block_rows != 1 && d->block_rows != 128) return MLA_ERR_UNSUPPORTED;
+    if (d->M > kMaxTokens || d->K > kMaxWidth) return MLA_ERR_UNSUPPORTED;
+    if (d->K % 16) return MLA_ERR_ALIGN;
+    if (d->x_stride < d->K || d->code_stride < d->K) return MLA_ERR_SHAPE;
+    if (d->scale_stride < (d->block_rows == 1 ? d->M : (d->K + 127) / 128)) return MLA_ERR_SHAPE;
+    if (d->x_stride % 8 || d->code_stride % 16) return MLA_ERR_ALIGN;
+    return MLA_OK;
+}
+
+int check_linear_fp8(const mla_linear_fp8_desc *d, bool residual) {
+    if (!d) return MLA_ERR_NULL;
+    if (d->M < 0 || d->K < 1 || d->N < 1) return MLA_ERR_SHAPE;
+    if (d->act < MLA_ACT_NONE || d->act > MLA_ACT_GELU_TANH) return MLA_ERR_UNSUPPORTED;
+    if (d->M > kMaxTokens || d->K > kMaxWidth || d->N > kMaxWidth) return MLA_ERR_UNSUPPORTED;
+    if (d->K % 16 || d->N % 8) return MLA_ERR_ALIGN;
+    if (d->x_stride < d->K || d->x_scale_stride < d->M || d->out_stride < d->N || (residual && d->residual_stride < d->N))
+        return MLA_ERR_SHAPE;
+    if (d->x_stride % 16 || d->out_stride % 8 || (residual && d->residual_stride % 8)) return MLA_ERR_ALIGN;
+    // a tensor map's strides stay below 2^40 bytes
+    if (d->x_stride > (1ll << 39) || d->out_stride > (1ll << 38) || (residual && d->residual_stride > (1ll << 38)))
+        return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+unsigned long long wait_ns() {
+    const unsigned long long ns = mla::wait_limit_ns();
+    return ns == 0 ? kWaitNs : ns < (1ull << 61) ? ns : 1ull << 61;  // twice that are cycles
 }
 
 int check_linear(const mla_linear_desc *d, bool residual) {
@@ -229,8 +285,7 @@ MLA_API int mla_latent_store(const mla_dims *dims, const mla_rope_plan *plan, co
                              const mla_cache *cache, int *status, void *stream) {
     int s = check_tokens(dims);
     if (s) return s;
-    if (dims->d_c < 1 || dims->d_rope < 0) return MLA_ERR_SHAPE;
-    if (dims->d_c % 64 || dims->d_c > 512 || dims->d_rope % 16 || dims->d_rope > 64) return MLA_ERR_UNSUPPORTED;
+    if ((s = check_widths(dims))) return s;
     if (plan && !good_plan(plan)) return MLA_ERR_UNSUPPORTED;
     if (plan && plan->d_rope != dims->d_rope) return MLA_ERR_SHAPE;
     if (norm_weight && (!(eps >= 0.f) || !isfinite(eps))) return MLA_ERR_SHAPE;
@@ -260,18 +315,8 @@ MLA_API int mla_latent_store(const mla_dims *dims, const mla_rope_plan *plan, co
     a.slots = slots;
     a.status = status;
     if (plan) a.plan = *plan;
-    mla::AttnParams &p = a.cache;
-    p.s_q = dims->s_q;
-    p.kv = cache->kv;
-    p.kv_fp8 = cache->kv_dtype == MLA_KV_E4M3;
-    p.kv_scale = p.kv_fp8 ? cache->kv_scale : 1.f;
-    p.seq_stride = cache->seq_stride;
-    p.capacity = cache->block_table ? cache->max_pages * cache->page_size : cache->capacity;
-    p.block_table = cache->block_table;
-    p.max_pages = cache->max_pages;
-    p.page_size = cache->page_size;
-    p.num_pages = cache->num_pages;
-    p.seq_lens = cache->seq_lens;
+    a.dtype = cache->kv_dtype;
+    fill_cache(*dims, *cache, a.cache);
     return result(mla::launch_latent_store(a, as_stream(stream)));
 }
 
@@ -327,9 +372,105 @@ MLA_API int mla_linear_status(const mla_linear_desc *d, const void *x, const voi
     a.residual_stride = d->residual_stride;
     a.part = (float *)workspace;
     a.status = status;
-    const unsigned long long ns = mla::wait_limit_ns();
-    a.wait_ns = ns == 0 ? kWaitNs : ns < (1ull << 61) ? ns : 1ull << 61;  // twice that are cycles
+    a.wait_ns = wait_ns();
     return result(mla::launch_linear(a, plan, as_stream(stream)));
+}
+
+MLA_API long long mla_latent_row_bytes(const mla_dims *dims) {
+    if (!dims || check_widths(dims)) return 0;
+    return dims->d_c + 16 + 2 * dims->d_rope;
+}
+
+MLA_API int mla_latent_load(const mla_dims *dims, const mla_cache *cache, int rows, const int *positions, void *out,
+                            long long out_stride, int *status, void *stream) {
+    int s = check_tokens(dims);
+    if (s) return s;
+    if ((s = check_widths(dims))) return s;
+    if ((s = check_store_cache(dims, cache))) return s;
+    const long long W = dims->d_c + dims->d_rope;
+    if (rows < 0 || out_stride < rows * W) return MLA_ERR_SHAPE;
+    if (rows > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+    if (out_stride % 8) return MLA_ERR_ALIGN;
+    if (dims->B == 0 || rows == 0) return MLA_OK;
+    if (!out) return MLA_ERR_NULL;
+    if (!aligned(out, 16) || !aligned(positions, 4) || !aligned(status, 4)) return MLA_ERR_ALIGN;
+    if (out == cache->kv) return MLA_ERR_UNSUPPORTED;
+    mla::LoadArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.d_c = dims->d_c;
+    a.width = (int)W;
+    a.dtype = cache->kv_dtype;
+    a.positions = positions;
+    a.out = (__nv_bfloat16 *)out;
+    a.out_stride = out_stride;
+    a.row_bytes = a.dtype == MLA_KV_BF16 ? 2 * W : a.dtype == MLA_KV_E4M3 ? W : mla_latent_row_bytes(dims);
+    a.seq_bytes = cache->seq_stride * (a.dtype == MLA_KV_BF16 ? 2 : 1);
+    fill_cache(*dims, *cache, a.cache);
+    a.status = status;
+    return result(mla::launch_latent_load(a, as_stream(stream)));
+}
+
+MLA_API int mla_quantize(const mla_quantize_desc *d, const void *x, const void *norm_weight, float eps, void *codes,
+                         float *scales, void *stream) {
+    const int s = check_quantize(d);
+    if (s) return s;
+    if (norm_weight && d->block_rows != 1) return MLA_ERR_UNSUPPORTED;
+    if (norm_weight && (!(eps >= 0.f) || !isfinite(eps))) return MLA_ERR_SHAPE;
+    if (d->M == 0) return MLA_OK;
+    if (!x || !codes || !scales) return MLA_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(norm_weight, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MLA_ERR_ALIGN;
+    if (codes == x || scales == x || (const void *)scales == codes) return MLA_ERR_UNSUPPORTED;
+    const mla::QuantizeArgs a{d->M, d->K, d->block_rows, (const __nv_bfloat16 *)x, d->x_stride,
+                              (const __nv_bfloat16 *)norm_weight, eps, (uint8_t *)codes, d->code_stride, scales,
+                              d->scale_stride};
+    return result(mla::launch_quantize(a, as_stream(stream)));
+}
+
+MLA_API int mla_linear_fp8_query_cut(const mla_linear_fp8_desc *d, mla_linear_cut *cut) {
+    const int s = check_linear_fp8(d, false);
+    if (s) return s;
+    if (!cut) return MLA_ERR_NULL;
+    if (d->M == 0) return MLA_ERR_SHAPE;
+    const mla::LinearFp8Plan p = mla::linear_fp8_plan(d->M, d->K, d->N, mla::layer_num_sms());
+    *cut = mla_linear_cut{p.pair ? 256 : 128, p.columns, p.cluster, 0, p.grid};
+    return MLA_OK;
+}
+
+MLA_API int mla_linear_fp8(const mla_linear_fp8_desc *d, const void *x, const float *x_scale, const void *w,
+                           const float *w_scale, const void *bias, const void *residual, void *out, int *status,
+                           void *stream) {
+    const int s = check_linear_fp8(d, residual != nullptr);
+    if (s) return s;
+    if (d->M == 0) return MLA_OK;
+    if (!x || !x_scale || !w || !w_scale || !out) return MLA_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16) ||
+        !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(status, 4))
+        return MLA_ERR_ALIGN;
+    if (out == x || out == w || (out == residual && d->M > 1 && d->out_stride != d->residual_stride))
+        return MLA_ERR_UNSUPPORTED;
+    mla::LinearFp8Args a;
+    memset(&a, 0, sizeof a);
+    a.M = d->M;
+    a.K = d->K;
+    a.N = d->N;
+    a.act = d->act;
+    a.x = (const __nv_bfloat16 *)x;
+    a.w = (const __nv_bfloat16 *)w;
+    a.bias = (const __nv_bfloat16 *)bias;
+    a.residual = (const __nv_bfloat16 *)residual;
+    a.out = (__nv_bfloat16 *)out;
+    a.x_stride = d->x_stride;
+    a.out_stride = d->out_stride;
+    a.residual_stride = d->residual_stride;
+    a.status = status;
+    a.wait_ns = wait_ns();
+    a.x_scale = x_scale;
+    a.w_scale = w_scale;
+    a.x_scale_stride = d->x_scale_stride;
+    const mla::LinearFp8Plan plan = mla::linear_fp8_plan(d->M, d->K, d->N, mla::layer_num_sms());
+    if (plan.grid == 0) return MLA_ERR_UNSUPPORTED;
+    return result(mla::launch_linear_fp8(a, plan, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,603 @@
+// out = residual + act(x . W^T + bias) of E4M3 codes with a scale for each 128 values of a row of x
+// and for each 128 x 128 values of W, on the 5th-generation tensor cores (tcgen05, kind::f8f6f4).
+//
+// With block b of K holding the values [128 b, 128 b + 128),
+//   sum_k x[m, k] W[n, k] = sum_b sx[b, m] sw[n / 128, b] sum_{k in b} cx[m, k] cw[n, k],
+// so the tensor cores' sum ends with each block: block b's product of the codes goes to one of two
+// accumulators in tensor memory, and while the MMAs fill the other one, eight warps take it from
+// there, times its scale, into the tile's fp32 sums, which stay in their registers.  The MMA's rows
+// are the tokens and its columns those of the output: a lane then has one token, a warp's columns lie
+// in one block of W, and a value costs half an instruction (two fp32 multiply-adds each).
+//
+// A tile is 128 tokens x 64 or 128 columns on one CTA, or 256 x 256 on a pair of CTAs, each of which
+// loads half of both operands and holds the sums of its 128 tokens.  K runs in blocks of 128 through
+// a ring of TMA stages.  The CTAs take whole tiles one after another, or, where there are few tiles,
+// the 2, 4 or 8 CTAs (or pairs) of a cluster take equal parts of a tile's K, exchange their sums through
+// distributed shared memory and finish a share of its columns each.  Parts are added in the order of K,
+// so results do not depend on timing.
+//
+// Warps: 0 issues the loads, 1 the MMAs, 4-11 hold the sums.
+#include <atomic>
+
+#include "layer.h"
+#include "linear_common.cuh"
+#include "tmap.h"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+using namespace product;
+
+constexpr int kRows = 128;  // tokens a CTA
+constexpr int kBK = 128;    // values, and bytes, of K a stage: a block
+constexpr int kThreads = 384;
+constexpr int kSumWarps = 8;  // two for each quarter of the tokens, half of the columns each
+constexpr int kFirstSum = 4;  // the first of them
+// Registers: the launch's 384 x 168 are dealt out anew, 128 of them a lane for the sums alone.
+constexpr int kRegSum = 216, kRegOther = 72;
+static_assert(2 * kRegSum + kRegOther == 3 * 168, "the split must equal the launch's total");
+
+template <int kValue>
+struct Act {
+    static constexpr int value = kValue;
+};
+
+using Plan = LinearFp8Plan;
+
+template <int kCols, bool kPair>
+struct Smem {
+    static constexpr int kXBytes = kRows * kBK;
+    static constexpr int kWBytes = (kPair ? kCols / 2 : kCols) * kBK;
+    static constexpr int kStage = kXBytes + kWBytes;
+    static constexpr int kTile = kRows * kCols * 2;  // the output's tile: slabs of 64 columns, 128 bytes a token
+    static constexpr int kStages = (227 * 1024 - 2048 - kTile) / kStage;
+    static constexpr int kBytes = kStages * kStage + kTile + 1024 /* barriers */ + 1024 /* alignment */;
+    static constexpr uint32_t kTmemCols = 2 * kCols;
+    static constexpr int kParts = kPair ? 2 : 1;  // of a block's accumulator, see the MMA warp
+    // a cluster's sums are exchanged in the ring, rows of share + 4 floats
+    static_assert(kRows * (kCols + 4 * 8) * 4 <= kStages * kStage, "exchange");
+    static_assert(kBytes <= 232448, "shared memory over the per-CTA limit");
+};
+
+// Instruction descriptor of kind::f8f6f4 with E4M3 A and B (formats 0), both K-major, fp32 D.
+constexpr uint32_t idesc_e4m3(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+
+template <bool kPair>
+__device__ __forceinline__ void mma_codes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+
+// Waits for the tensor-memory loads issued so far; r passes through it, so that no use of the
+// loaded values can be moved before it.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void fma2(float &a, float &b, uint32_t x, uint32_t y, float s) {
+    asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %4};\n\tfma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}" : "+f"(a), "+f"(b) : "r"(x), "r"(y), "f"(s));
+}
+// sums += scale * the kWide columns of tensor memory at taddr; the next 16 are on their way
+// while 16 are added.
+template <int kWide>
+__device__ __forceinline__ void add_block(float (&sums)[kWide], uint32_t taddr, float scale) {
+    uint32_t r0[16], r1[16];
+    tmem_ld16(taddr, r0);
+#pragma unroll
+    for (int c = 0; c < kWide; c += 32) {
+        tmem_ld_wait16(r0);
+        tmem_ld16(taddr + c + 16, r1);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) fma2(sums[c + e], sums[c + e + 1], r0[e], r0[e + 1], scale);
+        tmem_ld_wait16(r1);
+        if (c + 32 < kWide) tmem_ld16(taddr + c + 32, r0);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) fma2(sums[c + 16 + e], sums[c + 17 + e], r1[e], r1[e + 1], scale);
+    }
+}
+
+// The epilogue of 32 columns of a token, from its fp32 sums: `row` is the token's row of the slab
+// that holds them (16-byte chunk c at c ^ swz), with the residual in it if there is one; the result
+// takes its place.  n: the first column; columns at N and behind are not stored.
+template <int kAct>
+__device__ __forceinline__ void finish_columns(const LinearArgs &a, const float *sums, uint8_t *row, int first_chunk, int swz,
+                                               int n) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        uint4 *at = reinterpret_cast<uint4 *>(row + (((first_chunk + g) ^ swz) << 4));
+        float y[8], f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = sums[8 * g + e];
+        if (a.bias && n + 8 * g < a.N) {
+            Finish::unpack8(__ldg(reinterpret_cast<const uint4 *>(a.bias + n + 8 * g)), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += f[e];
+        }
+        activate_all<kAct>(y);
+        if (a.residual) {
+            Finish::unpack8(*at, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] += f[e];
+        }
+        *at = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// "The accumulator was taken", across the pair.  Nothing in memory goes with it (what was read is in
+// registers), so neither side orders memory: an arrival that does waits for all that the warp has under
+// way (.release.cluster: 4096 x 16384 x 7168 875 us, without 488).
+__device__ __forceinline__ void arrive_taken(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool try_taken(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ int ctas_a_tile(const Plan &p) { return p.pair ? 2 * p.cluster : p.cluster; }
+
+template <int kCols, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_fp8_tc(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                  const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
+                  const __grid_constant__ LinearFp8Args a, const __grid_constant__ Plan plan) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using L = Smem<kCols, kPair>;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTile);
+    uint64_t *empty = full + L::kStages;
+    uint64_t *acc_full = empty + L::kStages;  // [block's parity][part]
+    uint64_t *acc_empty = acc_full + 4;
+    uint64_t *drain = acc_empty + 4;
+    uint64_t *tile_free = drain + 1;  // the tile's memory holds the residual, or nothing that is needed
+    uint64_t *tile_done = tile_free + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tile_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    // a pair's: whether some pair of the cluster gave up, and the stages the other CTA issued
+    volatile int *gave_up = abort_flag + 1;
+    volatile uint32_t *peer_issued = reinterpret_cast<volatile uint32_t *>(gave_up + 1);
+    const Patience patience{a.wait_ns, abort_flag};
+    const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], (kPair ? 2 : 1) * kSumWarps / L::kParts);
+        }
+        mbar_init(tile_free, 1);
+        mbar_init(tile_done, kSumWarps);
+        mbar_init(drain, 1);
+        *abort_flag = *gave_up = 0;
+        *peer_issued = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_w);
+    }
+    if (warp == 1) {
+        if (kPair) tmem_alloc_pair<L::kTmemCols>(tmem_slot);
+        else tmem_alloc<L::kTmemCols>(tmem_slot);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (kPair) cluster_sync();  // the leader's barriers are ready for the other CTA
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    constexpr int kTileM = kPair ? 2 * kRows : kRows;
+    const int half = kPair ? (int)(blockIdx.x & 1) : 0;
+    const uint32_t leader = kPair ? cluster_rank() & ~1u : 0, both = 3u << leader;
+    // this CTA's tiles, and its blocks of each (a cluster's CTAs: a part of one tile's)
+    const int part = blockIdx.x % ctas_a_tile(plan) / (kPair ? 2 : 1);
+    const int tiles = plan.tiles_m * plan.tiles_n, first_tile = blockIdx.x / ctas_a_tile(plan);
+    const int tile_step = plan.grid / ctas_a_tile(plan);
+    const int k0 = (int)((long long)plan.nk * part / plan.cluster), k1 = (int)((long long)plan.nk * (part + 1) / plan.cluster);
+    uint32_t issued = 0;  // the load warp's stages
+
+    // The loads' and the MMAs' loops are run by whole warps on values that are the same in
+    // every lane, and one elected lane issues: the operands stay in uniform registers.
+    if (warp < kFirstSum) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
+        if (warp == 0) {
+            const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), leader) : 0;
+            uint32_t s = 0, phase = 1;
+            bool ok = true, free = mbar_test_wait(&empty[0], 1);
+            for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
+                const int t0 = tile % plan.tiles_m * kTileM + half * kRows;
+                const int n0 = tile / plan.tiles_m * kCols + half * 64;
+                for (int kc = k0; kc < k1; ++kc) {
+                    // the first round's waits are for the phase before the barriers' first: over at once
+                    if (!warp_wait(free, &empty[s], phase, patience)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = smem + s * L::kStage;
+                    uint64_t *bar = &full[s];
+                    const uint32_t lead = lead_full + s * 8;
+                    if (++s == L::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    free = mbar_test_wait(&empty[s], phase);
+                    if (elect_one()) {
+                        if (kPair) {
+                            if (half == 0) mbar_arrive_expect_tx(bar, 2 * L::kStage);
+                            tma_load_2d_pair(st, &tm_x, lead, kc * kBK, t0);
+                            // the first 128 columns' half, and the second's
+                        tma_load_2d_pair(st + L::kXBytes, &tm_w, lead, kc * kBK, n0);
+                        tma_load_2d_pair(st + L::kXBytes + 64 * kBK, &tm_w, lead, kc * kBK, n0 + 128);
+                        } else {
+                            mbar_arrive_expect_tx(bar, L::kStage);
+                            tma_load_2d(st, &tm_x, bar, kc * kBK, t0);
+                            tma_load_2d(st + L::kXBytes, &tm_w, bar, kc * kBK, n0);
+                        }
+                    }
+                    ++issued;
+                }
+            }
+            // The copies in flight land in this CTA's shared memory.  A pair's are counted by the
+            // leader, both halves of a stage together; where it does not see them all, the
+            // cluster's CTAs settle it after their next barrier.
+            const uint32_t tail = issued > L::kStages ? issued - L::kStages : 0;
+            if (!kPair) {
+                for (uint32_t i = tail; i < issued; ++i) ok &= mbar_wait(&full[i % L::kStages], (i / L::kStages) & 1);
+                if (!ok) *abort_flag = 1;
+            } else if (half == 0) {
+                for (uint32_t i = tail; i < issued; ++i)
+                    ok = ok && warp_wait(false, &full[i % L::kStages], (i / L::kStages) & 1, patience);
+                if (!ok && lane < 2 * plan.cluster) st_cluster_u32(map_to_rank(smem_u32((const void *)gave_up), lane), 1);
+            } else if (lane == 0) {
+                st_cluster_u32(map_to_rank(smem_u32((const void *)peer_issued), leader), issued);
+            }
+            __syncwarp();
+        } else if (warp == 1 && half == 0) {
+            // A block's MMAs are issued for 128 columns of a pair's tile at a time, each with a barrier
+            // of their own: the sums' warps of those columns take them while the others' are computed, and
+            // the MMAs wait for a quarter of the tensor memory at a time.
+            constexpr uint32_t idesc = idesc_e4m3(kTileM, kCols / L::kParts);
+            // descriptors of stage 0: a stage and a step of K move the start address (in 16 bytes)
+            const uint64_t x_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+            const uint64_t w_desc = smem_desc_sw128(smem_u32(smem) + L::kXBytes, 16, 1024);
+            const uint32_t acc0 = __shfl_sync(~0u, tmem, 0);
+            uint32_t s = 0, phase = 0, n = 0;  // n: blocks issued
+            bool ok = true, there = false;
+            for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
+                for (int kc = k0; ok && kc < k1; ++kc, ++n) {
+                    const uint32_t b = n & 1, taken = (n / 2 - 1) & 1;
+                    if (!warp_wait(there, &full[s], phase, patience)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t dx = x_desc + (uint64_t)(s * (L::kStage >> 4)), dw = w_desc + (uint64_t)(s * (L::kStage >> 4));
+                    uint64_t *bar = &empty[s];
+                    if (++s == L::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    there = mbar_test_wait(&full[s], phase);  // its answer comes while the MMAs are issued
+#pragma unroll
+                    for (int h = 0; h < L::kParts; ++h) {
+                        uint64_t *mine = &acc_empty[2 * b + h];
+                        if (n >= 2 && !warp_wait<kPair>(try_taken(mine, taken), mine, taken, patience)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < kBK / 32; ++kk)
+                                mma_codes<kPair>(acc0 + b * kCols + h * 128, dx + kk * (32 >> 4),
+                                                 dw + h * (64 * kBK >> 4) + kk * (32 >> 4), idesc, kk > 0);
+                            if (kPair) {
+                                mma_commit_pair(&acc_full[2 * b + h], both);
+                                if (h + 1 == L::kParts) mma_commit_pair(bar, both);
+                            } else {
+                                mma_commit(&acc_full[2 * b + h]);
+                                if (h + 1 == L::kParts) mma_commit(bar);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (elect_one()) {  // waited for at the end
+                if (kPair) mma_commit_pair(drain, both);
+                else mma_commit(drain);
+            }
+            __syncwarp();
+        } else if (warp == 2 && plan.cluster == 1) {
+            // The output's tiles: the residual comes to the tile's memory early, the sums' warps turn it into
+            // the result, and that is copied out.  Both sides of this come whatever else happens: the waits
+            // are not for work.
+            uint8_t *slabs = smem + L::kStages * L::kStage;
+            bool ok = true;
+            uint32_t i = 0;
+            for (int tile = first_tile; ok && tile < tiles; tile += tile_step, ++i) {
+                const int t0 = tile % plan.tiles_m * kTileM + half * kRows, n0 = tile / plan.tiles_m * kCols;
+                const int slabs_used = t0 < a.M ? min(kCols / 64, (a.N - n0 + 63) / 64) : 0;
+                if (lane == 0) {
+                    if (a.residual && slabs_used > 0) {
+                        mbar_arrive_expect_tx(tile_free, slabs_used * (kRows * 128));
+                        for (int j = 0; j < slabs_used; ++j)
+                            tma_load_2d(slabs + j * (kRows * 128), &tm_res, tile_free, n0 + 64 * j, t0);
+                    } else {
+                        mbar_arrive(tile_free);
+                    }
+                }
+                __syncwarp();
+                ok = __all_sync(~0u, mbar_wait(tile_done, i & 1));
+                if (ok && lane == 0) {
+                    for (int j = 0; j < slabs_used; ++j) tma_store_2d(&tm_out, slabs + j * (kRows * 128), n0 + 64 * j, t0);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                }
+                __syncwarp();
+            }
+            if (lane == 0) bulk_wait_all();
+            if (!ok) *abort_flag = 1;
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSum));
+        constexpr int kWide = kCols / 2;  // a warp's columns
+        const int q = warp & 3, cw = (warp - kFirstSum) / 4 * kWide;
+        const uint32_t lead_empty = kPair ? map_to_rank(smem_u32(acc_empty), leader) : 0;
+        const int part_of_acc = L::kParts == 2 ? (warp - kFirstSum) / 4 : 0;
+        uint8_t *slabs = smem + L::kStages * L::kStage + (q * 32 + lane) * 128;  // this token's rows of them
+        bool ok = true;
+        uint32_t n = 0, done = 0;  // blocks and tiles taken
+        for (int tile = first_tile; tile < tiles; tile += tile_step) {
+            const int t0 = tile % plan.tiles_m * kTileM + half * kRows, n0 = tile / plan.tiles_m * kCols;
+            const int nt = min(kRows, a.M - t0);
+            const bool active = q * 32 < nt && n0 + cw < a.N;
+            float sums[kWide];
+#pragma unroll
+            for (int e = 0; e < kWide; ++e) sums[e] = 0.f;
+            // the blocks' scales come four at a time, while the four before are at work
+            const float *sx = a.x_scale + min(t0 + q * 32 + lane, a.M - 1);
+            const float *sw = a.w_scale + (long long)(min(n0 + cw, a.N - 1) / kBK) * plan.nk;
+            float nx[4], nw[4];
+            auto load_scales = [&](int kc) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = min(kc + j, k1 - 1);
+                    nx[j] = __ldg(sx + k * a.x_scale_stride);
+                    nw[j] = __ldg(sw + k);
+                }
+            };
+            load_scales(k0);
+            float scale[4];
+#pragma unroll 1
+            for (int kc = k0; ok && kc < k1; ++kc, ++n) {
+                const int j = (kc - k0) & 3;
+                if (j == 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) scale[e] = nx[e] * nw[e];
+                    load_scales(kc + 4);
+                }
+                const uint32_t b = n & 1, at = 2 * b + part_of_acc;
+                ok = warp_wait(mbar_try_wait(&acc_full[at], (n / 2) & 1), &acc_full[at], (n / 2) & 1, patience);
+                // a warp that gave up holds the accumulator: its arrivals, which wait for nothing, would
+                // stand for those of a warp that still reads
+                if (!ok) break;
+                tc_fence_after();
+                const float s = j < 2 ? (j == 0 ? scale[0] : scale[1]) : (j == 2 ? scale[2] : scale[3]);
+                if (active) add_block<kWide>(sums, tmem + tmem_lane_base(q) + b * kCols + cw, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (half == 0) mbar_arrive(&acc_empty[at]);
+                    else arrive_taken(lead_empty + at * 8);
+                }
+            }
+            if (!ok) {
+#pragma unroll
+                for (int e = 0; e < kWide; ++e) sums[e] = __int_as_float(0x7fc00000);
+            }
+            if (plan.cluster == 1) {
+                if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
+                ++done;
+                if (active) {
+#pragma unroll
+                    for (int c = 0; c < kWide; c += 32) {
+                        const int column = cw + c;
+                        uint8_t *row = slabs + column / 64 * (kRows * 128);
+                        auto finish = [&](auto act) {
+                            finish_columns<decltype(act)::value>(a, sums + c, row, column % 64 / 8, lane & 7, n0 + column);
+                        };
+                        switch (a.act) {
+                            case MLA_ACT_RELU: finish(Act<MLA_ACT_RELU>()); break;
+                            case MLA_ACT_SILU: finish(Act<MLA_ACT_SILU>()); break;
+                            case MLA_ACT_GELU: finish(Act<MLA_ACT_GELU>()); break;
+                            case MLA_ACT_GELU_TANH: finish(Act<MLA_ACT_GELU_TANH>()); break;
+                            default: finish(Act<MLA_ACT_NONE>()); break;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();  // the copy reads the tile through the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tile_done);
+            } else {
+                // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
+                // have, takes the parts of the columns this CTA finishes, one slot a rank.
+                const int share = kCols / plan.cluster, pitch = share + 4;
+                cluster_sync();
+                if (kPair && *gave_up) cluster_sync();  // the load warps settle it before this
+                const int token = q * 32 + lane;
+                if (token < nt) {
+                    const uint32_t mine = smem_u32(smem) + (uint32_t)(part * kRows + token) * (uint32_t)pitch * 4;
+#pragma unroll
+                    for (int e = 0; e < kWide / 4; ++e) {
+                        const int c = cw + 4 * e, to = c / share;
+                        st_cluster_v4(map_to_rank(mine + (uint32_t)(c - to * share) * 4, kPair ? 2 * to + half : to),
+                                      sums[4 * e], sums[4 * e + 1], sums[4 * e + 2], sums[4 * e + 3]);
+                    }
+                }
+                __syncwarp();
+                cluster_sync();
+                const int groups = share / 8, i0 = threadIdx.x - 32 * kFirstSum;  // groups: a power of two up to 16
+                Finish fin(a, t0, n0 + part * share + i0 % groups * 8);
+                const float *from = reinterpret_cast<const float *>(smem) + i0 % groups * 8;
+                const int per = 32 * kSumWarps / groups;  // tokens at a time, the next ones' residual under way
+                fin.load_half(a, i0 / groups, nt);
+                for (int t = i0 / groups; t < nt; t += per) {
+                    const uint4 res = fin.res[0];
+                    fin.load_half(a, t + per, nt);
+                    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    for (int s = 0; s < plan.cluster; ++s) {
+                        const float4 *v = reinterpret_cast<const float4 *>(from + (s * kRows + t) * pitch);
+                        const float4 lo = v[0], hi = v[1];
+                        sum[0] += lo.x; sum[1] += lo.y; sum[2] += lo.z; sum[3] += lo.w;
+                        sum[4] += hi.x; sum[5] += hi.y; sum[6] += hi.z; sum[7] += hi.w;
+                    }
+                    fin.store(a, t, nt, sum, res);
+                }
+            }
+        }
+    }
+    if (plan.cluster > 1 && warp < kFirstSum) {  // the barriers of the exchange
+        __syncwarp();
+        cluster_sync();
+        if (kPair && *gave_up) {  // the same for every CTA of the cluster
+            if (warp == 0 && half == 0 && !settle_pair<L::kStages, L::kStage>(full, issued, *peer_issued)) *abort_flag = 1;
+            __syncwarp();
+            cluster_sync();
+        }
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) set_status(a.status, MLA_ERR_TIMEOUT);
+    // The MMAs end, and with them the arrivals on this CTA's barriers, before its memory is given
+    // up.  They have ended where their results were waited for, and where that was given up
+    // nobody reads what they still write.
+    if (warp == 1) mbar_wait(drain, 0);
+    __syncwarp();
+    if (kPair) {
+        cluster_sync();  // neither CTA's memory is used by the other any more
+        if (plan.cluster == 1 && *gave_up) {
+            if (warp == 0 && half == 0) settle_pair<L::kStages, L::kStage>(full, issued, *peer_issued);
+            __syncwarp();
+            cluster_sync();
+        }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        if (kPair) tmem_free_pair<L::kTmemCols>(tmem);
+        else tmem_free<L::kTmemCols>(tmem);
+    }
+}
+
+template <int kCols, bool kPair = false>
+cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
+    CUtensorMap tm_x, tm_w;
+    if (!encode_u8_sw128(&tm_x, a.x, a.K, a.M, a.x_stride, kRows) ||
+        !encode_u8_sw128(&tm_w, a.w, a.K, a.N, a.K, kPair ? 64 : kCols))
+        return cudaErrorInvalidValue;
+    CUtensorMap tm_out = tm_x, tm_res = tm_x;  // read for whole tiles alone
+    if (p.cluster == 1) {
+        const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.M}, out_stride = a.out_stride * 2, res_stride = a.residual_stride * 2;
+        const uint32_t box[2] = {64, kRows};
+        if (!encode_bf16_sw128(&tm_out, a.out, 2, dims, &out_stride, box) ||
+            (a.residual && !encode_bf16_sw128(&tm_res, a.residual, 2, dims, &res_stride, box)))
+            return cudaErrorInvalidValue;
+    }
+    const int smem = Smem<kCols, kPair>::kBytes;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    static std::atomic<unsigned long long> ready{0};  // devices the kernel's shared memory is allowed on
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(linear_fp8_tc<kCols, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair ? 2 * p.cluster : p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair || p.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_fp8_tc<kCols, kPair>, tm_x, tm_w, tm_out, tm_res, a, p);
+}
+
+}  // namespace
+
+// The plan with the shortest estimate, in SM cycles.
+LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
+    Plan best{};
+    double best_cost = 0.0;
+    const double weights = 1.0 * K * N / 3500.0;  // however they are dealt out
+    const int nk = (K + kBK - 1) / kBK;
+    for (int form = 0; form < 3; ++form) {
+        Plan p;
+        p.pair = form == 2;
+        p.columns = form == 0 ? 64 : form == 1 ? 128 : 256;
+        const int tile_m = p.pair ? 2 * kRows : kRows;
+        if (p.pair && M <= kRows) break;
+        p.tiles_m = (M + tile_m - 1) / tile_m;
+        p.tiles_n = (N + p.columns - 1) / p.columns;
+        p.nk = nk;
+        const long long tiles = (long long)p.tiles_m * p.tiles_n;
+        if (tiles > (1ll << 28)) continue;
+        const double block = p.pair ? 560.0 : form == 1 ? 480.0 : 400.0, epilogue = 1500.0 + 10.0 * p.columns;
+        for (p.cluster = 1; p.cluster <= (p.pair ? 4 : 8); p.cluster *= 2) {
+            const int ctas = p.pair ? 2 * p.cluster : p.cluster;
+            // clusters that fit the SMs: fewer than an even share, as a cluster stays within one of
+            // the groups the SMs are built in
+            const int fit = ctas == 1 ? sms : ctas == 2 ? sms / 2 : ctas == 4 ? sms / 4 - 2 : sms / 8 - 4;
+            if (fit < 1 || (p.cluster > 1 && (nk < 2 * p.cluster || tiles > fit))) break;
+            p.grid = (int)(tiles < fit ? tiles : fit) * ctas;
+            const double k = (nk + p.cluster - 1) / p.cluster * block, waves = (double)((tiles + fit - 1) / fit);
+            const double work = waves * (k + epilogue), cost = (work > weights ? work : weights) + (p.cluster > 1 ? 2500.0 : 0.0);
+            if (best.grid == 0 || cost < best_cost) {
+                best = p;
+                best_cost = cost;
+            }
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_linear_fp8(const LinearFp8Args &a, const LinearFp8Plan &p, cudaStream_t st) {
+    if (p.pair) return launch<256, true>(a, p, st);
+    return p.columns == 128 ? launch<128>(a, p, st) : launch<64>(a, p, st);
+}
+
+}  // namespace mla

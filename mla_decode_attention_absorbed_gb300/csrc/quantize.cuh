@@ -1,0 +1,71 @@
+// Quantising by blocks of 128: the codes are OCP E4M3, each block has one fp32 scale.
+//
+//   A = max(max |y|, 2^-100),   scale = A / 448,   code = E4M3(y * (448 / A))
+//
+// 448 is the largest E4M3 value, so the block's largest value takes the last code and nothing
+// saturates; both quotients are rounded once in fp32 (division, not a reciprocal's estimate, so
+// that any fp32 program gives the same codes and scales).  The 2^-100 keeps 448 / A finite for
+// a block of zeros or of values that no result can show.  A NaN keeps its own code and leaves the
+// rest of its block alone (fmaxf returns the other operand); an infinity makes A infinite and
+// with it every value of the block NaN or 0 x infinity, so that it shows in what is computed.
+#pragma once
+
+#include "layer.h"
+#include "sm100.cuh"
+
+namespace mla {
+namespace quant {
+
+constexpr int kBlock = 128;
+constexpr float kTop = 448.f;
+constexpr float kLeast = 0x1p-100f;
+constexpr int kScaleBytes = 16;  // of a cache row of blocks: four scales, whatever its width
+
+// Two values as E4M3 codes (v0 in the low byte): nearest even, saturating at +-448.
+__device__ __forceinline__ uint32_t e4m3x2(float v0, float v1) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v1), "f"(v0));
+    return r;
+}
+// Two E4M3 codes as values, exactly (every one of them is an fp16 number).
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
+    float2 f;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+}
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack(w[e]);
+        f[2 * e] = p.x;
+        f[2 * e + 1] = p.y;
+    }
+}
+__device__ __forceinline__ float top8(const float (&f)[8]) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+    return top;
+}
+// The largest of 16 neighbouring lanes, which hold a block of 128 values, 8 each.
+__device__ __forceinline__ float top16(float top) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    return top;
+}
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float unit) {
+    return make_uint2(e4m3x2(f[0] * unit, f[1] * unit) | e4m3x2(f[2] * unit, f[3] * unit) << 16,
+                      e4m3x2(f[4] * unit, f[5] * unit) | e4m3x2(f[6] * unit, f[7] * unit) << 16);
+}
+
+}  // namespace quant
+}  // namespace mla

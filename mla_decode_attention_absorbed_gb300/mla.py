@@ -36,7 +36,7 @@ class Cache(ctypes.Structure):
                 ("kv_dtype", ctypes.c_int), ("kv_scale", ctypes.c_float)]
 
 
-KV_BF16, KV_E4M3 = 0, 1
+KV_BF16, KV_E4M3, KV_E4M3_BLOCKS = 0, 1, 3
 ABI_VERSION = 2
 SPLITS_BALANCED = -1  # num_splits asking for the balanced plan (MLA_SPLITS_BALANCED)
 
@@ -48,7 +48,8 @@ EXPORTS = ("mla_status_string", "mla_abi_version", "mla_absorb_q", "mla_decode_w
            "mla_prefill_expand_workspace_size", "mla_prefill_expand", "mla_prefill_workspace_size", "mla_prefill",
            "mla_decode_step", "mla_set_wait_limit_ns", "mla_rope_init", "mla_rope", "mla_pages_update",
            "mla_latent_store", "mla_linear_workspace_size", "mla_linear", "mla_linear_status",
-           "mla_linear_query_cut")
+           "mla_linear_query_cut", "mla_latent_row_bytes", "mla_latent_load", "mla_quantize", "mla_linear_fp8",
+           "mla_linear_fp8_query_cut")
 PATH_ABSORB, PATH_EXPAND = 0, 1
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
@@ -76,6 +77,17 @@ class PagePool(ctypes.Structure):
 class LinearDesc(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int), ("act", ctypes.c_int),
                 ("x_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong),
+                ("residual_stride", ctypes.c_longlong)]
+
+
+class QuantizeDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("K", ctypes.c_int), ("block_rows", ctypes.c_int), ("x_stride", ctypes.c_longlong),
+                ("code_stride", ctypes.c_longlong), ("scale_stride", ctypes.c_longlong)]
+
+
+class LinearFp8Desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int), ("act", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong), ("x_scale_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong),
                 ("residual_stride", ctypes.c_longlong)]
 
 
@@ -158,6 +170,17 @@ def load(path: str | None = None):
     lib.mla_linear_status.restype = I
     lib.mla_linear_query_cut.argtypes = [pl, ctypes.POINTER(LinearCut)]
     lib.mla_linear_query_cut.restype = I
+    pq, pf = ctypes.POINTER(QuantizeDesc), ctypes.POINTER(LinearFp8Desc)
+    lib.mla_latent_row_bytes.argtypes = [pd]
+    lib.mla_latent_row_bytes.restype = LL
+    lib.mla_latent_load.argtypes = [pd, pc, I, P, P, LL, P, P]
+    lib.mla_latent_load.restype = I
+    lib.mla_quantize.argtypes = [pq, P, P, ctypes.c_float, P, P, P]
+    lib.mla_quantize.restype = I
+    lib.mla_linear_fp8.argtypes = [pf, P, P, P, P, P, P, P, P, P]
+    lib.mla_linear_fp8.restype = I
+    lib.mla_linear_fp8_query_cut.argtypes = [pf, ctypes.POINTER(LinearCut)]
+    lib.mla_linear_fp8_query_cut.restype = I
     if path is None:
         _lib = lib
     return lib
@@ -218,14 +241,18 @@ def make_cache(prob: Problem, kv: torch.Tensor, seq_lens: torch.Tensor, block_ta
                page_size: int = 64, max_seq_len: int = 0, kv_scale: float | None = None) -> Cache:
     """Cache descriptor for a contiguous [B, T_max, W] (any sequence stride) or paged
     [P, page, W] latent cache already on the device: bf16 values, or FP8 E4M3 codes
-    (uint8 or float8_e4m3fn) with their ``kv_scale`` (value = kv_scale * code)."""
+    (uint8 or float8_e4m3fn) with their ``kv_scale`` (value = kv_scale * code), or uint8 rows
+    of ``latent_row_bytes`` (codes, a scale a block of 128, keys in bf16: no ``kv_scale``)."""
     W = prob.d_c + prob.d_rope
+    blocks = kv.dtype == torch.uint8 and kv.shape[-1] == prob.d_c + 16 + 2 * prob.d_rope
+    if blocks:
+        W = kv.shape[-1]
     fp8 = kv.dtype in (torch.uint8, torch.float8_e4m3fn)
     if (kv.dtype != torch.bfloat16 and not fp8) or kv.shape[-1] != W or kv.stride(-1) != 1:
         raise ValueError("kv must be bf16 or FP8 codes with rows of d_c + d_rope contiguous values")
-    if fp8 and kv_scale is None:
+    if fp8 and not blocks and kv_scale is None:
         raise ValueError("an FP8 cache needs its kv_scale")
-    dt, sc = (KV_E4M3, float(kv_scale)) if fp8 else (KV_BF16, 1.0)
+    dt, sc = (KV_E4M3_BLOCKS, 1.0) if blocks else (KV_E4M3, float(kv_scale)) if fp8 else (KV_BF16, 1.0)
     if block_table is None:
         if kv.dim() != 3 or kv.stride(1) != W:
             raise ValueError("contiguous kv must be [B, T_max, W] with dense token rows")
@@ -724,6 +751,120 @@ def linear(x, w, bias=None, residual=None, act: int = ACT_NONE, out=None, worksp
             code = lib.mla_linear_status(at, rows, weight, b, res, to, workspace.data_ptr(), nbytes, word, st)
     if code:
         raise MLAError(code, "mla_linear")
+    return out
+
+
+# --------------------------------------------------------------- 8 bits with scales by blocks of 128
+_E4M3, _F32 = torch.float8_e4m3fn, torch.float32
+
+
+def latent_row_bytes(prob: Problem) -> int:
+    """mla_latent_row_bytes: the width of a cache row in blocks (a uint8 cache of it is one for ``make_cache``)."""
+    n = load().mla_latent_row_bytes(prob.dims_ref())
+    if n == 0:
+        raise ValueError("mla_latent_row_bytes rejected the widths")
+    return int(n)
+
+
+def _codes(t, what: str, dev: int, M: int, K: int) -> int:
+    """Address of t, E4M3 codes [M, K] with contiguous rows (any stride between them)."""
+    if t.dtype != _E4M3 or t.get_device() != dev or t.shape != (M, K) or (K > 1 and t.stride(1) != 1):
+        _refuse(t, what, f"a torch.float8_e4m3fn tensor [{M}, {K}] with contiguous rows on device {dev}")
+    return t.data_ptr()
+
+
+def quantize(x, norm_weight=None, eps: float = 1e-6, block_rows: int = 1, codes=None, scales=None, stream=None):
+    """mla_quantize: x [M, K] (any row stride), after its RMS norm if ``norm_weight`` [K] is given, as E4M3 codes
+    [M, K] with fp32 scales: [ceil(K / 128), M] for ``block_rows`` 1 (activations), [ceil(M / 128), ceil(K / 128)]
+    for 128 (weights, [N, K] as ``linear_fp8`` takes them).  Returns (codes, scales)."""
+    lib = _lib or load()
+    dev = _device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    rows = _rows(x, "x", dev, M, K)
+    weight = None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, dev, (K,))
+    wide = (K + 127) // 128
+    shape = (wide, M) if block_rows == 1 else ((M + 127) // 128, wide)
+    new = _allocator(stream)
+    if codes is None:
+        codes = new((M, K), (K, 1), _E4M3)
+        to, code_stride = codes.data_ptr(), K
+    else:
+        to, code_stride = _codes(codes, "codes", dev, M, K), codes.stride(0) if M > 1 else K
+    if scales is None:
+        scales = new(shape, (shape[1], 1), _F32)
+        at = scales.data_ptr()
+    else:
+        at = _dense(scales, "scales", _F32, dev, shape)
+    desc = QuantizeDesc(M, K, block_rows, x.stride(0) if M > 1 else K, code_stride, shape[1])
+    code = lib.mla_quantize(ctypes.byref(desc), rows, weight, eps, to, at, _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_quantize")
+    return codes, scales
+
+
+def linear_fp8(x, x_scale, w, w_scale, bias=None, residual=None, act: int = ACT_NONE, out=None, stream=None, status=None):
+    """mla_linear_fp8: residual + act(x . w^T + bias) of E4M3 codes x [M, K] (rows any multiple of 16 bytes apart) and
+    w [N, K] dense, with the scales that ``quantize`` gives: x_scale [ceil(K / 128), M], w_scale [ceil(N / 128),
+    ceil(K / 128)].  bias, residual, out and ``status`` as for ``linear``."""
+    lib = _lib or load()
+    dev = _device(x, "x")
+    if w.dim() != 2 or x.dim() != 2:
+        raise ValueError("x must be [M, K], w [N, K]")
+    N, K = w.shape
+    M = x.shape[0]
+    rows = _codes(x, "x", dev, M, K)
+    if w.dtype != _E4M3 or w.get_device() != dev or not w.is_contiguous():
+        _refuse(w, "w", f"a dense torch.float8_e4m3fn tensor on device {dev}")
+    wide = (K + 127) // 128
+    xs = _dense(x_scale, "x_scale", _F32, dev, (wide, M))
+    ws = _dense(w_scale, "w_scale", _F32, dev, ((N + 127) // 128, wide))
+    b = None if bias is None else _dense(bias, "bias", _BF16, dev, (N,))
+    res = None if residual is None else _rows(residual, "residual", dev, M, N)
+    word = None if status is None else _word(status, dev)
+    if out is None:
+        out = _allocator(stream)((M, N), (N, 1), _BF16)
+        to, out_stride = out.data_ptr(), N
+    else:
+        to, out_stride = _rows(out, "out", dev, M, N), out.stride(0)
+    if M > 1:
+        desc = LinearFp8Desc(M, K, N, act, x.stride(0), M, out_stride, N if res is None else residual.stride(0))
+    else:  # a single row has no stride
+        desc = LinearFp8Desc(M, K, N, act, K, M, N, N)
+    code = lib.mla_linear_fp8(ctypes.byref(desc), rows, xs, w.data_ptr(), ws, b, res, to, word, _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_linear_fp8")
+    return out
+
+
+def linear_fp8_cut(M: int, K: int, N: int) -> LinearCut:
+    """mla_linear_fp8_query_cut: how a product of these sizes is cut on the current device (host only)."""
+    desc, cut = LinearFp8Desc(M, K, N, ACT_NONE, K, M, N, N), LinearCut()
+    _check(load().mla_linear_fp8_query_cut(ctypes.byref(desc), ctypes.byref(cut)), "mla_linear_fp8_query_cut")
+    return cut
+
+
+def latent_load(prob: Problem, cache: Cache, rows: int, positions=None, out=None, status=None, stream=None):
+    """mla_latent_load: ``rows`` tokens of each sequence back as bf16 [B, rows, d_c + d_rope] (``out``: any stride
+    between sequences), the first ones or those of ``positions`` [B, rows].  Rows of no token stay as they were."""
+    lib = _lib or load()
+    B, width = prob.B, prob.d_c + prob.d_rope
+    dev = _current_device()
+    if out is None:
+        out = _allocator(stream)((B, rows, width), (rows * width, width, 1), _BF16)
+        stride = rows * width
+    else:
+        if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, rows, width) or out.stride(2) != 1 or
+                (rows > 1 and out.stride(1) != width)):
+            _refuse(out, "out", f"torch.bfloat16 [{B}, {rows}, {width}] with dense rows on device {dev}")
+        stride = out.stride(0) if B > 1 else rows * width
+    at = None if positions is None else _dense(positions, "positions", _I32, dev, (B, rows))
+    word = None if status is None else _word(status, dev)
+    code = lib.mla_latent_load(prob.dims_ref(), ctypes.byref(cache), rows, at, out.data_ptr(), stride, word,
+                               _raw_stream(dev, stream))
+    if code:
+        raise MLAError(code, "mla_latent_load")
     return out
 
 
