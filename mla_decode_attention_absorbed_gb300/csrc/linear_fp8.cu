@@ -53,10 +53,9 @@ struct Smem {
     static constexpr int kTile = kRows * kCols * 2;  // the output's tile: slabs of 64 columns, 128 bytes a token
     static constexpr int kStages = (227 * 1024 - 2048 - kTile) / kStage;
     static constexpr int kBytes = kStages * kStage + kTile + 1024 /* barriers */ + 1024 /* alignment */;
-    static constexpr uint32_t kTmemCols = 2 * kCols;
+    static constexpr int kBufs = 512 / kCols;  // accumulators: a block of K each
     static constexpr int kParts = kPair ? 2 : 1;  // of a block's accumulator, see the MMA warp
-    // a cluster's sums are exchanged in the ring, rows of share + 4 floats
-    static_assert(kRows * (kCols + 4 * 8) * 4 <= kStages * kStage, "exchange");
+    static_assert(kRows * kCols * 4 <= kStages * kStage, "a cluster's sums are exchanged in the ring");
     static_assert(kBytes <= 232448, "shared memory over the per-CTA limit");
 };
 
@@ -174,11 +173,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using L = Smem<kCols, kPair>;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTile);
+    uint64_t *acc_full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTile);  // [accumulator][part]
+    uint64_t *acc_empty = acc_full + L::kBufs * L::kParts;
+    uint64_t *full = acc_empty + L::kBufs * L::kParts;
     uint64_t *empty = full + L::kStages;
-    uint64_t *acc_full = empty + L::kStages;  // [block's parity][part]
-    uint64_t *acc_empty = acc_full + 4;
-    uint64_t *drain = acc_empty + 4;
+    uint64_t *drain = empty + L::kStages;
     uint64_t *tile_free = drain + 1;  // the tile's memory holds the residual, or nothing that is needed
     uint64_t *tile_done = tile_free + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tile_done + 1);
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < L::kBufs * L::kParts; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], (kPair ? 2 : 1) * kSumWarps / L::kParts);
         }
@@ -208,14 +207,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_w);
     }
     if (warp == 1) {
-        if (kPair) tmem_alloc_pair<L::kTmemCols>(tmem_slot);
-        else tmem_alloc<L::kTmemCols>(tmem_slot);
+        if (kPair) tmem_alloc_pair<512>(tmem_slot);
+        else tmem_alloc<512>(tmem_slot);
     }
     tc_fence_before();
     __syncthreads();
     if (kPair) cluster_sync();  // the leader's barriers are ready for the other CTA
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();  // launched while the grid before it ends: nothing of it is read before
     constexpr int kTileM = kPair ? 2 * kRows : kRows;
     const int half = kPair ? (int)(blockIdx.x & 1) : 0;
     const uint32_t leader = kPair ? cluster_rank() & ~1u : 0, both = 3u << leader;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int part = blockIdx.x % ctas_a_tile(plan) / (kPair ? 2 : 1);
     const int tiles = plan.tiles_m * plan.tiles_n, first_tile = blockIdx.x / ctas_a_tile(plan);
     const int tile_step = plan.grid / ctas_a_tile(plan);
-    const int k0 = (int)((long long)plan.nk * part / plan.cluster), k1 = (int)((long long)plan.nk * (part + 1) / plan.cluster);
+    const int k0 = plan.nk * part / plan.cluster, k1 = plan.nk * (part + 1) / plan.cluster;
     uint32_t issued = 0;  // the load warp's stages
 
     // The loads' and the MMAs' loops are run by whole warps on values that are the same in
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true, there = false;
             for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
                 for (int kc = k0; ok && kc < k1; ++kc, ++n) {
-                    const uint32_t b = n & 1, taken = (n / 2 - 1) & 1;
+                    const uint32_t b = n % L::kBufs, taken = (n / L::kBufs - 1) & 1;
                     if (!warp_wait(there, &full[s], phase, patience)) {
                         ok = false;
                         break;
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     there = mbar_test_wait(&full[s], phase);  // its answer comes while the MMAs are issued
 #pragma unroll
                     for (int h = 0; h < L::kParts; ++h) {
-                        uint64_t *mine = &acc_empty[2 * b + h];
-                        if (n >= 2 && !warp_wait<kPair>(try_taken(mine, taken), mine, taken, patience)) {
+                        uint64_t *mine = &acc_empty[L::kParts * b + h];
+                        if (n >= L::kBufs && !warp_wait<kPair>(try_taken(mine, taken), mine, taken, patience)) {
                             ok = false;
                             break;
                         }
@@ -321,10 +321,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_codes<kPair>(acc0 + b * kCols + h * 128, dx + kk * (32 >> 4),
                                                  dw + h * (64 * kBK >> 4) + kk * (32 >> 4), idesc, kk > 0);
                             if (kPair) {
-                                mma_commit_pair(&acc_full[2 * b + h], both);
+                                mma_commit_pair(&acc_full[L::kParts * b + h], both);
                                 if (h + 1 == L::kParts) mma_commit_pair(bar, both);
                             } else {
-                                mma_commit(&acc_full[2 * b + h]);
+                                mma_commit(&acc_full[L::kParts * b + h]);
                                 if (h + 1 == L::kParts) mma_commit(bar);
                             }
                         }
@@ -337,7 +337,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else mma_commit(drain);
             }
             __syncwarp();
-        } else if (warp == 2 && plan.cluster == 1) {
+        } else if (warp == 2 && plan.cluster > 1) {
+            // the residual of the columns this CTA finishes (whole slabs of 64)
+            const int share = kCols / plan.cluster, t0 = first_tile % plan.tiles_m * kTileM + half * kRows;
+            const int n0 = first_tile / plan.tiles_m * kCols + part * share / 64 * 64;
+            if (lane == 0) {
+                if (a.residual && t0 < a.M && n0 < a.N) {
+                    const bool second = share > 64 && n0 + 64 < a.N;
+                    mbar_arrive_expect_tx(tile_free, (second ? 2 : 1) * (kRows * 128));
+                    tma_load_2d(smem + L::kStages * L::kStage, &tm_res, tile_free, n0, t0);
+                    if (second) tma_load_2d(smem + L::kStages * L::kStage + kRows * 128, &tm_res, tile_free, n0 + 64, t0);
+                } else {
+                    mbar_arrive(tile_free);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 2) {
             // The output's tiles: the residual comes to the tile's memory early, the sums' warps turn it into
             // the result, and that is copied out.  Both sides of this come whatever else happens: the waits
             // are not for work.
@@ -373,9 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSum));
         constexpr int kWide = kCols / 2;  // a warp's columns
         const int q = warp & 3, cw = (warp - kFirstSum) / 4 * kWide;
-        const uint32_t lead_empty = kPair ? map_to_rank(smem_u32(acc_empty), leader) : 0;
+        const uint32_t lead_empty = map_to_rank(smem_u32(acc_empty + (L::kParts == 2 ? (warp - kFirstSum) / 4 : 0)), kPair ? leader : cluster_rank());
         const int part_of_acc = L::kParts == 2 ? (warp - kFirstSum) / 4 : 0;
-        uint8_t *slabs = smem + L::kStages * L::kStage + (q * 32 + lane) * 128;  // this token's rows of them
+        uint8_t *tile_memory = smem + L::kStages * L::kStage;  // slabs of 64 columns, 128 bytes a token
+        const uint32_t acc0 = __shfl_sync(~0u, tmem + tmem_lane_base(q) + cw, 0);
         bool ok = true;
         uint32_t n = 0, done = 0;  // blocks and tiles taken
         for (int tile = first_tile; tile < tiles; tile += tile_step) {
@@ -386,40 +402,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < kWide; ++e) sums[e] = 0.f;
             // the blocks' scales come four at a time, while the four before are at work
-            const float *sx = a.x_scale + min(t0 + q * 32 + lane, a.M - 1);
-            const float *sw = a.w_scale + (long long)(min(n0 + cw, a.N - 1) / kBK) * plan.nk;
+            const float *sx = a.x_scale + k0 * a.x_scale_stride + min(t0 + q * 32 + lane, a.M - 1);
+            const float *sw = a.w_scale + (long long)(min(n0 + cw, a.N - 1) / kBK) * plan.nk + k0;
             float nx[4], nw[4];
-            auto load_scales = [&](int kc) {
+            auto load_scales = [&](int left) {  // the next `left` blocks', at most 4
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < left) {
+                        nx[j] = __ldg(sx);
+                        nw[j] = __ldg(sw + j);
+                        sx += a.x_scale_stride;
+                    }
+                sw += 4;
+            };
+            load_scales(k1 - k0);
+#pragma unroll 1
+            for (int kc = k0; ok && kc < k1; kc += 4) {
+                float scale[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) scale[e] = nx[e] * nw[e];
+                load_scales(k1 - kc - 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int k = min(kc + j, k1 - 1);
-                    nx[j] = __ldg(sx + k * a.x_scale_stride);
-                    nw[j] = __ldg(sw + k);
-                }
-            };
-            load_scales(k0);
-            float scale[4];
-#pragma unroll 1
-            for (int kc = k0; ok && kc < k1; ++kc, ++n) {
-                const int j = (kc - k0) & 3;
-                if (j == 0) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) scale[e] = nx[e] * nw[e];
-                    load_scales(kc + 4);
-                }
-                const uint32_t b = n & 1, at = 2 * b + part_of_acc;
-                ok = warp_wait(mbar_try_wait(&acc_full[at], (n / 2) & 1), &acc_full[at], (n / 2) & 1, patience);
-                // a warp that gave up holds the accumulator: its arrivals, which wait for nothing, would
-                // stand for those of a warp that still reads
-                if (!ok) break;
-                tc_fence_after();
-                const float s = j < 2 ? (j == 0 ? scale[0] : scale[1]) : (j == 2 ? scale[2] : scale[3]);
-                if (active) add_block<kWide>(sums, tmem + tmem_lane_base(q) + b * kCols + cw, s);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (half == 0) mbar_arrive(&acc_empty[at]);
-                    else arrive_taken(lead_empty + at * 8);
+                    if (!ok || kc + j >= k1) continue;
+                    const uint32_t b = n % L::kBufs, parity = (n / L::kBufs) & 1;
+                    uint64_t *ready = acc_full + L::kParts * b + part_of_acc;
+                    ok = warp_wait(mbar_try_wait(ready, parity), ready, parity, patience);
+                    // a warp that gave up holds the accumulator: its arrivals, which wait for nothing, would
+                    // stand for those of a warp that still reads
+                    if (!ok) continue;
+                    tc_fence_after();
+                    if (active) add_block<kWide>(sums, acc0 + b * kCols, scale[j]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_taken(lead_empty + b * (8 * L::kParts));
+                    ++n;
                 }
             }
             if (!ok) {
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kWide; c += 32) {
                         const int column = cw + c;
-                        uint8_t *row = slabs + column / 64 * (kRows * 128);
+                        uint8_t *row = tile_memory + (column / 64 * kRows + q * 32 + lane) * 128;
                         auto finish = [&](auto act) {
                             finish_columns<decltype(act)::value>(a, sums + c, row, column % 64 / 8, lane & 7, n0 + column);
                         };
@@ -452,37 +469,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
                 // have, takes the parts of the columns this CTA finishes, one slot a rank.
-                const int share = kCols / plan.cluster, pitch = share + 4;
+                const int share = kCols / plan.cluster, token = q * 32 + lane;  // share: a power of two, 8 or more
                 cluster_sync();
                 if (kPair && *gave_up) cluster_sync();  // the load warps settle it before this
-                const int token = q * 32 + lane;
-                if (token < nt) {
-                    const uint32_t mine = smem_u32(smem) + (uint32_t)(part * kRows + token) * (uint32_t)pitch * 4;
+                // four columns of the tokens lie together, so that a warp writes and reads 512 bytes at a time
+                if (q * 32 < nt) {
+                    const uint32_t mine = smem_u32(smem) + (uint32_t)(part * (share / 4) * kRows + token) * 16;
 #pragma unroll
                     for (int e = 0; e < kWide / 4; ++e) {
                         const int c = cw + 4 * e, to = c / share;
-                        st_cluster_v4(map_to_rank(mine + (uint32_t)(c - to * share) * 4, kPair ? 2 * to + half : to),
+                        st_cluster_v4(map_to_rank(mine + (uint32_t)(c / 4 % (share / 4)) * (kRows * 16), kPair ? 2 * to + half : to),
                                       sums[4 * e], sums[4 * e + 1], sums[4 * e + 2], sums[4 * e + 3]);
                     }
                 }
                 __syncwarp();
+                if (!__all_sync(~0u, mbar_wait(tile_free, 0))) *abort_flag = 1;
                 cluster_sync();
-                const int groups = share / 8, i0 = threadIdx.x - 32 * kFirstSum;  // groups: a power of two up to 16
-                Finish fin(a, t0, n0 + part * share + i0 % groups * 8);
-                const float *from = reinterpret_cast<const float *>(smem) + i0 % groups * 8;
-                const int per = 32 * kSumWarps / groups;  // tokens at a time, the next ones' residual under way
-                fin.load_half(a, i0 / groups, nt);
-                for (int t = i0 / groups; t < nt; t += per) {
-                    const uint4 res = fin.res[0];
-                    fin.load_half(a, t + per, nt);
-                    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    for (int s = 0; s < plan.cluster; ++s) {
-                        const float4 *v = reinterpret_cast<const float4 *>(from + (s * kRows + t) * pitch);
-                        const float4 lo = v[0], hi = v[1];
-                        sum[0] += lo.x; sum[1] += lo.y; sum[2] += lo.z; sum[3] += lo.w;
-                        sum[4] += hi.x; sum[5] += hi.y; sum[6] += hi.z; sum[7] += hi.w;
+                // 32 tokens x 8 columns at a time, dealt out to the warps
+                const int runs = (nt + 31) / 32;
+#pragma unroll 1
+                for (int i = warp - kFirstSum; i < runs * (share / 8); i += kSumWarps) {
+                    const int g = i / runs, token = (i - g * runs) * 32 + lane;
+                    if (token >= nt) continue;
+                    const float4 *from = reinterpret_cast<const float4 *>(smem) + token;
+                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8];
+                    for (int r = 0; r < plan.cluster; ++r) {
+                        const float4 lo = from[(r * (share / 4) + 2 * g) * kRows], hi = from[(r * (share / 4) + 2 * g + 1) * kRows];
+                        y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
+                        y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
                     }
-                    fin.store(a, t, nt, sum, res);
+                    const int at = part * share + 8 * g, n = n0 + at;  // in the tile, in the output
+                    if (n >= a.N) continue;
+                    if (a.bias) {
+                        Finish::unpack8(__ldg(reinterpret_cast<const uint4 *>(a.bias + n)), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] += f[e];
+                    }
+                    activate(a.act, y);
+                    if (a.residual) {
+                        const int in_slabs = at - part * share / 64 * 64, chunk = in_slabs % 64 / 8;
+                        Finish::unpack8(*reinterpret_cast<const uint4 *>(tile_memory + (in_slabs / 64 * kRows + token) * 128 +
+                                                                         ((chunk ^ (token & 7)) << 4)), f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] += f[e];
+                    }
+                    *reinterpret_cast<uint4 *>(a.out + (long long)(t0 + token) * a.out_stride + n) = make_uint4(
+                        pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
                 }
             }
         }
@@ -515,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1) {
         tc_fence_after();
-        if (kPair) tmem_free_pair<L::kTmemCols>(tmem);
-        else tmem_free<L::kTmemCols>(tmem);
+        if (kPair) tmem_free_pair<512>(tmem);
+        else tmem_free<512>(tmem);
     }
 }
 
@@ -526,14 +558,13 @@ cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
     if (!encode_u8_sw128(&tm_x, a.x, a.K, a.M, a.x_stride, kRows) ||
         !encode_u8_sw128(&tm_w, a.w, a.K, a.N, a.K, kPair ? 64 : kCols))
         return cudaErrorInvalidValue;
-    CUtensorMap tm_out = tm_x, tm_res = tm_x;  // read for whole tiles alone
-    if (p.cluster == 1) {
-        const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.M}, out_stride = a.out_stride * 2, res_stride = a.residual_stride * 2;
-        const uint32_t box[2] = {64, kRows};
-        if (!encode_bf16_sw128(&tm_out, a.out, 2, dims, &out_stride, box) ||
-            (a.residual && !encode_bf16_sw128(&tm_res, a.residual, 2, dims, &res_stride, box)))
-            return cudaErrorInvalidValue;
-    }
+    // the output's map is for whole tiles alone, the residual's for a residual: else not read
+    CUtensorMap tm_out = tm_x, tm_res = tm_x;
+    const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.M}, out_stride = a.out_stride * 2, res_stride = a.residual_stride * 2;
+    const uint32_t box[2] = {64, kRows};
+    if ((p.cluster == 1 && !encode_bf16_sw128(&tm_out, a.out, 2, dims, &out_stride, box)) ||
+        (a.residual && !encode_bf16_sw128(&tm_res, a.residual, 2, dims, &res_stride, box)))
+        return cudaErrorInvalidValue;
     const int smem = Smem<kCols, kPair>::kBytes;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -548,12 +579,14 @@ cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPair ? 2 * p.cluster : p.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kPair ? 2 * p.cluster : p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kPair || p.cluster > 1 ? 1 : 0;
+    cfg.numAttrs = kPair || p.cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, linear_fp8_tc<kCols, kPair>, tm_x, tm_w, tm_out, tm_res, a, p);
 }
 
