@@ -107,7 +107,9 @@ struct LinearFp8Plan {
     int tiles_m, tiles_n;  // tile t: tokens t % tiles_m, columns t / tiles_m
     int nk;                // blocks of K
     int grid;
-    int cluster;           // CTAs, or pairs of them, that share a tile's K (1: none)
+    int whole;             // tiles that a CTA (or pair) takes whole, one after another; of the others,
+    int cluster;           // the CTAs (or pairs) of a cluster share one's K (1: there are none)
+    int x_rows;            // of a copy of x: as many as there are, up to 128
     bool pair;             // a tile is 256 tokens x 256 columns, taken by a pair of CTAs
 };
 LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms);

@@ -17,6 +17,8 @@
 // so results do not depend on timing.
 //
 // Warps: 0 issues the loads, 1 the MMAs, 4-11 hold the sums.
+#include <limits.h>
+
 #include <atomic>
 
 #include "layer.h"
@@ -163,7 +165,43 @@ __device__ __forceinline__ bool try_taken(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-__device__ __forceinline__ int ctas_a_tile(const Plan &p) { return p.pair ? 2 * p.cluster : p.cluster; }
+// For what comes once the waits for work have ended, one way or the other (a whole warp).
+__device__ __forceinline__ bool wait_beyond(uint64_t *bar, uint32_t parity, uint64_t wait_ns) {
+    const uint64_t t0 = globaltimer_ns(), ns = wait_ns + 2 * kWaitLimitNs;
+    const long long c0 = clock64();
+    while (!__all_sync(~0u, mbar_try_wait(bar, parity)))
+        if (__any_sync(~0u, globaltimer_ns() - t0 > ns || clock64() - c0 > (long long)(2 * ns))) return false;
+    return true;
+}
+
+// A CTA's work (a pair's, "unit"): whole tiles, then, for a cluster's units together, a share of one
+// tile's K.
+struct Segment {
+    int tile, k0, k1;
+    bool cut;
+};
+struct Walk {
+    const Plan &p;
+    int unit, units, tile, part;
+    bool split;  // this cluster has a tile to share: the same for all its CTAs
+    __device__ __forceinline__ Walk(const Plan &plan) : p(plan) {
+        unit = tile = plan.pair ? blockIdx.x / 2 : blockIdx.x;
+        units = plan.pair ? plan.grid / 2 : plan.grid;
+        part = unit % plan.cluster;
+        split = plan.cluster > 1 && plan.whole + unit / plan.cluster < plan.tiles_m * plan.tiles_n;
+    }
+    __device__ __forceinline__ bool next(Segment &s) {
+        if (tile < p.whole) {
+            s = Segment{tile, 0, p.nk, false};
+            tile += units;
+            return true;
+        }
+        if (!split || tile == INT_MAX) return false;
+        s = Segment{p.whole + unit / p.cluster, p.nk * part / p.cluster, p.nk * (part + 1) / p.cluster, true};
+        tile = INT_MAX;
+        return true;
+    }
+};
 
 template <int kCols, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -215,15 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kPair) cluster_sync();  // the leader's barriers are ready for the other CTA
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();  // launched while the grid before it ends: nothing of it is read before
+    // Launched while the grid before it ends, whose results are read from here on; the next one may
+    // begin its setup, too (its tensor memory is another SM's: two of these do not fit one).
+    pdl_launch_dependents();
+    pdl_wait();
     constexpr int kTileM = kPair ? 2 * kRows : kRows;
     const int half = kPair ? (int)(blockIdx.x & 1) : 0;
     const uint32_t leader = kPair ? cluster_rank() & ~1u : 0, both = 3u << leader;
-    // this CTA's tiles, and its blocks of each (a cluster's CTAs: a part of one tile's)
-    const int part = blockIdx.x % ctas_a_tile(plan) / (kPair ? 2 : 1);
-    const int tiles = plan.tiles_m * plan.tiles_n, first_tile = blockIdx.x / ctas_a_tile(plan);
-    const int tile_step = plan.grid / ctas_a_tile(plan);
-    const int k0 = plan.nk * part / plan.cluster, k1 = plan.nk * (part + 1) / plan.cluster;
+    Walk walk(plan);
+    Segment seg;
     uint32_t issued = 0;  // the load warp's stages
 
     // The loads' and the MMAs' loops are run by whole warps on values that are the same in
@@ -234,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), leader) : 0;
             uint32_t s = 0, phase = 1;
             bool ok = true, free = mbar_test_wait(&empty[0], 1);
-            for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
-                const int t0 = tile % plan.tiles_m * kTileM + half * kRows;
-                const int n0 = tile / plan.tiles_m * kCols + half * 64;
-                for (int kc = k0; kc < k1; ++kc) {
+            while (ok && walk.next(seg)) {
+                const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows;
+                const int n0 = seg.tile / plan.tiles_m * kCols + half * 64;
+                for (int kc = seg.k0; kc < seg.k1; ++kc) {
                     // the first round's waits are for the phase before the barriers' first: over at once
                     if (!warp_wait(free, &empty[s], phase, patience)) {
                         ok = false;
@@ -256,10 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (half == 0) mbar_arrive_expect_tx(bar, 2 * L::kStage);
                             tma_load_2d_pair(st, &tm_x, lead, kc * kBK, t0);
                             // the first 128 columns' half, and the second's
-                        tma_load_2d_pair(st + L::kXBytes, &tm_w, lead, kc * kBK, n0);
-                        tma_load_2d_pair(st + L::kXBytes + 64 * kBK, &tm_w, lead, kc * kBK, n0 + 128);
+                            tma_load_2d_pair(st + L::kXBytes, &tm_w, lead, kc * kBK, n0);
+                            tma_load_2d_pair(st + L::kXBytes + 64 * kBK, &tm_w, lead, kc * kBK, n0 + 128);
                         } else {
-                            mbar_arrive_expect_tx(bar, L::kStage);
+                            mbar_arrive_expect_tx(bar, plan.x_rows * kBK + L::kWBytes);
                             tma_load_2d(st, &tm_x, bar, kc * kBK, t0);
                             tma_load_2d(st + L::kXBytes, &tm_w, bar, kc * kBK, n0);
                         }
@@ -293,8 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t acc0 = __shfl_sync(~0u, tmem, 0);
             uint32_t s = 0, phase = 0, n = 0;  // n: blocks issued
             bool ok = true, there = false;
-            for (int tile = first_tile; ok && tile < tiles; tile += tile_step) {
-                for (int kc = k0; ok && kc < k1; ++kc, ++n) {
+            while (ok && walk.next(seg)) {
+                for (int kc = seg.k0; ok && kc < seg.k1; ++kc, ++n) {
                     const uint32_t b = n % L::kBufs, taken = (n / L::kBufs - 1) & 1;
                     if (!warp_wait(there, &full[s], phase, patience)) {
                         ok = false;
@@ -337,44 +375,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else mma_commit(drain);
             }
             __syncwarp();
-        } else if (warp == 2 && plan.cluster > 1) {
-            // the residual of the columns this CTA finishes (whole slabs of 64)
-            const int share = kCols / plan.cluster, t0 = first_tile % plan.tiles_m * kTileM + half * kRows;
-            const int n0 = first_tile / plan.tiles_m * kCols + part * share / 64 * 64;
-            if (lane == 0) {
-                if (a.residual && t0 < a.M && n0 < a.N) {
-                    const bool second = share > 64 && n0 + 64 < a.N;
-                    mbar_arrive_expect_tx(tile_free, (second ? 2 : 1) * (kRows * 128));
-                    tma_load_2d(smem + L::kStages * L::kStage, &tm_res, tile_free, n0, t0);
-                    if (second) tma_load_2d(smem + L::kStages * L::kStage + kRows * 128, &tm_res, tile_free, n0 + 64, t0);
-                } else {
-                    mbar_arrive(tile_free);
-                }
-            }
-            __syncwarp();
         } else if (warp == 2) {
-            // The output's tiles: the residual comes to the tile's memory early, the sums' warps turn it into
-            // the result, and that is copied out.  Both sides of this come whatever else happens: the waits
-            // are not for work.
+            // The output's tiles: the residual comes to the tile's memory early (of a tile that a cluster
+            // shares, the slabs with this CTA's columns), the sums' warps turn it into the result, and that is
+            // copied out.  They do so whatever else happens: the wait for them is not one for work.
             uint8_t *slabs = smem + L::kStages * L::kStage;
             bool ok = true;
             uint32_t i = 0;
-            for (int tile = first_tile; ok && tile < tiles; tile += tile_step, ++i) {
-                const int t0 = tile % plan.tiles_m * kTileM + half * kRows, n0 = tile / plan.tiles_m * kCols;
-                const int slabs_used = t0 < a.M ? min(kCols / 64, (a.N - n0 + 63) / 64) : 0;
+            for (; ok && walk.next(seg); ++i) {
+                const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows;
+                int n0 = seg.tile / plan.tiles_m * kCols, used = kCols / 64;
+                if (seg.cut) {
+                    const int share = kCols / plan.cluster;
+                    n0 += walk.part * share / 64 * 64;
+                    used = share > 64 ? share / 64 : 1;
+                }
+                used = t0 < a.M && n0 < a.N ? min(used, (a.N - n0 + 63) / 64) : 0;
                 if (lane == 0) {
-                    if (a.residual && slabs_used > 0) {
-                        mbar_arrive_expect_tx(tile_free, slabs_used * (kRows * 128));
-                        for (int j = 0; j < slabs_used; ++j)
+                    if (a.residual && used > 0) {
+                        mbar_arrive_expect_tx(tile_free, used * (kRows * 128));
+                        for (int j = 0; j < used; ++j)
                             tma_load_2d(slabs + j * (kRows * 128), &tm_res, tile_free, n0 + 64 * j, t0);
                     } else {
                         mbar_arrive(tile_free);
                     }
                 }
                 __syncwarp();
-                ok = __all_sync(~0u, mbar_wait(tile_done, i & 1));
+                if (seg.cut) break;
+                ok = wait_beyond(tile_done, i & 1, a.wait_ns);
                 if (ok && lane == 0) {
-                    for (int j = 0; j < slabs_used; ++j) tma_store_2d(&tm_out, slabs + j * (kRows * 128), n0 + 64 * j, t0);
+                    for (int j = 0; j < used; ++j) tma_store_2d(&tm_out, slabs + j * (kRows * 128), n0 + 64 * j, t0);
                     bulk_commit();
                     bulk_wait_read_all();
                 }
@@ -394,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t acc0 = __shfl_sync(~0u, tmem + tmem_lane_base(q) + cw, 0);
         bool ok = true;
         uint32_t n = 0, done = 0;  // blocks and tiles taken
-        for (int tile = first_tile; tile < tiles; tile += tile_step) {
-            const int t0 = tile % plan.tiles_m * kTileM + half * kRows, n0 = tile / plan.tiles_m * kCols;
+        for (; walk.next(seg); ++done) {
+            const int k0 = seg.k0, k1 = seg.k1;
+            const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows, n0 = seg.tile / plan.tiles_m * kCols;
             const int nt = min(kRows, a.M - t0);
             const bool active = q * 32 < nt && n0 + cw < a.N;
             float sums[kWide];
@@ -443,9 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < kWide; ++e) sums[e] = __int_as_float(0x7fc00000);
             }
-            if (plan.cluster == 1) {
+            if (!seg.cut) {
                 if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
-                ++done;
                 if (active) {
 #pragma unroll
                     for (int c = 0; c < kWide; c += 32) {
@@ -469,12 +499,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
                 // have, takes the parts of the columns this CTA finishes, one slot a rank.
-                const int share = kCols / plan.cluster, token = q * 32 + lane;  // share: a power of two, 8 or more
+                const int share = kCols / plan.cluster, part = walk.part;  // share: a power of two, 8 or more
                 cluster_sync();
                 if (kPair && *gave_up) cluster_sync();  // the load warps settle it before this
                 // four columns of the tokens lie together, so that a warp writes and reads 512 bytes at a time
                 if (q * 32 < nt) {
-                    const uint32_t mine = smem_u32(smem) + (uint32_t)(part * (share / 4) * kRows + token) * 16;
+                    const uint32_t mine = smem_u32(smem) + (uint32_t)(part * (share / 4) * kRows + q * 32 + lane) * 16;
 #pragma unroll
                     for (int e = 0; e < kWide / 4; ++e) {
                         const int c = cw + 4 * e, to = c / share;
@@ -483,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (!__all_sync(~0u, mbar_wait(tile_free, 0))) *abort_flag = 1;
+                if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
                 cluster_sync();
                 // 32 tokens x 8 columns at a time, dealt out to the warps
                 const int runs = (nt + 31) / 32;
@@ -519,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (plan.cluster > 1 && warp < kFirstSum) {  // the barriers of the exchange
+    if (walk.split && warp < kFirstSum) {  // the barriers of the exchange
         __syncwarp();
         cluster_sync();
         if (kPair && *gave_up) {  // the same for every CTA of the cluster
@@ -539,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (kPair) {
         cluster_sync();  // neither CTA's memory is used by the other any more
-        if (plan.cluster == 1 && *gave_up) {
+        if (!walk.split && *gave_up) {
             if (warp == 0 && half == 0) settle_pair<L::kStages, L::kStage>(full, issued, *peer_issued);
             __syncwarp();
             cluster_sync();
@@ -555,14 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int kCols, bool kPair = false>
 cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
     CUtensorMap tm_x, tm_w;
-    if (!encode_u8_sw128(&tm_x, a.x, a.K, a.M, a.x_stride, kRows) ||
+    if (!encode_u8_sw128(&tm_x, a.x, a.K, a.M, a.x_stride, p.x_rows) ||
         !encode_u8_sw128(&tm_w, a.w, a.K, a.N, a.K, kPair ? 64 : kCols))
         return cudaErrorInvalidValue;
     // the output's map is for whole tiles alone, the residual's for a residual: else not read
     CUtensorMap tm_out = tm_x, tm_res = tm_x;
     const uint64_t dims[2] = {(uint64_t)a.N, (uint64_t)a.M}, out_stride = a.out_stride * 2, res_stride = a.residual_stride * 2;
     const uint32_t box[2] = {64, kRows};
-    if ((p.cluster == 1 && !encode_bf16_sw128(&tm_out, a.out, 2, dims, &out_stride, box)) ||
+    if ((p.whole > 0 && !encode_bf16_sw128(&tm_out, a.out, 2, dims, &out_stride, box)) ||
         (a.residual && !encode_bf16_sw128(&tm_res, a.residual, 2, dims, &res_stride, box)))
         return cudaErrorInvalidValue;
     const int smem = Smem<kCols, kPair>::kBytes;
@@ -604,21 +634,36 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
         p.columns = form == 0 ? 64 : form == 1 ? 128 : 256;
         const int tile_m = p.pair ? 2 * kRows : kRows;
         if (p.pair && M <= kRows) break;
+        p.x_rows = M < kRows ? (M + 7) / 8 * 8 : kRows;
         p.tiles_m = (M + tile_m - 1) / tile_m;
         p.tiles_n = (N + p.columns - 1) / p.columns;
         p.nk = nk;
         const long long tiles = (long long)p.tiles_m * p.tiles_n;
         if (tiles > (1ll << 28)) continue;
-        const double block = p.pair ? 560.0 : form == 1 ? 480.0 : 400.0, epilogue = 1500.0 + 10.0 * p.columns;
+        const double block = p.pair ? 800.0 : form == 1 ? 560.0 : 450.0, epilogue = 1500.0 + 10.0 * p.columns;
+        const int rows = M < kRows ? M : kRows;
         for (p.cluster = 1; p.cluster <= (p.pair ? 4 : 8); p.cluster *= 2) {
             const int ctas = p.pair ? 2 * p.cluster : p.cluster;
             // clusters that fit the SMs: fewer than an even share, as a cluster stays within one of
             // the groups the SMs are built in
             const int fit = ctas == 1 ? sms : ctas == 2 ? sms / 2 : ctas == 4 ? sms / 4 - 2 : sms / 8 - 4;
-            if (fit < 1 || (p.cluster > 1 && (nk < 2 * p.cluster || tiles > fit))) break;
-            p.grid = (int)(tiles < fit ? tiles : fit) * ctas;
-            const double k = (nk + p.cluster - 1) / p.cluster * block, waves = (double)((tiles + fit - 1) / fit);
-            const double work = waves * (k + epilogue), cost = (work > weights ? work : weights) + (p.cluster > 1 ? 2500.0 : 0.0);
+            if (fit < 1 || (p.cluster > 1 && nk < 2 * p.cluster)) break;
+            double cost;
+            if (p.cluster == 1) {
+                p.whole = (int)tiles;
+                p.grid = (int)(tiles < fit ? tiles : fit) * ctas;
+                cost = (double)((tiles + fit - 1) / fit) * (nk * block + epilogue);
+            } else {
+                // rounds of whole tiles, one a unit, and at most one tile a cluster left
+                const long long a_round = (long long)fit * p.cluster;
+                p.whole = (int)(tiles / a_round * a_round);
+                if (tiles - p.whole < 1 || tiles - p.whole > fit) continue;
+                p.grid = (p.whole > 0 ? fit : (int)tiles) * ctas;
+                const double sent = (double)rows * p.columns * 4 * (p.cluster - 1) / p.cluster;
+                cost = (double)(p.whole / a_round) * (nk * block + epilogue) + (nk + p.cluster - 1) / p.cluster * block +
+                       4000.0 + sent / 12.0 + 40.0 * rows * p.columns / p.cluster / 256.0;
+            }
+            if (cost < weights) cost = weights + cost * 1e-3;
             if (best.grid == 0 || cost < best_cost) {
                 best = p;
                 best_cost = cost;
