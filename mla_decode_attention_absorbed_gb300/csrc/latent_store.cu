@@ -194,14 +194,23 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
             if (kDtype == MLA_KV_E4M3_BLOCKS) {
                 // 16 lanes hold a block of the latent; the key keeps bf16
                 uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
+                float mine = 0.f;  // lane i of a half holds the i-th chunk's block's
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float v[8] = {f[i][0].x, f[i][0].y, f[i][1].x, f[i][1].y, f[i][2].x, f[i][2].y, f[i][3].x, f[i][3].y};
-                    const float top = fmaxf(quant::top16(quant::top8(v)), quant::kLeast);
-                    const int c = lane + 32 * i;
-                    if (c < nc) *(reinterpret_cast<uint2 *>(dst) + c) = quant::codes8(v, __fdiv_rn(quant::kTop, top));
-                    if ((lane & 15) == 0)
-                        *(reinterpret_cast<float *>(dst + a.d_c) + c / 16) = c < nc ? __fdiv_rn(top, quant::kTop) : 0.f;
+                    const float top = quant::top16(quant::top8(v));
+                    if ((lane & 15) == i) mine = fmaxf(top, quant::kLeast);
+                }
+                const float unit = __fdiv_rn(quant::kTop, mine);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float v[8] = {f[i][0].x, f[i][0].y, f[i][1].x, f[i][1].y, f[i][2].x, f[i][2].y, f[i][3].x, f[i][3].y};
+                    const uint2 codes = quant::codes8(v, quant::unit_of(unit, lane, i));
+                    if (lane + 32 * i < nc) *(reinterpret_cast<uint2 *>(dst) + lane + 32 * i) = codes;
+                }
+                if ((lane & 15) < 2) {  // chunk 16 * block is the block's first
+                    const int block = lane / 16 + 2 * (lane & 15);
+                    *(reinterpret_cast<float *>(dst + a.d_c) + block) = 16 * block < nc ? __fdiv_rn(mine, quant::kTop) : 0.f;
                 }
                 if (key.active)
                     *reinterpret_cast<uint32_t *>(dst + a.d_c + quant::kScaleBytes + 2 * key.at) = sm100::pack_bf16x2(k.x, k.y);

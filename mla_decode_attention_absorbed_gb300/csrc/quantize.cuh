@@ -56,12 +56,23 @@ __device__ __forceinline__ float top8(const float (&f)[8]) {
     for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
     return top;
 }
+// The same of 8 bf16 values as they come, two at a time (max.bf16x2 leaves a NaN out, too).
+__device__ __forceinline__ float top8(uint4 v) {
+    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+    auto pair = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+    const float2 f = __bfloat1622float2(__hmax2(__hmax2(pair(w[0]), pair(w[1])), __hmax2(pair(w[2]), pair(w[3]))));
+    return fmaxf(fmaxf(f.x, 0.f), f.y);
+}
 // The largest of 16 neighbouring lanes, which hold a block of 128 values, 8 each.
 __device__ __forceinline__ float top16(float top) {
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     return top;
 }
+// 448 / A of block `which` of the calling lane's 16, of which lane i holds block i's in `mine`: a
+// division takes as long as all the rest of a block's work for a lane, so each is made once.
+__device__ __forceinline__ float unit_of(float mine, int lane, int which) { return __shfl_sync(~0u, mine, (lane & 16) | which); }
+
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float unit) {
     return make_uint2(e4m3x2(f[0] * unit, f[1] * unit) | e4m3x2(f[2] * unit, f[3] * unit) << 16,
                       e4m3x2(f[4] * unit, f[5] * unit) | e4m3x2(f[6] * unit, f[7] * unit) << 16);
