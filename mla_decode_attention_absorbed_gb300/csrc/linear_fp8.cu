@@ -153,16 +153,46 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *s
 __device__ __forceinline__ void arrive_taken(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool try_taken(uint64_t *bar, uint32_t parity) {
+// Whether a phase is over: at once, or after the hardware's own short wait for it (which lasts longer than
+// a limit of microseconds).  kCluster: of a barrier that arrive_taken arrives on.
+template <bool kCluster>
+__device__ __forceinline__ bool is_over(uint64_t *bar, uint32_t parity, bool at_once) {
+    if (!kCluster) return at_once ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if (at_once)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
     return ok != 0;
+}
+// A whole warp's wait for work (see Patience), unless it is `done` already.  The clocks are read only
+// once a first try has not been enough (read before it, as by warp_wait, they were part of every block's
+// time).
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_for(bool done, uint64_t *bar, uint32_t parity, const Patience &p) {
+    const bool at_once = p.ns < 1000000;
+    if (__all_sync(~0u, done || is_over<kCluster>(bar, parity, at_once))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    const long long c0 = clock64();
+    for (uint32_t it = 0;; ++it) {
+        if (__all_sync(~0u, is_over<kCluster>(bar, parity, at_once))) return true;
+        if ((it & 15u) == 0 && __any_sync(~0u, p.over(t0, c0))) {
+            *p.abort_flag = 1;
+            return false;
+        }
+    }
 }
 
 // For what comes once the waits for work have ended, one way or the other (a whole warp).
@@ -277,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int n0 = seg.tile / plan.tiles_m * kCols + half * 64;
                 for (int kc = seg.k0; kc < seg.k1; ++kc) {
                     // the first round's waits are for the phase before the barriers' first: over at once
-                    if (!warp_wait(free, &empty[s], phase, patience)) {
+                    if (!wait_for(free, &empty[s], phase, patience)) {
                         ok = false;
                         break;
                     }
@@ -314,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) *abort_flag = 1;
             } else if (half == 0) {
                 for (uint32_t i = tail; i < issued; ++i)
-                    ok = ok && warp_wait(false, &full[i % L::kStages], (i / L::kStages) & 1, patience);
+                    ok = ok && wait_for(false, &full[i % L::kStages], (i / L::kStages) & 1, patience);
                 if (!ok && lane < 2 * plan.cluster) st_cluster_u32(map_to_rank(smem_u32((const void *)gave_up), lane), 1);
             } else if (lane == 0) {
                 st_cluster_u32(map_to_rank(smem_u32((const void *)peer_issued), leader), issued);
@@ -334,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && walk.next(seg)) {
                 for (int kc = seg.k0; ok && kc < seg.k1; ++kc, ++n) {
                     const uint32_t b = n % L::kBufs, taken = (n / L::kBufs - 1) & 1;
-                    if (!warp_wait(there, &full[s], phase, patience)) {
+                    if (!wait_for(there, &full[s], phase, patience)) {
                         ok = false;
                         break;
                     }
@@ -348,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < L::kParts; ++h) {
                         uint64_t *mine = &acc_empty[L::kParts * b + h];
-                        if (n >= L::kBufs && !warp_wait<kPair>(try_taken(mine, taken), mine, taken, patience)) {
+                        if (n >= L::kBufs && !wait_for<true>(false, mine, taken, patience)) {
                             ok = false;
                             break;
                         }
@@ -458,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok || kc + j >= k1) continue;
                     const uint32_t b = n % L::kBufs, parity = (n / L::kBufs) & 1;
                     uint64_t *ready = acc_full + L::kParts * b + part_of_acc;
-                    ok = warp_wait(mbar_try_wait(ready, parity), ready, parity, patience);
+                    ok = wait_for(false, ready, parity, patience);
                     // a warp that gave up holds the accumulator: its arrivals, which wait for nothing, would
                     // stand for those of a warp that still reads
                     if (!ok) continue;

@@ -1,5 +1,6 @@
 """Plain 64-bit implementations of the operators around the attention, from their definitions: rotary positions, page
-tables, the latent store and the matrix product with its epilogue.  Test infrastructure only."""
+tables, the latent store, the matrix product with its epilogue, and values in blocks of 128 with a scale each.  Test
+infrastructure only."""
 from __future__ import annotations
 
 import math
@@ -67,6 +68,32 @@ def linear(x, w, bias=None, residual=None, name: str = "none") -> torch.Tensor:
         y = y + bias.double()
     y = act(name, y)
     return y if residual is None else y + residual.double()
+
+
+def spread(scales: torch.Tensor, rows: int, M: int, K: int) -> torch.Tensor:
+    """Scales of blocks of rows x 128 as one a value."""
+    return scales.double().repeat_interleave(rows, 0)[:M].repeat_interleave(128, 1)[:, :K]
+
+
+def blocks(y: torch.Tensor, rows: int = 1):
+    """The quotients that are rounded to codes (their largest 448 in a block) and the scales [M / rows, K / 128]; a NaN
+    is left out of its block's scale."""
+    y = y.double()
+    M, K = y.shape
+    scales = torch.empty(-(-M // rows), -(-K // 128), dtype=torch.float64)
+    for i in range(scales.shape[0]):
+        for j in range(scales.shape[1]):
+            part = y[rows * i:rows * i + rows, 128 * j:128 * j + 128].abs()
+            part = part[~torch.isnan(part)]
+            scales[i, j] = max(float(part.max()) if part.numel() else 0.0, 2.0 ** -100) / 448
+    return y / spread(scales, rows, M, K), scales
+
+
+def linear_fp8(x, x_scale, w, w_scale, bias=None, residual=None, name: str = "none") -> torch.Tensor:
+    """x [M, K], w [N, K] codes, x_scale [K / 128, M], w_scale [N / 128, K / 128]."""
+    (M, K), N = x.shape, w.shape[0]
+    xv = x.double() * spread(x_scale.t(), 1, M, K)
+    return linear(xv, (w.double() * spread(w_scale, 128, N, K)).t(), bias, residual, name)
 
 
 SEQLEN, PAGE, SHAPE = 3, 9, 2

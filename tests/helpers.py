@@ -117,3 +117,23 @@ LINEAR_FORMS = {
     (256, 128, 8, 0): (1237, 14288, 136), (256, 128, 1, 1): (2869, 13720, 864),
     (256, 256, 1, 0): (5234, 904, 392), (256, 256, 2, 0): (3310, 4648, 280), (256, 256, 4, 0): (1604, 5968, 272),
 }
+
+# The same of mla_linear_fp8, (rows a tile, columns a tile, parts of K, rounds of whole tiles: 0, 1 or 2 for more) to (M, K, N).
+LINEAR_FP8_FORMS = {
+    (128, 64, 1, 1): (3, 208, 136), (128, 64, 2, 0): (2, 1216, 4840), (128, 64, 4, 0): (5, 912, 136),
+    (128, 64, 8, 0): (121, 1968, 136), (128, 128, 1, 1): (3, 208, 9864), (128, 128, 1, 2): (3, 208, 20552),
+    (128, 128, 2, 0): (1, 1520, 5216), (128, 128, 2, 1): (2, 688, 20464), (128, 128, 4, 0): (1, 944, 2520),
+    (128, 128, 4, 1): (1, 1088, 20056), (128, 128, 8, 0): (1, 2096, 1008),
+    (256, 256, 1, 1): (135, 208, 10784), (256, 256, 1, 2): (157, 208, 19496), (256, 256, 2, 0): (130, 8272, 6584),
+    (256, 256, 2, 1): (529, 2928, 8232), (256, 256, 4, 0): (171, 9664, 3088),
+}
+
+
+def linear_fp8_form(M: int, K: int, N: int):
+    """The form that mla_linear_fp8 takes for a product."""
+    c = mla.linear_fp8_cut(M, K, N)
+    tiles = -(-M // c.tile_rows) * -(-N // c.tile_columns)
+    units = c.ctas // (2 if c.tile_rows == 256 else 1)
+    if c.k_parts == 1:
+        return c.tile_rows, c.tile_columns, 1, 1 if tiles <= units else 2
+    return c.tile_rows, c.tile_columns, c.k_parts, 0 if units == tiles * c.k_parts else 1
