@@ -9,14 +9,14 @@
 // are the tokens and its columns those of the output: a lane then has one token, a warp's columns lie
 // in one block of W, and a value costs half an instruction (two fp32 multiply-adds each).
 //
-// A tile is 128 tokens x 64 or 128 columns on one CTA, or 256 x 256 on a pair of CTAs, each of which
-// loads half of both operands and holds the sums of its 128 tokens.  K runs in blocks of 128 through
-// a ring of TMA stages.  The CTAs take whole tiles one after another, or, where there are few tiles,
-// the 2, 4 or 8 CTAs (or pairs) of a cluster take equal parts of a tile's K, exchange their sums through
-// distributed shared memory and finish a share of its columns each.  Parts are added in the order of K,
-// so results do not depend on timing.
+// A tile is 128 tokens x 64 or 128 columns on one CTA, or 256 x 128 or 256 on a pair of CTAs, each of
+// which loads half of both operands and holds the sums of its 128 tokens.  K runs in blocks of 128
+// through a ring of TMA stages.  The CTAs take whole tiles one after another; of a tile that is left (or of
+// all, where there are few) the 2, 4 or 8 CTAs or pairs of a cluster take equal parts of K, exchange their
+// sums through distributed shared memory and finish a share of the columns each.  Parts are added in the
+// order of K, so results do not depend on timing.
 //
-// Warps: 0 issues the loads, 1 the MMAs, 4-11 hold the sums.
+// Warps: 0 issues the loads, 1 the MMAs, 2 moves residuals in and outputs out, 4-11 hold the sums.
 #include <limits.h>
 
 #include <atomic>
@@ -56,7 +56,7 @@ struct Smem {
     static constexpr int kStages = (227 * 1024 - 2048 - kTile) / kStage;
     static constexpr int kBytes = kStages * kStage + kTile + 1024 /* barriers */ + 1024 /* alignment */;
     static constexpr int kBufs = 512 / kCols;  // accumulators: a block of K each
-    static constexpr int kParts = kPair ? 2 : 1;  // of a block's accumulator, see the MMA warp
+    static constexpr int kParts = kCols == 256 ? 2 : 1;  // of a block's accumulator, see the MMA warp
     static_assert(kRows * kCols * 4 <= kStages * kStage, "a cluster's sums are exchanged in the ring");
     static_assert(kBytes <= 232448, "shared memory over the per-CTA limit");
 };
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(st, &tm_x, lead, kc * kBK, t0);
                             // the first 128 columns' half, and the second's
                             tma_load_2d_pair(st + L::kXBytes, &tm_w, lead, kc * kBK, n0);
-                            tma_load_2d_pair(st + L::kXBytes + 64 * kBK, &tm_w, lead, kc * kBK, n0 + 128);
+                            if (L::kParts == 2) tma_load_2d_pair(st + L::kXBytes + 64 * kBK, &tm_w, lead, kc * kBK, n0 + 128);
                         } else {
                             mbar_arrive_expect_tx(bar, plan.x_rows * kBK + L::kWBytes);
                             tma_load_2d(st, &tm_x, bar, kc * kBK, t0);
@@ -652,16 +652,27 @@ cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
 
 }  // namespace
 
-// The plan with the shortest estimate, in SM cycles.
+// The plan with the shortest estimate, in SM cycles.  What the parts were measured to take (timings of
+// every form and cluster at 30 sizes, clock traces at four of them):
+//   a block of a tile   450 cycles at 128 x 64, 560 at 128 x 128, 510 at 256 x 128 on a pair and 860 at
+//                       256 x 256 on a pair (the MMAs alone: 512); all of them together at least what it
+//                       takes the card to bring the weights, at 3500 bytes a cycle
+//   a tile's epilogue   1500 cycles and 10 a column
+//   a shared tile       4000 cycles of barriers, the sums sent at 12 bytes a cycle, and the finish
+// E.g. 64 x 16384 x 7168: 27.9 us in clusters of 2, 35.5 in whole tiles of 64 columns, 40 of 128; 256 x
+// 7168 x 24576: 54 us whole and shared, 58 whole; 1024 x 7168 x 7168: 51.5 us in pairs' tiles of 128
+// columns, 61.5 of 256; 4096 x 16384 x 7168: 334 us in pairs' tiles of 256 columns, 439 of 128, 464 on
+// single CTAs; 64 x 7168 x 576: 7.1 us in clusters of 8, 18 in whole tiles.  Over 30 sizes from 1 x 7168 x
+// 576 up the choice was within 12 % of the best form timed, within 5 % for all but three.
 LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
     Plan best{};
     double best_cost = 0.0;
     const double weights = 1.0 * K * N / 3500.0;  // however they are dealt out
     const int nk = (K + kBK - 1) / kBK;
-    for (int form = 0; form < 3; ++form) {
+    for (int form = 0; form < 4; ++form) {
         Plan p;
-        p.pair = form == 2;
-        p.columns = form == 0 ? 64 : form == 1 ? 128 : 256;
+        p.pair = form >= 2;
+        p.columns = form == 0 ? 64 : form == 2 ? 256 : 128;
         const int tile_m = p.pair ? 2 * kRows : kRows;
         if (p.pair && M <= kRows) break;
         p.x_rows = M < kRows ? (M + 7) / 8 * 8 : kRows;
@@ -670,7 +681,7 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
         p.nk = nk;
         const long long tiles = (long long)p.tiles_m * p.tiles_n;
         if (tiles > (1ll << 28)) continue;
-        const double block = p.pair ? 800.0 : form == 1 ? 560.0 : 450.0, epilogue = 1500.0 + 10.0 * p.columns;
+        const double block = form == 0 ? 450.0 : form == 1 ? 560.0 : form == 2 ? 860.0 : 510.0, epilogue = 1500.0 + 10.0 * p.columns;
         const int rows = M < kRows ? M : kRows;
         for (p.cluster = 1; p.cluster <= (p.pair ? 4 : 8); p.cluster *= 2) {
             const int ctas = p.pair ? 2 * p.cluster : p.cluster;
@@ -704,7 +715,7 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
 }
 
 cudaError_t launch_linear_fp8(const LinearFp8Args &a, const LinearFp8Plan &p, cudaStream_t st) {
-    if (p.pair) return launch<256, true>(a, p, st);
+    if (p.pair) return p.columns == 256 ? launch<256, true>(a, p, st) : launch<128, true>(a, p, st);
     return p.columns == 128 ? launch<128>(a, p, st) : launch<64>(a, p, st);
 }
 

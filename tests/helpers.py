@@ -124,8 +124,10 @@ LINEAR_FP8_FORMS = {
     (128, 64, 8, 0): (121, 1968, 136), (128, 128, 1, 1): (3, 208, 9864), (128, 128, 1, 2): (3, 208, 20552),
     (128, 128, 2, 0): (1, 1520, 5216), (128, 128, 2, 1): (2, 688, 20464), (128, 128, 4, 0): (1, 944, 2520),
     (128, 128, 4, 1): (1, 1088, 20056), (128, 128, 8, 0): (1, 2096, 1008),
-    (256, 256, 1, 1): (135, 208, 10784), (256, 256, 1, 2): (157, 208, 19496), (256, 256, 2, 0): (130, 8272, 6584),
-    (256, 256, 2, 1): (529, 2928, 8232), (256, 256, 4, 0): (171, 9664, 3088),
+    (256, 128, 1, 1): (143, 208, 5144), (256, 128, 1, 2): (1547, 208, 2608), (256, 128, 2, 0): (3561, 4048, 144),
+    (256, 128, 2, 1): (166, 2912, 20104), (256, 128, 4, 0): (153, 3872, 1448),
+    (256, 256, 1, 1): (135, 208, 10784), (256, 256, 1, 2): (300, 208, 38008), (256, 256, 2, 0): (156, 15664, 4912),
+    (256, 256, 2, 1): (1039, 4544, 4904), (256, 256, 4, 0): (397, 18272, 1352),
 }
 
 

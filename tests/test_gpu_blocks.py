@@ -296,7 +296,7 @@ def test_linear_fp8_in_place_on_the_residual_stream():
 
 def test_linear_fp8_repeats_bit_for_bit():
     g = gen(32)
-    for M, K, N in ((64, 16384, 1024), (333, 1008, 1544), (1, 8192, 264), (8, 1008, 20480), (529, 2928, 8232)):
+    for M, K, N in ((64, 16384, 1024), (333, 1008, 1544), (1, 8192, 264), (8, 1008, 20480), (529, 2928, 8232), (166, 2912, 20104)):
         args = [t.to(DEV) for t in operands(g, M, K, N, False)]
         a = mla.linear_fp8(*args)
         for _ in range(4):
@@ -372,7 +372,7 @@ def test_linear_fp8_offsets_past_32_bits():
 TIMEOUT_CASES = [
     # M, K, N: whole tiles, clusters, pairs in several rounds, whole tiles and a shared one, clusters of pairs
     (333, 1008, 1544), (64, 16384, 1024), (3, 65536, 136), (8, 4112, 20480), (5000, 1040, 6000), (250, 8208, 7000),
-    (529, 2928, 8232), (171, 9664, 3088),
+    (529, 2928, 8232), (171, 9664, 3088), (1039, 4544, 4904), (397, 18272, 1352), (166, 2912, 20104), (153, 3872, 1448),
 ]
 
 
