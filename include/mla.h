@@ -325,10 +325,10 @@ MLA_API int mla_decode_attn_noalloc(const mla_dims *dims, const void *q_cat, con
 /* Diagnostics (the pages have no counterpart): the bound, in nanoseconds, of
  * every wait for work inside the attention kernels launched from now on by this
  * process (mla_decode_attn, mla_decode_step, the sparse, prefill and no-alloc
- * entry points) and mla_linear.  A wait that runs out records MLA_ERR_TIMEOUT in
+ * entry points), mla_linear and mla_linear_fp8.  A wait that runs out records MLA_ERR_TIMEOUT in
  * the status word; the kernel then drains the copies and MMAs it has in flight
  * (those waits keep the default bound) and returns, outputs undefined (those of
- * mla_linear NaN or right).  0 restores the default, 2 s.  For tests of the timeout
+ * the products NaN or right).  0 restores the default, 2 s.  For tests of the timeout
  * path and for diagnosing a stalled GPU; not for production use.  Always returns
  * MLA_OK. */
 MLA_API int mla_set_wait_limit_ns(unsigned long long ns);

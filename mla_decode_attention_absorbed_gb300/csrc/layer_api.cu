@@ -383,9 +383,11 @@ MLA_API long long mla_latent_row_bytes(const mla_dims *dims) {
 
 MLA_API int mla_latent_load(const mla_dims *dims, const mla_cache *cache, int rows, const int *positions, void *out,
                             long long out_stride, int *status, void *stream) {
-    int s = check_tokens(dims);
+    if (!dims) return MLA_ERR_NULL;
+    if (dims->B < 0) return MLA_ERR_SHAPE;
+    if (dims->B > 65535) return MLA_ERR_UNSUPPORTED;
+    int s = check_widths(dims);
     if (s) return s;
-    if ((s = check_widths(dims))) return s;
     if ((s = check_store_cache(dims, cache))) return s;
     const long long W = dims->d_c + dims->d_rope;
     if (rows < 0 || out_stride < rows * W) return MLA_ERR_SHAPE;

@@ -83,8 +83,6 @@ struct Finish {
     float bias[8];
     uint4 res[2];
 
-    enum NoBias { kNoBias };  // of a use that loads residuals alone
-    __device__ __forceinline__ Finish(const LinearArgs &, int t0, int n, NoBias) : t0(t0), n(n) {}
     __device__ __forceinline__ Finish(const LinearArgs &a, int t0, int n) : t0(t0), n(n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) bias[e] = 0.f;

@@ -48,19 +48,6 @@ inline bool encode_bf16_sw128(CUtensorMap *m, const void *base, int rank, const 
     return r == CUDA_SUCCESS;
 }
 
-// A matrix of bytes (8-bit codes), 128-byte swizzle: `width` bytes a row, rows `stride` bytes apart (a
-// multiple of 16), boxes of 128 bytes x box_rows.  Out-of-range elements read as zero.
-inline bool encode_u8_sw128(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, uint64_t stride,
-                            uint32_t box_rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t gd[2] = {width, rows}, gs[1] = {stride};
-    const cuuint32_t bd[2] = {128, box_rows}, es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), gd, gs, bd, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
-}
-
 // A rank-`rank` tensor of 32-bit elements, no swizzle (rows land row-major in
 // shared memory at the box's width): dims[0] is the contiguous dimension in
 // 32-bit units, strides_bytes the byte strides of dims 1..rank-1 (multiples of

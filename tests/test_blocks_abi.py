@@ -193,7 +193,8 @@ def test_load_refusals(lib):
     bad = cache()
     bad.kv_dtype = 2
     assert call(c=bad) == 6
-    assert call(rows=0, out=NUL) == 0 and call(d=dims(B=0), out=NUL) == 0
+    assert call(rows=0, out=NUL) == 0 and call(d=dims(B=0), out=NUL) == 0 and call(d=dims(B=-1)) == 2
+    assert call(d=dims(B=65535, s_q=1 << 21, H=-1), rows=0, out=NUL) == 0  # of the sizes, B and the widths alone are read
 
 
 # ---------------------------------------------------------------------------------------------------------- python
