@@ -2,7 +2,14 @@
 // (activations), or of 128 x 128 (weights); activations on request after their RMS norm.
 //
 // Every value is read once, as 16 bytes a lane; 16 lanes hold 128 values of a row, so a
-// row's block is one reduction over half a warp.
+// row's block is one reduction over half a warp.  The two divisions of a block are made once, by
+// the lane that holds its maximum for the others (made by every lane, and with rows 8 to a warp in fp32
+// instead of pairs of bf16: 4096 x 16384 43.0 us, so 33.6).
+//
+// Measured (device time; copies at the card's measured rate): rows of 4096 x 16384 33.6 us against 29.9 of bytes, squares of
+// 7168 x 16384 50.7 against 51.9, both bound by HBM; after the norm 4096 x 7168 20.8 against 13.1, bound by
+// the chain load - sum - barrier - maximum - code with four CTAs an SM (the next row on its way meanwhile,
+// in persistent CTAs of twice the registers: 20.9); 16384 x 512 7.2 against 3.7; 64 x 7168 2.5, a launch and a round trip.
 #include "quantize.cuh"
 
 namespace mla {
