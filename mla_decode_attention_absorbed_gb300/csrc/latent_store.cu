@@ -15,9 +15,9 @@
 // row waits for its length and then for its page; the half layout 0.4 more.  On one set, in L2,
 // 10.9 and 11.7.  64 rows: 2.3 us, a launch and a round trip.
 //
-// Into rows of blocks (codes of the latent with a scale for each 128 values, the key in bf16) 16.8 us of 8.8,
-// bound by instructions, of which a row has about 350 whatever its width (the rotation, two reductions of the maxima and
-// the division on top of the norm's; half of a half warp's lanes make the divisions for the others).
+// Into rows of blocks (codes of the latent with a scale for each 128 values, the key in bf16) 14.9 us of 8.8,
+// bound by instructions, of which a row has about 320 whatever its width (the rotation, the two blocks' maxima
+// and the division on top of the norm's).
 #include "quantize.cuh"
 #include "rope.cuh"
 
@@ -25,12 +25,15 @@ namespace mla {
 namespace {
 
 using quant::e4m3x2;
+using quant::mul2;
 using quant::unpack;
 
 constexpr int kWarps = 4;  // warps a CTA
 // As many as the 72 registers of each variant allow: 32768 rows in L2 10.9 us, with 6 11.1, with
 // 8 11.9 (a second wave for the eighth), with 12 11.3, one warp a token without the loop 14.3.
 constexpr int kCtasPerSm = 7;
+// Rows of blocks, bound by instructions: 14.9, with 5 15.4, with 7 17.2.
+constexpr int kCtasPerSmBlocks = 6;
 
 // What a warp reads of one token before it can compute: the row, and where it goes.
 struct Row {
@@ -60,7 +63,6 @@ struct KeyLane {
     }
 };
 
-// Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     unsigned long long r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
@@ -69,14 +71,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
           "l"(*reinterpret_cast<unsigned long long *>(&c)));
     return *reinterpret_cast<float2 *>(&r);
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-    return *reinterpret_cast<float2 *>(&r);
-}
-
 template <bool kHalf>
 __device__ __forceinline__ Row load_row(const StoreArgs &a, int t, int lane) {
     Row r;
@@ -198,23 +192,25 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
             if (kDtype == MLA_KV_E4M3_BLOCKS) {
                 // 16 lanes hold a block of the latent; the key keeps bf16
                 uint8_t *dst = const_cast<uint8_t *>(static_cast<const uint8_t *>(a.cache.kv)) + at;
-                float mine = 0.f;  // lane i of a half holds the i-th chunk's block's
+                float v[2][8], top[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float v[8] = {f[i][0].x, f[i][0].y, f[i][1].x, f[i][1].y, f[i][2].x, f[i][2].y, f[i][3].x, f[i][3].y};
-                    const float top = quant::top16(quant::top8(v));
-                    if ((lane & 15) == i) mine = fmaxf(top, quant::kLeast);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[i][2 * e] = f[i][e].x;
+                        v[i][2 * e + 1] = f[i][e].y;
+                    }
+                    top[i] = quant::top8(v[i]);
                 }
-                const float unit = __fdiv_rn(quant::kTop, mine);
+                const float mine = quant::unit_or_scale(quant::tops16(top, lane), lane);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float v[8] = {f[i][0].x, f[i][0].y, f[i][1].x, f[i][1].y, f[i][2].x, f[i][2].y, f[i][3].x, f[i][3].y};
-                    const uint2 codes = quant::codes8(v, quant::unit_of(unit, lane, i));
+                    const uint2 codes = quant::codes8(v[i], quant::unit_of<2>(mine, lane, i));
                     if (lane + 32 * i < nc) *(reinterpret_cast<uint2 *>(dst) + lane + 32 * i) = codes;
                 }
-                if ((lane & 15) < 2) {  // chunk 16 * block is the block's first
-                    const int block = lane / 16 + 2 * (lane & 15);
-                    *(reinterpret_cast<float *>(dst + a.d_c) + block) = 16 * block < nc ? __fdiv_rn(mine, quant::kTop) : 0.f;
+                if (lane % 8 == 1) {  // chunk 16 * block is the block's first
+                    const int block = lane / 16 + 2 * (lane / 8 % 2);
+                    *(reinterpret_cast<float *>(dst + a.d_c) + block) = 16 * block < nc ? mine : 0.f;
                 }
                 if (key.active)
                     *reinterpret_cast<uint32_t *>(dst + a.d_c + quant::kScaleBytes + 2 * key.at) = sm100::pack_bf16x2(k.x, k.y);
@@ -252,7 +248,8 @@ __global__ void __launch_bounds__(32 * kWarps) latent_rows(const __grid_constant
 
 cudaError_t launch_latent_store(const StoreArgs &a, cudaStream_t st) {
     int grid = (a.tokens + kWarps - 1) / kWarps;
-    if (grid > layer_num_sms() * kCtasPerSm) grid = layer_num_sms() * kCtasPerSm;
+    const int most = layer_num_sms() * (a.dtype == MLA_KV_E4M3_BLOCKS ? kCtasPerSmBlocks : kCtasPerSm);
+    if (grid > most) grid = most;
     const bool half = a.rotate && a.plan.layout == MLA_ROPE_HALF;
     auto launch = [&](auto with_half, auto without) {
         if (half) with_half<<<grid, 32 * kWarps, 0, st>>>(a);

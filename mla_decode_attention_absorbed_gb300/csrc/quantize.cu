@@ -2,14 +2,16 @@
 // (activations), or of 128 x 128 (weights); activations on request after their RMS norm.
 //
 // Every value is read once, as 16 bytes a lane; 16 lanes hold 128 values of a row, so a
-// row's block is one reduction over half a warp.  The two divisions of a block are made once, by
-// the lane that holds its maximum for the others (made by every lane, and with rows 8 to a warp in fp32
-// instead of pairs of bf16: 4096 x 16384 43.0 us, so 33.6).
+// row's block is a reduction over half a warp, and those of up to 8 blocks are one.  Each of the two divisions
+// of a block is made once, by a lane that holds its maximum for the others (made by every lane: 4096 x 16384 43.0 us;
+// by one, with a reduction for each block, 33.6; so 31.1).
 //
-// Measured (device time; copies at the card's measured rate): rows of 4096 x 16384 33.6 us against 29.9 of bytes, squares of
-// 7168 x 16384 50.7 against 51.9, both bound by HBM; after the norm 4096 x 7168 20.8 against 13.1, bound by
+// Measured (device time; copies at the card's measured rate): rows of 4096 x 16384 31.1 us against 29.9 of bytes, squares of
+// 7168 x 16384 50.7 against 51.9, both bound by HBM; after the norm 4096 x 7168 20.2 against 13.1, bound by
 // the chain load - sum - barrier - maximum - code with four CTAs an SM (the next row on its way meanwhile,
-// in persistent CTAs of twice the registers: 20.9); 16384 x 512 7.2 against 3.7; 64 x 7168 2.5, a launch and a round trip.
+// in persistent CTAs of twice the registers: 20.9 when this took 20.8; the weight's load before the barrier, which
+// spills: 27.9; bf16 kept and normalised twice, for more CTAs an SM: 23.8); 16384 x 512 7.0 against 3.7;
+// 64 x 7168 2.6, a launch and a round trip.
 #include "quantize.cuh"
 
 namespace mla {
@@ -37,22 +39,20 @@ __global__ void __launch_bounds__(kThreads, 4) quantize_rows(const QuantizeArgs 
         v[r] = make_uint4(0, 0, 0, 0);
         if (r < rows && k < a.K) v[r] = *reinterpret_cast<const uint4 *>(a.x + (m0 + r) * a.x_stride + k);
     }
-    float mine = kLeast;  // lane r of a half holds row r's
+    float top[kRowsAWarp];
 #pragma unroll
-    for (int r = 0; r < kRowsAWarp; ++r) {
-        const float top = top16(top8(v[r]));
-        if ((lane & 15) == r) mine = fmaxf(top, kLeast);
-    }
-    const float unit = __fdiv_rn(kTop, mine);
+    for (int r = 0; r < kRowsAWarp; ++r) top[r] = top8(v[r]);
+    const float mine = unit_or_scale(tops16(top, lane), lane);
 #pragma unroll
     for (int r = 0; r < kRowsAWarp; ++r) {
         float f[8];
         unpack8(v[r], f);
-        const uint2 codes = codes8(f, unit_of(unit, lane, r));
+        const uint2 codes = codes8(f, unit_of<kRowsAWarp>(mine, lane, r));
         if (r < rows && k < a.K) *reinterpret_cast<uint2 *>(a.codes + (m0 + r) * a.code_stride + k) = codes;
     }
-    if ((lane & 15) < rows && (k & ~(kBlock - 1)) < a.K)
-        a.scales[(long long)(k / kBlock) * a.scale_stride + m0 + (lane & 15)] = __fdiv_rn(mine, kTop);
+    const int row = (lane & 15) / (16 / kRowsAWarp);
+    if (lane % 2 == 1 && row < rows && (k & ~(kBlock - 1)) < a.K)
+        a.scales[(long long)(k / kBlock) * a.scale_stride + m0 + row] = mine;
 }
 
 // The sum over a CTA's warps, of any number up to kMostThreads / 32.
@@ -104,27 +104,34 @@ __global__ void __launch_bounds__(kMostThreads, 2) quantize_normed(const Quantiz
     const float inv = rsqrtf(sum / (float)a.K + a.eps);
     for (int c0 = 0; c0 < nc; c0 += kParts * step) {
         if (kAgain) load(c0);
-        // whole half warps are at work on a block, or beyond the row; lane i of a half holds part i's
-        float mine = kLeast;
+        // whole half warps are at work on a block, or beyond the row
+        float top[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const int c = c0 + i * step + t;
-            float w[8];
-            unpack8(c < nc ? __ldg(weight + c) : make_uint4(0, 0, 0, 0), w);
+            const uint4 w = c < nc ? __ldg(weight + c) : make_uint4(0, 0, 0, 0);
+            const float2 inv2 = make_float2(inv, inv);
+            float g[8];
+            unpack8(w, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] * inv * w[e];
-            const float top = top16(top8(y[i]));
-            if ((lane & 15) == i) mine = fmaxf(top, kLeast);
+            for (int e = 0; e < 8; e += 2) {
+                const float2 p = mul2(mul2(make_float2(y[i][e], y[i][e + 1]), inv2), make_float2(g[e], g[e + 1]));
+                y[i][e] = p.x;
+                y[i][e + 1] = p.y;
+            }
+            top[i] = top8(y[i]);
         }
-        const float unit = __fdiv_rn(kTop, mine);
+        const float mine = unit_or_scale(tops16(top, lane), lane);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             const int c = c0 + i * step + t;
-            const uint2 codes = codes8(y[i], unit_of(unit, lane, i));
+            const uint2 codes = codes8(y[i], unit_of<kParts>(mine, lane, i));
             if (c < nc) dst[c] = codes;
         }
-        const int block = (c0 + (lane & 15) * step + t - (lane & 15)) / 16;
-        if ((lane & 15) < kParts && block * 16 < nc) a.scales[(long long)block * a.scale_stride + m] = __fdiv_rn(mine, kTop);
+        // of a part's 16 / kParts lanes the second has its scale
+        constexpr int kLanes = 16 / kParts;
+        const int block = (c0 + (lane & 15) / kLanes * step + t - (lane & 15)) / 16;
+        if (lane % kLanes == 1 && block * 16 < nc) a.scales[(long long)block * a.scale_stride + m] = mine;
         if (!kAgain) break;
     }
 }
@@ -166,22 +173,16 @@ cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t st) {
     if (a.block_rows != 1) {
         quantize_squares<<<dim3((a.K + kBlock - 1) / kBlock, (a.M + kBlock - 1) / kBlock), kThreads, 0, st>>>(a);
     } else if (a.weight) {
-        // a warp a row up to 1024 values (16384 rows of 512: 7.2 us, a CTA a row 17.6), then a CTA's 256
-        // threads up to 8192, then 512
+        // a warp a row up to 1024 values (16384 rows of 512: 6.9 us, a CTA a row 17.6), then as many warps as
+        // 1024 values each take, up to 16 (4096 rows of 2048, 5120 and 12288: 6.9, 14.4 and 38.3 us; with
+        // 256 threads, past 8192 512, that hold less each or stand idle: 8.7, 18.4, 41.1)
         const int nc = a.K / 8;
-        if (nc <= 128) {
-            const unsigned grid = (a.M + kThreads / 32 - 1) / (kThreads / 32);
-            if (nc <= 32) quantize_normed<1, true, false><<<grid, kThreads, 0, st>>>(a);
-            else if (nc <= 64) quantize_normed<2, true, false><<<grid, kThreads, 0, st>>>(a);
-            else quantize_normed<4, true, false><<<grid, kThreads, 0, st>>>(a);
-        } else {
-            const int most = nc <= 4 * kThreads ? kThreads : kMostThreads, threads = nc < most ? (nc + 31) / 32 * 32 : most;
-            const int parts = (nc + threads - 1) / threads;
-            if (parts <= 1) quantize_normed<1, false, false><<<a.M, threads, 0, st>>>(a);
-            else if (parts <= 2) quantize_normed<2, false, false><<<a.M, threads, 0, st>>>(a);
-            else if (parts <= 4) quantize_normed<4, false, false><<<a.M, threads, 0, st>>>(a);
-            else quantize_normed<4, false, true><<<a.M, threads, 0, st>>>(a);
-        }
+        const unsigned grid = (a.M + kThreads / 32 - 1) / (kThreads / 32);
+        if (nc <= 32) quantize_normed<1, true, false><<<grid, kThreads, 0, st>>>(a);
+        else if (nc <= 64) quantize_normed<2, true, false><<<grid, kThreads, 0, st>>>(a);
+        else if (nc <= 128) quantize_normed<4, true, false><<<grid, kThreads, 0, st>>>(a);
+        else if (nc <= 4 * kMostThreads) quantize_normed<4, false, false><<<a.M, (nc + 127) / 128 * 32, 0, st>>>(a);
+        else quantize_normed<4, false, true><<<a.M, kMostThreads, 0, st>>>(a);
     } else {
         const int wide = (a.K + 255) / 256;
         const long long warps = (long long)((a.M + kRowsAWarp - 1) / kRowsAWarp) * wide;

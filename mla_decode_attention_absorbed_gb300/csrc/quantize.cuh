@@ -50,6 +50,14 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
         f[2 * e + 1] = p.y;
     }
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
 __device__ __forceinline__ float top8(const float (&f)[8]) {
     float top = 0.f;
 #pragma unroll
@@ -69,9 +77,32 @@ __device__ __forceinline__ float top16(float top) {
     for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     return top;
 }
-// 448 / A of block `which` of the calling lane's 16, of which lane i holds block i's in `mine`: a
-// division takes as long as all the rest of a block's work for a lane, so each is made once.
-__device__ __forceinline__ float unit_of(float mine, int lane, int which) { return __shfl_sync(~0u, mine, (lane & 16) | which); }
+// The same for kN blocks, a power of two up to 8: lane l of the 16 gets that of block l / (16 / kN).  While
+// blocks are left to part, lanes trade halves of them: kN = 8 takes 8 trades, one by one 32.
+template <int kN>
+__device__ __forceinline__ float tops16(float (&top)[kN], int lane) {
+    int o = 8;
+#pragma unroll
+    for (int n = kN / 2; n > 0; n /= 2, o /= 2) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            top[i] = fmaxf(upper ? top[i + n] : top[i], __shfl_xor_sync(~0u, upper ? top[i] : top[i + n], o));
+    }
+#pragma unroll
+    for (int p = 8 / kN; p > 0; p /= 2) top[0] = fmaxf(top[0], __shfl_xor_sync(~0u, top[0], p));
+    return fmaxf(top[0], kLeast);
+}
+// A division takes as long as all the rest of a block's work for a lane, so each of a block's two is
+// made once: of the 16 / kN lanes that have its A, the even ones make 448 / A, the odd ones A / 448.
+__device__ __forceinline__ float unit_or_scale(float top, int lane) {
+    return __fdiv_rn(lane & 1 ? top : kTop, lane & 1 ? kTop : top);
+}
+// 448 / A of block `which`, for all of its lanes.
+template <int kN>
+__device__ __forceinline__ float unit_of(float mine, int lane, int which) {
+    return __shfl_sync(~0u, mine, (lane & 16) | which * (16 / kN));
+}
 
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float unit) {
     return make_uint2(e4m3x2(f[0] * unit, f[1] * unit) | e4m3x2(f[2] * unit, f[3] * unit) << 16,
