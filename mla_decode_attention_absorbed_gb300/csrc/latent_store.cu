@@ -15,7 +15,7 @@
 // row waits for its length and then for its page; the half layout 0.4 more.  On one set, in L2,
 // 10.9 and 11.7.  64 rows: 2.3 us, a launch and a round trip.
 //
-// Into rows of blocks (codes of the latent with a scale for each 128 values, the key in bf16) 14.9 us of 8.8,
+// Into rows of blocks (codes of the latent with a scale for each 128 values, the key in bf16) 14.5 us of 8.8,
 // bound by instructions, of which a row has about 320 whatever its width (the rotation, the two blocks' maxima
 // and the division on top of the norm's).
 #include "quantize.cuh"
@@ -25,6 +25,7 @@ namespace mla {
 namespace {
 
 using quant::e4m3x2;
+using quant::fma2;
 using quant::mul2;
 using quant::unpack;
 
@@ -32,7 +33,7 @@ constexpr int kWarps = 4;  // warps a CTA
 // As many as the 72 registers of each variant allow: 32768 rows in L2 10.9 us, with 6 11.1, with
 // 8 11.9 (a second wave for the eighth), with 12 11.3, one warp a token without the loop 14.3.
 constexpr int kCtasPerSm = 7;
-// Rows of blocks, bound by instructions: 14.9, with 5 15.4, with 7 17.2.
+// Rows of blocks, bound by instructions: 14.5, with 5 15.4, with 7 17.2.
 constexpr int kCtasPerSmBlocks = 6;
 
 // What a warp reads of one token before it can compute: the row, and where it goes.
@@ -63,14 +64,6 @@ struct KeyLane {
     }
 };
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)),
-          "l"(*reinterpret_cast<unsigned long long *>(&c)));
-    return *reinterpret_cast<float2 *>(&r);
-}
 template <bool kHalf>
 __device__ __forceinline__ Row load_row(const StoreArgs &a, int t, int lane) {
     Row r;

@@ -7,10 +7,10 @@
 // by one, with a reduction for each block, 33.6; so 31.1).
 //
 // Measured (device time; copies at the card's measured rate): rows of 4096 x 16384 31.1 us against 29.9 of bytes, squares of
-// 7168 x 16384 50.7 against 51.9, both bound by HBM; after the norm 4096 x 7168 20.2 against 13.1, bound by
-// the chain load - sum - barrier - maximum - code with four CTAs an SM (the next row on its way meanwhile,
-// in persistent CTAs of twice the registers: 20.9 when this took 20.8; the weight's load before the barrier, which
-// spills: 27.9; bf16 kept and normalised twice, for more CTAs an SM: 23.8); 16384 x 512 7.0 against 3.7;
+// 7168 x 16384 50.7 against 51.9, both bound by HBM; after the norm 4096 x 7168 20.0 against 13.1, bound by
+// instructions, about 80 for a lane's 8 values (bf16 kept and normalised twice, for more CTAs an SM: 23.8; persistent
+// CTAs that have the next rows on their way, to registers 20.9 when this took 20.8, to shared memory by cp.async 20.5, and
+// 32.6 for 4096 x 12288, so 37.7, but 12.7 for 4096 x 4096, so 11.3, and 15.5 for 5120, so 14.3); 16384 x 512 6.9 against 3.7;
 // 64 x 7168 2.6, a launch and a round trip.
 #include "quantize.cuh"
 
@@ -89,15 +89,19 @@ __global__ void __launch_bounds__(kMostThreads, 2) quantize_normed(const Quantiz
 #pragma unroll
         for (int i = 0; i < kParts; ++i) unpack8(v[i], y[i]);
     };
-    float sum = 0.f;
+    float2 sums = make_float2(0.f, 0.f);
     for (int c0 = 0; c0 < nc; c0 += kParts * step) {
         load(c0);
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(y[i][e], y[i][e], sum);
+            for (int e = 0; e < 8; e += 2) {
+                const float2 p = make_float2(y[i][e], y[i][e + 1]);
+                sums = fma2(p, p, sums);
+            }
         if (!kAgain) break;
     }
+    float sum = sums.x + sums.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     if (!kWarp) sum = sum_of_warps(sum);
@@ -174,7 +178,7 @@ cudaError_t launch_quantize(const QuantizeArgs &a, cudaStream_t st) {
         quantize_squares<<<dim3((a.K + kBlock - 1) / kBlock, (a.M + kBlock - 1) / kBlock), kThreads, 0, st>>>(a);
     } else if (a.weight) {
         // a warp a row up to 1024 values (16384 rows of 512: 6.9 us, a CTA a row 17.6), then as many warps as
-        // 1024 values each take, up to 16 (4096 rows of 2048, 5120 and 12288: 6.9, 14.4 and 38.3 us; with
+        // 1024 values each take, up to 16 (4096 rows of 2048, 5120 and 12288: 7.0, 14.0 and 37.7 us; with
         // 256 threads, past 8192 512, that hold less each or stand idle: 8.7, 18.4, 41.1)
         const int nc = a.K / 8;
         const unsigned grid = (a.M + kThreads / 32 - 1) / (kThreads / 32);

@@ -51,6 +51,14 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     }
 }
 // Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<unsigned long long *>(&c)));
+    return *reinterpret_cast<float2 *>(&r);
+}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     unsigned long long r;
     asm("mul.rn.f32x2 %0, %1, %2;"
@@ -105,8 +113,14 @@ __device__ __forceinline__ float unit_of(float mine, int lane, int which) {
 }
 
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float unit) {
-    return make_uint2(e4m3x2(f[0] * unit, f[1] * unit) | e4m3x2(f[2] * unit, f[3] * unit) << 16,
-                      e4m3x2(f[4] * unit, f[5] * unit) | e4m3x2(f[6] * unit, f[7] * unit) << 16);
+    const float2 both = make_float2(unit, unit);
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 p = mul2(make_float2(f[2 * e], f[2 * e + 1]), both);
+        c[e] = e4m3x2(p.x, p.y);
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 }  // namespace quant
