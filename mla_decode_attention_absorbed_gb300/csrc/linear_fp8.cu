@@ -18,16 +18,17 @@
 //
 // Warps: 0 issues the loads, 1 the MMAs, 2 moves residuals in and outputs out, 4-11 hold the sums.
 //
-// Measured (device time): 4096 x 16384 x 7168 in 325 to 338 us for a dozen calls = 2,850 to 2,970 TFLOP/s, 1.5
-// times the measured bf16 rate (375 us = 2,570 in a long run of them, at the power limit): a block of a pair's
-// tile takes 800 cycles where its MMAs alone would take 512, as the MMAs wait for the sums' warps, which
-// take 450 to 550 for 128 columns, and 300 pass until the MMA warp knows (without the sums, 303 us).  64 x 16384 x
-// 7168 in 27.9 us: 117 MB of weights at 6.1 TB/s in 19 us, 2.7 of start and 4 of exchange and finish.  256 x 7168 x 24576 in
-// 54 us, 333 x 1008 x 1544 in 6.4, a chain of latencies.
+// Measured (device time): 4096 x 16384 x 7168 in 320 to 330 us for a dozen calls = 2,900 to 3,000 TFLOP/s, 1.5
+// times the measured bf16 rate (380 us = 2,530 in a long run of them, at the power limit): a block of a pair's
+// tile takes 800 cycles where its MMAs alone take 560.  Copies of the kernel without one part or another: MMAs alone 226 us,
+// loads alone 203, sums alone 270, loads and MMAs 269 (what comes in and what the MMAs read share the shared memory's
+// ports), MMAs and sums 295, handshakes alone 166.  64 x 16384 x 7168 in 27.4 us: 117 MB of weights at 6.1 TB/s in 19 us,
+// 2.7 of start and 4 of exchange and finish.  256 x 7168 x 24576 in 54 us, 333 x 1008 x 1544 in 6.4, a chain of latencies.
 //
-// What the sums' warps cost was found by taking it away: arrivals that order memory (875 us), clocks read
+// What measured slower: arrivals across the pair that order memory (875 us when this took 488), clocks read
 // before each wait, an epilogue turned over through shared memory (8 us a tile: 468), the scales' addresses
-// worked out block by block (438), one barrier for both halves of a tile (a tenth).
+// worked out block by block (438), a commit for the sums and one for the stage (335 us, so 321), a block's sums in two
+// halves with a commit each (336), waits of the sums' warps that poll (326).
 #include <limits.h>
 
 #include <atomic>
@@ -67,8 +68,8 @@ struct Smem {
     static constexpr int kStages = (227 * 1024 - 2048 - kTile) / kStage;
     static constexpr int kBytes = kStages * kStage + kTile + 1024 /* barriers */ + 1024 /* alignment */;
     static constexpr int kBufs = 512 / kCols;  // accumulators: a block of K each
-    static constexpr int kParts = kCols == 256 ? 2 : 1;  // of a block's accumulator, see the MMA warp
     static_assert(kRows * kCols * 4 <= kStages * kStage, "a cluster's sums are exchanged in the ring");
+    static_assert(kStages >= kBufs, "a stage's barrier tells the sums' warps, too, see the MMA warp");
     static_assert(kBytes <= 232448, "shared memory over the per-CTA limit");
 };
 
@@ -252,11 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     using L = Smem<kCols, kPair>;
-    uint64_t *acc_full = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTile);  // [accumulator][part]
-    uint64_t *acc_empty = acc_full + L::kBufs * L::kParts;
-    uint64_t *full = acc_empty + L::kBufs * L::kParts;
-    uint64_t *empty = full + L::kStages;
-    uint64_t *drain = empty + L::kStages;
+    uint64_t *taken = reinterpret_cast<uint64_t *>(smem + L::kStages * L::kStage + L::kTile);  // an accumulator, by the sums' warps
+    uint64_t *full = taken + L::kBufs;  // a stage's copies have come
+    uint64_t *spent = full + L::kStages;  // its MMAs are done: it is free, and their sums are there
+    uint64_t *drain = spent + L::kStages;
     uint64_t *tile_free = drain + 1;  // the tile's memory holds the residual, or nothing that is needed
     uint64_t *tile_done = tile_free + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tile_done + 1);
@@ -270,12 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&spent[s], 1);
         }
-        for (int i = 0; i < L::kBufs * L::kParts; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], (kPair ? 2 : 1) * kSumWarps / L::kParts);
-        }
+        for (int i = 0; i < L::kBufs; ++i) mbar_init(&taken[i], (kPair ? 2 : 1) * kSumWarps);
         mbar_init(tile_free, 1);
         mbar_init(tile_done, kSumWarps);
         mbar_init(drain, 1);
@@ -312,13 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             const uint32_t lead_full = kPair ? map_to_rank(smem_u32(full), leader) : 0;
             uint32_t s = 0, phase = 1;
-            bool ok = true, free = mbar_test_wait(&empty[0], 1);
+            bool ok = true, free = mbar_test_wait(&spent[0], 1);
             while (ok && walk.next(seg)) {
                 const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows;
-                const int n0 = seg.tile / plan.tiles_m * kCols + half * 64;
+                const int n0 = seg.tile / plan.tiles_m * kCols + half * (kCols / 2);
                 for (int kc = seg.k0; kc < seg.k1; ++kc) {
                     // the first round's waits are for the phase before the barriers' first: over at once
-                    if (!wait_for(free, &empty[s], phase, patience)) {
+                    if (!wait_for(free, &spent[s], phase, patience)) {
                         ok = false;
                         break;
                     }
@@ -329,14 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s = 0;
                         phase ^= 1;
                     }
-                    free = mbar_test_wait(&empty[s], phase);
+                    free = mbar_test_wait(&spent[s], phase);
                     if (elect_one()) {
                         if (kPair) {
                             if (half == 0) mbar_arrive_expect_tx(bar, 2 * L::kStage);
                             tma_load_2d_pair(st, &tm_x, lead, kc * kBK, t0);
-                            // the first 128 columns' half, and the second's
                             tma_load_2d_pair(st + L::kXBytes, &tm_w, lead, kc * kBK, n0);
-                            if (L::kParts == 2) tma_load_2d_pair(st + L::kXBytes + 64 * kBK, &tm_w, lead, kc * kBK, n0 + 128);
                         } else {
                             mbar_arrive_expect_tx(bar, plan.x_rows * kBK + L::kWBytes);
                             tma_load_2d(st, &tm_x, bar, kc * kBK, t0);
@@ -362,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else if (warp == 1 && half == 0) {
-            // A block's MMAs are issued for 128 columns of a pair's tile at a time, each with a barrier
-            // of their own: the sums' warps of those columns take them while the others' are computed, and
-            // the MMAs wait for a quarter of the tensor memory at a time.
-            constexpr uint32_t idesc = idesc_e4m3(kTileM, kCols / L::kParts);
+            // A commit takes some 200 cycles of the tensor pipe's time, so a block has one: its barrier tells the load
+            // warp that the stage is free and the sums' warps that the accumulator is full.  They cannot miss a
+            // phase of it: the stage's next MMAs come after kBufs or more others, and those wait for the sums' warps.
+            constexpr uint32_t idesc = idesc_e4m3(kTileM, kCols);
             // descriptors of stage 0: a stage and a step of K move the start address (in 16 bytes)
             const uint64_t x_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
             const uint64_t w_desc = smem_desc_sw128(smem_u32(smem) + L::kXBytes, 16, 1024);
@@ -374,39 +369,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true, there = false;
             while (ok && walk.next(seg)) {
                 for (int kc = seg.k0; ok && kc < seg.k1; ++kc, ++n) {
-                    const uint32_t b = n % L::kBufs, taken = (n / L::kBufs - 1) & 1;
+                    const uint32_t b = n % L::kBufs;
                     if (!wait_for(there, &full[s], phase, patience)) {
                         ok = false;
                         break;
                     }
                     const uint64_t dx = x_desc + (uint64_t)(s * (L::kStage >> 4)), dw = w_desc + (uint64_t)(s * (L::kStage >> 4));
-                    uint64_t *bar = &empty[s];
+                    uint64_t *bar = &spent[s];
                     if (++s == L::kStages) {
                         s = 0;
                         phase ^= 1;
                     }
                     there = mbar_test_wait(&full[s], phase);  // its answer comes while the MMAs are issued
+                    if (n >= L::kBufs && !wait_for<true>(false, &taken[b], (n / L::kBufs - 1) & 1, patience)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < L::kParts; ++h) {
-                        uint64_t *mine = &acc_empty[L::kParts * b + h];
-                        if (n >= L::kBufs && !wait_for<true>(false, mine, taken, patience)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = 0; kk < kBK / 32; ++kk)
-                                mma_codes<kPair>(acc0 + b * kCols + h * 128, dx + kk * (32 >> 4),
-                                                 dw + h * (64 * kBK >> 4) + kk * (32 >> 4), idesc, kk > 0);
-                            if (kPair) {
-                                mma_commit_pair(&acc_full[L::kParts * b + h], both);
-                                if (h + 1 == L::kParts) mma_commit_pair(bar, both);
-                            } else {
-                                mma_commit(&acc_full[L::kParts * b + h]);
-                                if (h + 1 == L::kParts) mma_commit(bar);
-                            }
-                        }
+                        for (int kk = 0; kk < kBK / 32; ++kk)
+                            mma_codes<kPair>(acc0 + b * kCols, dx + kk * (32 >> 4), dw + kk * (32 >> 4), idesc, kk > 0);
+                        if (kPair) mma_commit_pair(bar, both);
+                        else mma_commit(bar);
                     }
                 }
             }
@@ -459,12 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSum));
         constexpr int kWide = kCols / 2;  // a warp's columns
         const int q = warp & 3, cw = (warp - kFirstSum) / 4 * kWide;
-        const uint32_t lead_empty = map_to_rank(smem_u32(acc_empty + (L::kParts == 2 ? (warp - kFirstSum) / 4 : 0)), kPair ? leader : cluster_rank());
-        const int part_of_acc = L::kParts == 2 ? (warp - kFirstSum) / 4 : 0;
+        const uint32_t lead_taken = map_to_rank(smem_u32(taken), kPair ? leader : cluster_rank());
         uint8_t *tile_memory = smem + L::kStages * L::kStage;  // slabs of 64 columns, 128 bytes a token
         const uint32_t acc0 = __shfl_sync(~0u, tmem + tmem_lane_base(q) + cw, 0);
         bool ok = true;
-        uint32_t n = 0, done = 0;  // blocks and tiles taken
+        uint32_t b = 0, s = 0, phase = 0, done = 0;  // the next block's accumulator and stage; tiles taken
         for (; walk.next(seg); ++done) {
             const int k0 = seg.k0, k1 = seg.k1;
             const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows, n0 = seg.tile / plan.tiles_m * kCols;
@@ -497,9 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (!ok || kc + j >= k1) continue;
-                    const uint32_t b = n % L::kBufs, parity = (n / L::kBufs) & 1;
-                    uint64_t *ready = acc_full + L::kParts * b + part_of_acc;
-                    ok = wait_for(false, ready, parity, patience);
+                    ok = wait_for(false, &spent[s], phase, patience);
                     // a warp that gave up holds the accumulator: its arrivals, which wait for nothing, would
                     // stand for those of a warp that still reads
                     if (!ok) continue;
@@ -507,8 +489,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (active) add_block<kWide>(sums, acc0 + b * kCols, scale[j]);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_taken(lead_empty + b * (8 * L::kParts));
-                    ++n;
+                    if (lane == 0) arrive_taken(lead_taken + b * 8);
+                    b = (b + 1) % L::kBufs;
+                    if (++s == L::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
             }
             if (!ok) {
@@ -638,7 +624,7 @@ template <int kCols, bool kPair = false>
 cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
     CUtensorMap tm_x, tm_w;
     if (!encode_codes(&tm_x, a.x, a.K, a.M, a.x_stride, p.x_rows) ||
-        !encode_codes(&tm_w, a.w, a.K, a.N, a.K, kPair ? 64 : kCols))
+        !encode_codes(&tm_w, a.w, a.K, a.N, a.K, kPair ? kCols / 2 : kCols))
         return cudaErrorInvalidValue;
     // the output's map is for whole tiles alone, the residual's for a residual: else not read
     CUtensorMap tm_out = tm_x, tm_res = tm_x;
