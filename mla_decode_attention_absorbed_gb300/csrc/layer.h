@@ -104,7 +104,7 @@ struct LinearFp8Args : LinearArgs {
 // How a product of codes is cut (see linear_fp8.cu).
 struct LinearFp8Plan {
     int columns;           // of a tile a CTA accumulates, for 128 tokens
-    int tiles_m, tiles_n;  // tile t: tokens t % tiles_m, columns t / tiles_m
+    int tiles_m, tiles_n;  // of tokens, of columns
     int nk;                // blocks of K
     int grid;
     int whole;             // tiles that a CTA (or pair) takes whole, one after another; of the others,

@@ -19,7 +19,7 @@
 // Warps: 0 issues the loads, 1 the MMAs, 2 moves residuals in and outputs out, 4-11 hold the sums.
 //
 // Measured (device time): 4096 x 16384 x 7168 in 320 to 330 us for a dozen calls = 2,900 to 3,000 TFLOP/s, 1.5
-// times the measured bf16 rate (380 us = 2,530 in a long run of them, at the power limit): a block of a pair's
+// times the measured bf16 rate (372 us = 2,590 in a long run of them, at the power limit): a block of a pair's
 // tile takes 800 cycles where its MMAs alone take 560.  Copies of the kernel without one part or another: MMAs alone 226 us,
 // loads alone 203, sums alone 270, loads and MMAs 269 (what comes in and what the MMAs read share the shared memory's
 // ports), MMAs and sums 295, handshakes alone 166.  64 x 16384 x 7168 in 27.4 us: 117 MB of weights at 6.1 TB/s in 19 us,
@@ -219,9 +219,12 @@ __device__ __forceinline__ bool wait_beyond(uint64_t *bar, uint32_t parity, uint
 // A CTA's work (a pair's, "unit"): whole tiles, then, for a cluster's units together, a share of one
 // tile's K.
 struct Segment {
-    int tile, k0, k1;
+    int m, n, k0, k1;  // m, n: the tile's place
     bool cut;
 };
+// The tiles go column by column through a band of this many tiles of tokens: the band's x stays in L2 while
+// W passes.  4096 x 16384 x 7168 in a long run of calls 372 to 375 us, through all 16 tiles of tokens 380, through bands of 4 383.
+constexpr int kBand = 8;
 struct Walk {
     const Plan &p;
     int unit, units, tile, part;
@@ -234,14 +237,21 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(Segment &s) {
         if (tile < p.whole) {
-            s = Segment{tile, 0, p.nk, false};
+            s = Segment{0, 0, 0, p.nk, false};
+            place(s, tile);
             tile += units;
             return true;
         }
         if (!split || tile == INT_MAX) return false;
-        s = Segment{p.whole + unit / p.cluster, p.nk * part / p.cluster, p.nk * (part + 1) / p.cluster, true};
+        s = Segment{0, 0, p.nk * part / p.cluster, p.nk * (part + 1) / p.cluster, true};
+        place(s, p.whole + unit / p.cluster);
         tile = INT_MAX;
         return true;
+    }
+    __device__ __forceinline__ void place(Segment &s, int t) {
+        const int m0 = t / (kBand * p.tiles_n) * kBand, r = t - m0 * p.tiles_n, high = min(kBand, p.tiles_m - m0);
+        s.m = m0 + r % high;
+        s.n = r / high;
     }
 };
 
@@ -311,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s = 0, phase = 1;
             bool ok = true, free = mbar_test_wait(&spent[0], 1);
             while (ok && walk.next(seg)) {
-                const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows;
-                const int n0 = seg.tile / plan.tiles_m * kCols + half * (kCols / 2);
+                const int t0 = seg.m * kTileM + half * kRows;
+                const int n0 = seg.n * kCols + half * (kCols / 2);
                 for (int kc = seg.k0; kc < seg.k1; ++kc) {
                     // the first round's waits are for the phase before the barriers' first: over at once
                     if (!wait_for(free, &spent[s], phase, patience)) {
@@ -409,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             uint32_t i = 0;
             for (; ok && walk.next(seg); ++i) {
-                const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows;
-                int n0 = seg.tile / plan.tiles_m * kCols, used = kCols / 64;
+                const int t0 = seg.m * kTileM + half * kRows;
+                int n0 = seg.n * kCols, used = kCols / 64;
                 if (seg.cut) {
                     const int share = kCols / plan.cluster;
                     n0 += walk.part * share / 64 * 64;
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t b = 0, s = 0, phase = 0, done = 0;  // the next block's accumulator and stage; tiles taken
         for (; walk.next(seg); ++done) {
             const int k0 = seg.k0, k1 = seg.k1;
-            const int t0 = seg.tile % plan.tiles_m * kTileM + half * kRows, n0 = seg.tile / plan.tiles_m * kCols;
+            const int t0 = seg.m * kTileM + half * kRows, n0 = seg.n * kCols;
             const int nt = min(kRows, a.M - t0);
             const bool active = q * 32 < nt && n0 + cw < a.N;
             float sums[kWide];
@@ -663,15 +673,15 @@ cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
 // The plan with the shortest estimate, in SM cycles.  What the parts were measured to take (timings of
 // every form and cluster at 30 sizes, clock traces at four of them):
 //   a block of a tile   450 cycles at 128 x 64, 560 at 128 x 128, 510 at 256 x 128 on a pair and 860 at
-//                       256 x 256 on a pair (the MMAs alone: 512); all of them together at least what it
-//                       takes the card to bring the weights, at 3500 bytes a cycle
+//                       256 x 256 on a pair (of a long K 380, 480, 490 and 770, much the same in proportion); all
+//                       of them together at least what it takes the card to bring the weights, at 3500 bytes a cycle
 //   a tile's epilogue   1500 cycles and 10 a column
 //   a shared tile       4000 cycles of barriers, the sums sent at 12 bytes a cycle, and the finish
-// E.g. 64 x 16384 x 7168: 27.9 us in clusters of 2, 35.5 in whole tiles of 64 columns, 40 of 128; 256 x
-// 7168 x 24576: 54 us whole and shared, 58 whole; 1024 x 7168 x 7168: 51.5 us in pairs' tiles of 128
-// columns, 61.5 of 256; 4096 x 16384 x 7168: 334 us in pairs' tiles of 256 columns, 439 of 128, 464 on
-// single CTAs; 64 x 7168 x 576: 7.1 us in clusters of 8, 18 in whole tiles.  Over 30 sizes from 1 x 7168 x
-// 576 up the choice was within 12 % of the best form timed, within 5 % for all but three.
+// E.g. 64 x 16384 x 7168: 27.3 us in clusters of 2, 31 in whole tiles of 64 columns, 36 of 128; 256 x
+// 7168 x 24576: 54 us whole and shared, 58 whole; 1024 x 7168 x 7168: 51.2 us in pairs' tiles of 128
+// columns, 53.6 of 256; 4096 x 16384 x 7168: 321 us in pairs' tiles of 256 columns, 409 of 128, 399 on
+// single CTAs; 64 x 7168 x 576: 6.9 us in clusters of 8, 15 in whole tiles.  Over 23 sizes from 1 x 7168 x
+// 576 up the choice was within 7 % of the best form timed, within 3 % for all but two.
 LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
     Plan best{};
     double best_cost = 0.0;

@@ -270,6 +270,13 @@ def test_linear_fp8_every_form(form):
     check_product(M, K, N, True, "silu", True, 0, 0, 0, False, 2)
 
 
+@pytest.mark.parametrize("M", [1025, 2305, 4360])
+def test_linear_fp8_many_tiles_of_tokens(M):
+    """More tiles of tokens than go through the columns together, and a rest of them."""
+    check_product(M, 144, 1160, True, "none", True, 16, 8, 8, True, 3)
+    check_product(M, 272, 520, False, "none", False, 0, 0, 0, False, 4)
+
+
 def test_linear_fp8_of_what_quantize_gives():
     """The two calls one after the other, with nothing between them, against the product of the codes read back."""
     g = gen(5)
