@@ -110,7 +110,7 @@ struct LinearFp8Plan {
     int whole;             // tiles that a CTA (or pair) takes whole, one after another; of the others,
     int cluster;           // the CTAs (or pairs) of a cluster share one's K (1: there are none)
     int x_rows;            // of a copy of x: as many as there are, up to 128
-    bool pair;             // a tile is 256 tokens x 256 columns, taken by a pair of CTAs
+    bool pair;             // a tile is 256 tokens high, taken by a pair of CTAs
 };
 LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms);
 cudaError_t launch_linear_fp8(const LinearFp8Args &a, const LinearFp8Plan &p, cudaStream_t st);

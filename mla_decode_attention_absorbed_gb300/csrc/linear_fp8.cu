@@ -7,9 +7,9 @@
 // accumulators in tensor memory, and while the MMAs fill the other one, eight warps take it from
 // there, times its scale, into the tile's fp32 sums, which stay in their registers.  The MMA's rows
 // are the tokens and its columns those of the output: a lane then has one token, a warp's columns lie
-// in one block of W, and a value costs half an instruction (two fp32 multiply-adds each).
+// in one block of W (of a tile of 192 in one or two), and a value costs half an instruction (two fp32 multiply-adds each).
 //
-// A tile is 128 tokens x 64 or 128 columns on one CTA, or 256 x 128 or 256 on a pair of CTAs, each of
+// A tile is 128 tokens x 64 or 128 columns on one CTA, or 256 x 192 or 256 on a pair of CTAs, each of
 // which loads half of both operands and holds the sums of its 128 tokens.  K runs in blocks of 128
 // through a ring of TMA stages.  The CTAs take whole tiles one after another; of a tile that is left (or of
 // all, where there are few) the 2, 4 or 8 CTAs or pairs of a cluster take equal parts of K, exchange their
@@ -19,11 +19,11 @@
 // Warps: 0 issues the loads, 1 the MMAs, 2 moves residuals in and outputs out, 4-11 hold the sums.
 //
 // Measured (device time): 4096 x 16384 x 7168 in 320 to 330 us for a dozen calls = 2,900 to 3,000 TFLOP/s, 1.5
-// times the measured bf16 rate (372 us = 2,590 in a long run of them, at the power limit): a block of a pair's
+// times the measured bf16 rate (370 us = 2,600 in a long run of them, at the power limit): a block of a pair's
 // tile takes 800 cycles where its MMAs alone take 560.  Copies of the kernel without one part or another: MMAs alone 226 us,
 // loads alone 203, sums alone 270, loads and MMAs 269 (what comes in and what the MMAs read share the shared memory's
 // ports), MMAs and sums 295, handshakes alone 166.  64 x 16384 x 7168 in 27.4 us: 117 MB of weights at 6.1 TB/s in 19 us,
-// 2.7 of start and 4 of exchange and finish.  256 x 7168 x 24576 in 54 us, 333 x 1008 x 1544 in 6.4, a chain of latencies.
+// 2.7 of start and 4 of exchange and finish.  256 x 7168 x 24576 in 51 us, 333 x 1008 x 1544 in 6.4, a chain of latencies.
 //
 // What measured slower: arrivals across the pair that order memory (875 us when this took 488), clocks read
 // before each wait, an epilogue turned over through shared memory (8 us a tile: 468), the scales' addresses
@@ -68,6 +68,8 @@ struct Smem {
     static constexpr int kStages = (227 * 1024 - 2048 - kTile) / kStage;
     static constexpr int kBytes = kStages * kStage + kTile + 1024 /* barriers */ + 1024 /* alignment */;
     static constexpr int kBufs = 512 / kCols;  // accumulators: a block of K each
+    static constexpr int kWide = kCols / 2;    // columns of a warp's sums
+    static constexpr bool kTwo = kBK % kWide != 0;  // which may lie in two blocks of W
     static_assert(kRows * kCols * 4 <= kStages * kStage, "a cluster's sums are exchanged in the ring");
     static_assert(kStages >= kBufs, "a stage's barrier tells the sums' warps, too, see the MMA warp");
     static_assert(kBytes <= 232448, "shared memory over the per-CTA limit");
@@ -107,13 +109,14 @@ __device__ __forceinline__ void fma2(float &a, float &b, uint32_t x, uint32_t y,
     asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %4};\n\tfma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}" : "+f"(a), "+f"(b) : "r"(x), "r"(y), "f"(s));
 }
 // sums += scale * the kWide columns of tensor memory at taddr; the next 16 are on their way
-// while 16 are added.
+// while 16 are added.  Columns from `before` on, a multiple of 32, are in the next block of W: scale2.
 template <int kWide>
-__device__ __forceinline__ void add_block(float (&sums)[kWide], uint32_t taddr, float scale) {
+__device__ __forceinline__ void add_block(float (&sums)[kWide], uint32_t taddr, float scale1, float scale2, int before) {
     uint32_t r0[16], r1[16];
     tmem_ld16(taddr, r0);
 #pragma unroll
     for (int c = 0; c < kWide; c += 32) {
+        const float scale = c < before ? scale1 : scale2;
         tmem_ld_wait16(r0);
         tmem_ld16(taddr + c + 16, r1);
 #pragma unroll
@@ -422,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t0 = seg.m * kTileM + half * kRows;
                 int n0 = seg.n * kCols, used = kCols / 64;
                 if (seg.cut) {
-                    const int share = kCols / plan.cluster;
-                    n0 += walk.part * share / 64 * 64;
-                    used = share > 64 ? share / 64 : 1;
+                    const int share = kCols / plan.cluster, first = walk.part * share / 64;
+                    n0 += first * 64;
+                    used = (walk.part * share + share - 1) / 64 - first + 1;
                 }
                 used = t0 < a.M && n0 < a.N ? min(used, (a.N - n0 + 63) / 64) : 0;
                 if (lane == 0) {
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSum));
-        constexpr int kWide = kCols / 2;  // a warp's columns
+        constexpr int kWide = L::kWide;
         const int q = warp & 3, cw = (warp - kFirstSum) / 4 * kWide;
         const uint32_t lead_taken = map_to_rank(smem_u32(taken), kPair ? leader : cluster_rank());
         uint8_t *tile_memory = smem + L::kStages * L::kStage;  // slabs of 64 columns, 128 bytes a token
@@ -469,14 +472,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < kWide; ++e) sums[e] = 0.f;
             // the blocks' scales come four at a time, while the four before are at work
             const float *sx = a.x_scale + k0 * a.x_scale_stride + min(t0 + q * 32 + lane, a.M - 1);
-            const float *sw = a.w_scale + (long long)(min(n0 + cw, a.N - 1) / kBK) * plan.nk + k0;
-            float nx[4], nw[4];
+            const int row = min(n0 + cw, a.N - 1) / kBK, before = L::kTwo ? kBK - (n0 + cw) % kBK : kWide;
+            const float *sw = a.w_scale + (long long)row * plan.nk + k0;
+            const int next = L::kTwo ? (min(n0 + cw + kWide, a.N) - 1) / kBK > row ? plan.nk : 0 : 0;
+            float nx[4], nw[4], nw2[4];
             auto load_scales = [&](int left) {  // the next `left` blocks', at most 4
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j < left) {
                         nx[j] = __ldg(sx);
                         nw[j] = __ldg(sw + j);
+                        if (L::kTwo) nw2[j] = __ldg(sw + next + j);
                         sx += a.x_scale_stride;
                     }
                 sw += 4;
@@ -484,9 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_scales(k1 - k0);
 #pragma unroll 1
             for (int kc = k0; ok && kc < k1; kc += 4) {
-                float scale[4];
+                float scale[4], scale2[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) scale[e] = nx[e] * nw[e];
+                for (int e = 0; e < 4; ++e) {
+                    scale[e] = nx[e] * nw[e];
+                    scale2[e] = L::kTwo ? nx[e] * nw2[e] : scale[e];
+                }
                 load_scales(k1 - kc - 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -496,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // stand for those of a warp that still reads
                     if (!ok) continue;
                     tc_fence_after();
-                    if (active) add_block<kWide>(sums, acc0 + b * kCols, scale[j]);
+                    if (active) add_block<kWide>(sums, acc0 + b * kCols, scale[j], scale2[j], before);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_taken(lead_taken + b * 8);
@@ -536,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
                 // have, takes the parts of the columns this CTA finishes, one slot a rank.
-                const int share = kCols / plan.cluster, part = walk.part;  // share: a power of two, 8 or more
+                const int share = kCols / plan.cluster, part = walk.part;  // share: a multiple of 8
                 cluster_sync();
                 if (kPair && *gave_up) cluster_sync();  // the load warps settle it before this
                 // four columns of the tokens lie together, so that a warp writes and reads 512 bytes at a time
@@ -670,27 +679,26 @@ cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
 
 }  // namespace
 
-// The plan with the shortest estimate, in SM cycles.  What the parts were measured to take (timings of
-// every form and cluster at 30 sizes, clock traces at four of them):
-//   a block of a tile   450 cycles at 128 x 64, 560 at 128 x 128, 510 at 256 x 128 on a pair and 860 at
-//                       256 x 256 on a pair (of a long K 380, 480, 490 and 770, much the same in proportion); all
-//                       of them together at least what it takes the card to bring the weights, at 3500 bytes a cycle
-//   a tile's epilogue   1500 cycles and 10 a column
-//   a shared tile       4000 cycles of barriers, the sums sent at 12 bytes a cycle, and the finish
-// E.g. 64 x 16384 x 7168: 27.3 us in clusters of 2, 31 in whole tiles of 64 columns, 36 of 128; 256 x
-// 7168 x 24576: 54 us whole and shared, 58 whole; 1024 x 7168 x 7168: 51.2 us in pairs' tiles of 128
-// columns, 53.6 of 256; 4096 x 16384 x 7168: 321 us in pairs' tiles of 256 columns, 409 of 128, 399 on
-// single CTAs; 64 x 7168 x 576: 6.9 us in clusters of 8, 15 in whole tiles.  Over 23 sizes from 1 x 7168 x
-// 576 up the choice was within 7 % of the best form timed, within 3 % for all but two.
+// The plan with the shortest estimate, in SM cycles.  The parts' costs were fitted to timings of every form and
+// cluster at 168 sizes (1 to 4096 tokens, K from 64 to 19000, 32 to 25000 columns): a block of a tile, a tile's
+// epilogue, and of a shared tile the barriers, the sums sent and the finish.  (Of a long K a block takes 380, 480, 690
+// and 770 cycles.)  The choice is within 0.7 % of the best form timed on average, within 7 % for all but four, and
+// 13 % at most.  Both sides of it, the best of each:
+//   64 x 16384 x 7168   27.3 us in clusters of 2, 31 in whole tiles of 64 columns, 36 of 128
+//   64 x 7168 x 576     6.9 us in clusters of 8, 15 in whole tiles
+//   256 x 7168 x 24576  51 us in pairs' tiles of 192 columns, 54 of 256, the last of them shared, 53 on single CTAs
+//   512 x 7168 x 7168   28 us in pairs' tiles of 192 columns, 30 of 256, 32 on single CTAs
+//   4096 x 16384 x 7168 321 us in pairs' tiles of 256 columns, 380 of 192, 399 on single CTAs
+//   373 x 1792 x 4856   9.7 us on single CTAs, 13 in pairs' tiles of 192 columns
+// Pairs' tiles of 128 columns were 9 % better than the best of these at one of 75 sizes, elsewhere 2 % at most.
 LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
     Plan best{};
     double best_cost = 0.0;
-    const double weights = 1.0 * K * N / 3500.0;  // however they are dealt out
     const int nk = (K + kBK - 1) / kBK;
     for (int form = 0; form < 4; ++form) {
         Plan p;
         p.pair = form >= 2;
-        p.columns = form == 0 ? 64 : form == 2 ? 256 : 128;
+        p.columns = 64 * (form + 1);
         const int tile_m = p.pair ? 2 * kRows : kRows;
         if (p.pair && M <= kRows) break;
         // of a shorter x no more than it has, in whole groups of 8; the rest of a tile's rows is then whatever
@@ -702,7 +710,7 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
         p.nk = nk;
         const long long tiles = (long long)p.tiles_m * p.tiles_n;
         if (tiles > (1ll << 28)) continue;
-        const double block = form == 0 ? 450.0 : form == 1 ? 560.0 : form == 2 ? 860.0 : 510.0, epilogue = 1500.0 + 10.0 * p.columns;
+        const double block = form == 0 ? 430.0 : form == 1 ? 600.0 : form == 2 ? 740.0 : 860.0, epilogue = 1500.0 + 14.0 * p.columns;
         const int rows = M < kRows ? M : kRows;
         for (p.cluster = 1; p.cluster <= (p.pair ? 4 : 8); p.cluster *= 2) {
             const int ctas = p.pair ? 2 * p.cluster : p.cluster;
@@ -723,9 +731,8 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
                 p.grid = (p.whole > 0 ? fit : (int)tiles) * ctas;
                 const double sent = (double)rows * p.columns * 4 * (p.cluster - 1) / p.cluster;
                 cost = (double)(p.whole / a_round) * (nk * block + epilogue) + (nk + p.cluster - 1) / p.cluster * block +
-                       4000.0 + sent / 12.0 + 40.0 * rows * p.columns / p.cluster / 256.0;
+                       6500.0 + sent / 9.0 + 60.0 * rows * p.columns / p.cluster / 256.0;
             }
-            if (cost < weights) cost = weights + cost * 1e-3;
             if (best.grid == 0 || cost < best_cost) {
                 best = p;
                 best_cost = cost;
@@ -736,7 +743,7 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
 }
 
 cudaError_t launch_linear_fp8(const LinearFp8Args &a, const LinearFp8Plan &p, cudaStream_t st) {
-    if (p.pair) return p.columns == 256 ? launch<256, true>(a, p, st) : launch<128, true>(a, p, st);
+    if (p.pair) return p.columns == 256 ? launch<256, true>(a, p, st) : launch<192, true>(a, p, st);
     return p.columns == 128 ? launch<128>(a, p, st) : launch<64>(a, p, st);
 }
 

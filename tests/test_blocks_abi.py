@@ -102,7 +102,7 @@ def test_linear_fp8_cuts_hold_over_the_range(lib):
             for N in (8, 72, 136, 7168, 1 << 20):
                 c = mla.linear_fp8_cut(M, K, N)
                 pair = c.tile_rows == 256
-                assert (c.tile_rows, c.tile_columns) in ((128, 64), (128, 128), (256, 128), (256, 256)) and c.runs == 0
+                assert (c.tile_rows, c.tile_columns) in ((128, 64), (128, 128), (256, 192), (256, 256)) and c.runs == 0
                 assert M > 128 or not pair
                 assert 1 <= c.k_parts <= (4 if pair else 8) and -(-K // 128) >= (2 * c.k_parts if c.k_parts > 1 else 1)
                 units, tiles = c.ctas // (2 if pair else 1), -(-M // c.tile_rows) * -(-N // c.tile_columns)

@@ -380,6 +380,7 @@ TIMEOUT_CASES = [
     # M, K, N: whole tiles, clusters, pairs in several rounds, whole tiles and a shared one, clusters of pairs
     (333, 1008, 1544), (64, 16384, 1024), (3, 65536, 136), (8, 4112, 20480), (5000, 1040, 6000), (250, 8208, 7000),
     (529, 2928, 8232), (171, 9664, 3088), (1039, 4544, 4904), (397, 18272, 1352), (166, 2912, 20104), (153, 3872, 1448),
+    (262, 10896, 3768), (130, 11632, 23432), (993, 11760, 608), (140, 7536, 5032), (145, 4304, 20296), (135, 8144, 2472),
 ]
 
 
