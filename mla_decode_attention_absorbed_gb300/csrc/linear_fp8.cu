@@ -53,7 +53,7 @@ constexpr int kRegSum = 216, kRegOther = 72;
 static_assert(2 * kRegSum + kRegOther == 3 * 168, "the split must equal the launch's total");
 
 template <int kValue>
-struct Act {
+struct Value {
     static constexpr int value = kValue;
 };
 
@@ -155,6 +155,9 @@ __device__ __forceinline__ void finish_columns(const LinearArgs &a, const float 
     }
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(m)),
@@ -531,11 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             finish_columns<decltype(act)::value>(a, sums + c, row, column % 64 / 8, lane & 7, n0 + column);
                         };
                         switch (a.act) {
-                            case MLA_ACT_RELU: finish(Act<MLA_ACT_RELU>()); break;
-                            case MLA_ACT_SILU: finish(Act<MLA_ACT_SILU>()); break;
-                            case MLA_ACT_GELU: finish(Act<MLA_ACT_GELU>()); break;
-                            case MLA_ACT_GELU_TANH: finish(Act<MLA_ACT_GELU_TANH>()); break;
-                            default: finish(Act<MLA_ACT_NONE>()); break;
+                            case MLA_ACT_RELU: finish(Value<MLA_ACT_RELU>()); break;
+                            case MLA_ACT_SILU: finish(Value<MLA_ACT_SILU>()); break;
+                            case MLA_ACT_GELU: finish(Value<MLA_ACT_GELU>()); break;
+                            case MLA_ACT_GELU_TANH: finish(Value<MLA_ACT_GELU_TANH>()); break;
+                            default: finish(Value<MLA_ACT_NONE>()); break;
                         }
                     }
                 }
@@ -545,53 +548,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // Every CTA of the cluster holds its part of the tile.  The ring, idle once all of them
                 // have, takes the parts of the columns this CTA finishes, one slot a rank.
-                const int share = kCols / plan.cluster, part = walk.part;  // share: a multiple of 8
-                cluster_sync();
-                if (kPair && *gave_up) cluster_sync();  // the load warps settle it before this
-                // four columns of the tokens lie together, so that a warp writes and reads 512 bytes at a time
-                if (q * 32 < nt) {
-                    const uint32_t mine = smem_u32(smem) + (uint32_t)(part * (share / 4) * kRows + q * 32 + lane) * 16;
+                // parts: the cluster's, where it is known to the compiler, that does without thirty divisions then (64 x
+                // 16384 x 7168 27.5 us, so 26.3; 2 x 1936 x 2352 6.9, so 5.9).  A pair's kernel that holds the code for 2 and
+                // for 4 is 5 % slower at whole tiles.
+                const int part = walk.part;
+                auto exchange = [&](auto known) {
+                    const int parts = decltype(known)::value ? decltype(known)::value : plan.cluster, share = kCols / parts;  // a multiple of 8
+                    cluster_sync();
+                    if (kPair && *gave_up) cluster_sync();  // the load warps settle it before this
+                    // four columns of the tokens lie together, so that a warp writes and reads 512 bytes at a time
+                    if (q * 32 + lane < nt) {
+                        const uint32_t mine = smem_u32(smem) + (uint32_t)(part * (share / 4) * kRows + q * 32 + lane) * 16;
 #pragma unroll
-                    for (int e = 0; e < kWide / 4; ++e) {
-                        const int c = cw + 4 * e, to = c / share;
-                        st_cluster_v4(map_to_rank(mine + (uint32_t)(c / 4 % (share / 4)) * (kRows * 16), kPair ? 2 * to + half : to),
-                                      sums[4 * e], sums[4 * e + 1], sums[4 * e + 2], sums[4 * e + 3]);
+                        for (int e = 0; e < kWide / 4; ++e) {
+                            const int c = cw + 4 * e, to = c / share;
+                            const uint32_t at = mine + (uint32_t)(c % share / 4) * (kRows * 16);
+                            if (to == part) st_shared_v4(at, sums[4 * e], sums[4 * e + 1], sums[4 * e + 2], sums[4 * e + 3]);
+                            else st_cluster_v4(map_to_rank(at, kPair ? 2 * to + half : to), sums[4 * e], sums[4 * e + 1], sums[4 * e + 2], sums[4 * e + 3]);
+                        }
                     }
-                }
-                __syncwarp();
-                if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
-                cluster_sync();
-                // 32 tokens x 8 columns at a time, dealt out to the warps
-                const int runs = (nt + 31) / 32;
+                    __syncwarp();
+                    if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
+                    cluster_sync();
+                    // 32 tokens x 8 columns at a time, dealt out to the warps
+                    const int runs = (nt + 31) / 32;
 #pragma unroll 1
-                for (int i = warp - kFirstSum; i < runs * (share / 8); i += kSumWarps) {
-                    const int g = i / runs, token = (i - g * runs) * 32 + lane;
-                    if (token >= nt) continue;
-                    const float4 *from = reinterpret_cast<const float4 *>(smem) + token;
-                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8];
-                    for (int r = 0; r < plan.cluster; ++r) {
-                        const float4 lo = from[(r * (share / 4) + 2 * g) * kRows], hi = from[(r * (share / 4) + 2 * g + 1) * kRows];
-                        y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
-                        y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
-                    }
-                    const int at = part * share + 8 * g, n = n0 + at;  // in the tile, in the output
-                    if (n >= a.N) continue;
-                    if (a.bias) {
-                        Finish::unpack8(__ldg(reinterpret_cast<const uint4 *>(a.bias + n)), f);
+                    for (int i = warp - kFirstSum; i < runs * (share / 8); i += kSumWarps) {
+                        const int g = i / runs, token = (i - g * runs) * 32 + lane;
+                        const int at = part * share + 8 * g, n = n0 + at;  // in the tile, in the output
+                        if (token >= nt || n >= a.N) continue;
+                        const float4 *from = reinterpret_cast<const float4 *>(smem) + 2 * g * kRows + token;
+                        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] += f[e];
-                    }
-                    activate(a.act, y);
-                    if (a.residual) {
-                        const int in_slabs = at - part * share / 64 * 64, chunk = in_slabs % 64 / 8;
-                        Finish::unpack8(*reinterpret_cast<const uint4 *>(tile_memory + (in_slabs / 64 * kRows + token) * 128 +
-                                                                         ((chunk ^ (token & 7)) << 4)), f);
+                        for (int r = 0; r < parts; ++r) {
+                            const float4 lo = from[r * (share / 4) * kRows], hi = from[(r * (share / 4) + 1) * kRows];
+                            y[0] += lo.x; y[1] += lo.y; y[2] += lo.z; y[3] += lo.w;
+                            y[4] += hi.x; y[5] += hi.y; y[6] += hi.z; y[7] += hi.w;
+                        }
+                        if (a.bias) {
+                            Finish::unpack8(__ldg(reinterpret_cast<const uint4 *>(a.bias + n)), f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] += f[e];
+                            for (int e = 0; e < 8; ++e) y[e] += f[e];
+                        }
+                        activate(a.act, y);
+                        if (a.residual) {
+                            const int in_slabs = at - part * share / 64 * 64, chunk = in_slabs % 64 / 8;
+                            Finish::unpack8(*reinterpret_cast<const uint4 *>(tile_memory + (in_slabs / 64 * kRows + token) * 128 +
+                                                                             ((chunk ^ (token & 7)) << 4)), f);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] += f[e];
+                        }
+                        *reinterpret_cast<uint4 *>(a.out + (long long)(t0 + token) * a.out_stride + n) = make_uint4(
+                            pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
                     }
-                    *reinterpret_cast<uint4 *>(a.out + (long long)(t0 + token) * a.out_stride + n) = make_uint4(
-                        pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-                }
+                };
+                if (kPair) exchange(Value<0>());
+                else if (plan.cluster == 2) exchange(Value<2>());
+                else if (plan.cluster == 4) exchange(Value<4>());
+                else exchange(Value<8>());
             }
         }
     }
