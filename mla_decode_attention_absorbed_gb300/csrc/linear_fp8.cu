@@ -22,8 +22,8 @@
 // times the measured bf16 rate (370 us = 2,600 in a long run of them, at the power limit): a block of a pair's
 // tile takes 800 cycles where its MMAs alone take 560.  Copies of the kernel without one part or another: MMAs alone 226 us,
 // loads alone 203, sums alone 270, loads and MMAs 269 (what comes in and what the MMAs read share the shared memory's
-// ports), MMAs and sums 295, handshakes alone 166.  64 x 16384 x 7168 in 27.4 us: 117 MB of weights at 6.1 TB/s in 19 us,
-// 2.7 of start and 4 of exchange and finish.  256 x 7168 x 24576 in 51 us, 333 x 1008 x 1544 in 6.4, a chain of latencies.
+// ports), MMAs and sums 295, handshakes alone 166.  64 x 16384 x 7168 in 26.3 us: 117 MB of weights at 6.1 TB/s in 19 us,
+// 2.7 of start and 4 of the wait for the other CTA, exchange and finish.  256 x 7168 x 24576 in 51 us, 333 x 1008 x 1544 in 6.4, a chain of latencies.
 //
 // What measured slower: arrivals across the pair that order memory (875 us when this took 488), clocks read
 // before each wait, an epilogue turned over through shared memory (8 us a tile: 468), the scales' addresses
@@ -696,10 +696,10 @@ cudaError_t launch(const LinearFp8Args &a, const Plan &p, cudaStream_t st) {
 // The plan with the shortest estimate, in SM cycles.  The parts' costs were fitted to timings of every form and
 // cluster at 168 sizes (1 to 4096 tokens, K from 64 to 19000, 32 to 25000 columns): a block of a tile, a tile's
 // epilogue, and of a shared tile the barriers, the sums sent and the finish.  (Of a long K a block takes 380, 480, 690
-// and 770 cycles.)  The choice is within 0.7 % of the best form timed on average, within 7 % for all but four, and
-// 13 % at most.  Both sides of it, the best of each:
-//   64 x 16384 x 7168   27.3 us in clusters of 2, 31 in whole tiles of 64 columns, 36 of 128
-//   64 x 7168 x 576     6.9 us in clusters of 8, 15 in whole tiles
+// and 770 cycles.)  The choice is within 0.6 % of the best form timed on average, within 5 % for all but six, and
+// 12 % at most.  Both sides of it, the best of each:
+//   64 x 16384 x 7168   26.3 us in clusters of 2, 31 in whole tiles of 64 columns, 36 of 128
+//   64 x 7168 x 576     6.3 us in clusters of 8, 15 in whole tiles
 //   256 x 7168 x 24576  51 us in pairs' tiles of 192 columns, 54 of 256, the last of them shared, 53 on single CTAs
 //   512 x 7168 x 7168   28 us in pairs' tiles of 192 columns, 30 of 256, 32 on single CTAs
 //   4096 x 16384 x 7168 321 us in pairs' tiles of 256 columns, 380 of 192, 399 on single CTAs
@@ -724,7 +724,7 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
         p.nk = nk;
         const long long tiles = (long long)p.tiles_m * p.tiles_n;
         if (tiles > (1ll << 28)) continue;
-        const double block = form == 0 ? 430.0 : form == 1 ? 600.0 : form == 2 ? 740.0 : 860.0, epilogue = 1500.0 + 14.0 * p.columns;
+        const double block = form == 0 ? 430.0 : form == 1 ? 560.0 : form == 2 ? 720.0 : 870.0, epilogue = 1500.0 + 14.0 * p.columns;
         const int rows = M < kRows ? M : kRows;
         for (p.cluster = 1; p.cluster <= (p.pair ? 4 : 8); p.cluster *= 2) {
             const int ctas = p.pair ? 2 * p.cluster : p.cluster;
@@ -745,7 +745,7 @@ LinearFp8Plan linear_fp8_plan(int M, int K, int N, int sms) {
                 p.grid = (p.whole > 0 ? fit : (int)tiles) * ctas;
                 const double sent = (double)rows * p.columns * 4 * (p.cluster - 1) / p.cluster;
                 cost = (double)(p.whole / a_round) * (nk * block + epilogue) + (nk + p.cluster - 1) / p.cluster * block +
-                       6500.0 + sent / 9.0 + 60.0 * rows * p.columns / p.cluster / 256.0;
+                       2000.0 + sent / 9.0 + 60.0 * rows * p.columns / p.cluster / 256.0;
             }
             if (best.grid == 0 || cost < best_cost) {
                 best = p;

@@ -121,13 +121,13 @@ LINEAR_FORMS = {
 # The same of mla_linear_fp8, (rows a tile, columns a tile, parts of K, rounds of whole tiles: 0, 1 or 2 for more) to (M, K, N).
 LINEAR_FP8_FORMS = {
     (128, 64, 1, 1): (3, 208, 136), (128, 64, 2, 0): (2, 2512, 4704), (128, 64, 4, 0): (5, 1728, 72),
-    (128, 64, 4, 1): (2, 12480, 9952), (128, 64, 8, 0): (9, 2192, 136), (128, 128, 1, 1): (3, 208, 10328),
+    (128, 64, 4, 1): (2, 12480, 9952), (128, 64, 8, 0): (121, 1968, 136), (128, 128, 1, 1): (3, 208, 10328),
     (128, 128, 1, 2): (3, 208, 20552), (128, 128, 2, 0): (2, 4272, 4904), (128, 128, 2, 1): (3, 1520, 23480),
     (128, 128, 4, 0): (2, 1936, 2352), (128, 128, 4, 1): (2, 912, 20568), (128, 128, 8, 0): (2, 2016, 968),
     (256, 192, 1, 1): (135, 208, 10840), (256, 192, 1, 2): (1039, 4544, 4904), (256, 192, 2, 0): (140, 7536, 5032),
     (256, 192, 2, 1): (145, 4304, 20296), (256, 192, 4, 0): (135, 8144, 2472),
     (256, 256, 1, 1): (137, 208, 16408), (256, 256, 1, 2): (515, 208, 12760), (256, 256, 2, 0): (262, 10896, 3768),
-    (256, 256, 2, 1): (5799, 4432, 1784), (256, 256, 4, 0): (993, 11760, 608),
+    (256, 256, 2, 1): (5799, 4432, 1784), (256, 256, 4, 0): (397, 18272, 1352),
 }
 
 
