@@ -766,11 +766,16 @@ def latent_row_bytes(prob: Problem) -> int:
     return int(n)
 
 
-def _codes(t, what: str, dev: int, M: int, K: int) -> int:
-    """Address of t, E4M3 codes [M, K] with contiguous rows (any stride between them)."""
-    if t.dtype != _E4M3 or t.get_device() != dev or t.shape != (M, K) or (K > 1 and t.stride(1) != 1):
-        _refuse(t, what, f"a torch.float8_e4m3fn tensor [{M}, {K}] with contiguous rows on device {dev}")
-    return t.data_ptr()
+def _matrix(t, what: str, dtype, dev: int, M: int, N: int):
+    """Address of t, a matrix of this type with contiguous rows, and the elements between them (any; a single
+    row has none of its own)."""
+    if t.dtype != dtype or t.get_device() != dev or t.shape != (M, N):
+        _refuse(t, what, f"a {dtype} tensor [{M}, {N}] with contiguous rows on device {dev}")
+    if t.is_contiguous():
+        return t.data_ptr(), N
+    if N > 1 and t.stride(1) != 1:
+        _refuse(t, what, f"a {dtype} tensor [{M}, {N}] with contiguous rows on device {dev}")
+    return t.data_ptr(), t.stride(0)
 
 
 def quantize(x, norm_weight=None, eps: float = 1e-6, block_rows: int = 1, codes=None, scales=None, stream=None):
@@ -782,7 +787,7 @@ def quantize(x, norm_weight=None, eps: float = 1e-6, block_rows: int = 1, codes=
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    rows = _rows(x, "x", dev, M, K)
+    rows, x_stride = _matrix(x, "x", _BF16, dev, M, K)
     weight = None if norm_weight is None else _dense(norm_weight, "norm_weight", _BF16, dev, (K,))
     wide = (K + 127) // 128
     shape = (wide, M) if block_rows == 1 else ((M + 127) // 128, wide)
@@ -791,13 +796,13 @@ def quantize(x, norm_weight=None, eps: float = 1e-6, block_rows: int = 1, codes=
         codes = new((M, K), (K, 1), _E4M3)
         to, code_stride = codes.data_ptr(), K
     else:
-        to, code_stride = _codes(codes, "codes", dev, M, K), codes.stride(0) if M > 1 else K
+        to, code_stride = _matrix(codes, "codes", _E4M3, dev, M, K)
     if scales is None:
         scales = new(shape, (shape[1], 1), _F32)
         at = scales.data_ptr()
     else:
         at = _dense(scales, "scales", _F32, dev, shape)
-    desc = QuantizeDesc(M, K, block_rows, x.stride(0) if M > 1 else K, code_stride, shape[1])
+    desc = QuantizeDesc(M, K, block_rows, x_stride, code_stride, shape[1])
     code = lib.mla_quantize(ctypes.byref(desc), rows, weight, eps, to, at, _raw_stream(dev, stream))
     if code:
         raise MLAError(code, "mla_quantize")
@@ -814,24 +819,21 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, residual=None, act: int = ACT_
         raise ValueError("x must be [M, K], w [N, K]")
     N, K = w.shape
     M = x.shape[0]
-    rows = _codes(x, "x", dev, M, K)
+    rows, x_stride = _matrix(x, "x", _E4M3, dev, M, K)
     if w.dtype != _E4M3 or w.get_device() != dev or not w.is_contiguous():
         _refuse(w, "w", f"a dense torch.float8_e4m3fn tensor on device {dev}")
     wide = (K + 127) // 128
     xs = _dense(x_scale, "x_scale", _F32, dev, (wide, M))
     ws = _dense(w_scale, "w_scale", _F32, dev, ((N + 127) // 128, wide))
     b = None if bias is None else _dense(bias, "bias", _BF16, dev, (N,))
-    res = None if residual is None else _rows(residual, "residual", dev, M, N)
+    res, res_stride = (None, N) if residual is None else _matrix(residual, "residual", _BF16, dev, M, N)
     word = None if status is None else _word(status, dev)
     if out is None:
         out = _allocator(stream)((M, N), (N, 1), _BF16)
         to, out_stride = out.data_ptr(), N
     else:
-        to, out_stride = _rows(out, "out", dev, M, N), out.stride(0)
-    if M > 1:
-        desc = LinearFp8Desc(M, K, N, act, x.stride(0), M, out_stride, N if res is None else residual.stride(0))
-    else:  # a single row has no stride
-        desc = LinearFp8Desc(M, K, N, act, K, M, N, N)
+        to, out_stride = _matrix(out, "out", _BF16, dev, M, N)
+    desc = LinearFp8Desc(M, K, N, act, x_stride, M, out_stride, res_stride)
     code = lib.mla_linear_fp8(ctypes.byref(desc), rows, xs, w.data_ptr(), ws, b, res, to, word, _raw_stream(dev, stream))
     if code:
         raise MLAError(code, "mla_linear_fp8")
