@@ -25,9 +25,9 @@ namespace mla {
 namespace {
 
 using quant::e4m3x2;
-using quant::fma2;
-using quant::mul2;
 using quant::unpack;
+using sm100::fma2;
+using sm100::mul2;
 
 constexpr int kWarps = 4;  // warps a CTA
 // As many as the 72 registers of each variant allow: 32768 rows in L2 10.9 us, with 6 11.1, with

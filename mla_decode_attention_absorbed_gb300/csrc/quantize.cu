@@ -18,6 +18,7 @@ namespace mla {
 namespace {
 
 using namespace quant;
+using sm100::fma2;
 
 constexpr int kThreads = 256;
 constexpr int kMostThreads = 512;  // with the norm

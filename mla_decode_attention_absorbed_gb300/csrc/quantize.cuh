@@ -16,6 +16,8 @@
 namespace mla {
 namespace quant {
 
+using sm100::mul2;
+
 constexpr int kBlock = 128;
 constexpr float kTop = 448.f;
 constexpr float kLeast = 0x1p-100f;
@@ -49,22 +51,6 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
         f[2 * e] = p.x;
         f[2 * e + 1] = p.y;
     }
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)),
-          "l"(*reinterpret_cast<unsigned long long *>(&c)));
-    return *reinterpret_cast<float2 *>(&r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(r)
-        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
-    return *reinterpret_cast<float2 *>(&r);
 }
 __device__ __forceinline__ float top8(const float (&f)[8]) {
     float top = 0.f;

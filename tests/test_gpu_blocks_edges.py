@@ -1,0 +1,108 @@
+"""The 8-bit operators with scales by blocks of 128 at the ends of what they are defined for: scales whose product is no normal
+number, or nearly infinite."""
+import pytest
+import torch
+
+from mla_decode_attention_absorbed_gb300 import build, mla
+from oracle import layer
+from test_gpu_blocks import BF16, DEV, E4M3, close, gen, operands, powers, randn, whole_codes
+
+pytestmark = pytest.mark.gpu
+
+# A tile of each form on a single CTA and on a pair, whole and shared (M, K, N).
+SIZES = [(3, 208, 136), (121, 1968, 136), (3, 208, 10328), (135, 208, 10840), (137, 208, 16408), (140, 7536, 5032)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    mla.load()
+
+
+# ------------------------------------------------------------------------------------------------- scales, far from 1
+# Half a step of bf16 is 2^-8 of a normal value and 2^-134 of a subnormal one; an fp32 subnormal on the way to it is off
+# by 2^-150.
+STEP, LEAST = 2.0 ** -8 * (1 + 2.0 ** -12), 2.0 ** -134 + 2.0 ** -150
+
+
+@pytest.mark.parametrize("low", [-122, -136, -150, -164])
+@pytest.mark.parametrize("M,K,N", SIZES)
+def test_linear_fp8_of_small_scales(M, K, N, low):
+    """Powers of two whose products go down to 2^low, of whole codes: every sum is exact, however small the scales'
+    product."""
+    g = gen(M + K - low)
+    x, w = whole_codes(g, M, K), whole_codes(g, N, K)
+    kb, half = -(-K // 128), low // 2
+    xs, ws = powers(g, kb, M, least=half, most=half + 2), powers(g, -(-N // 128), kb, least=low - half, most=low - half + 2)
+    r = (randn(g, M, N).double() * 2.0 ** (low + 10)).to(BF16)
+    want = layer.linear_fp8(x, xs, w, ws, None, r)
+    got = mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV), residual=r.to(DEV))
+    close(got, want, want.abs() * STEP + LEAST)
+
+
+@pytest.mark.parametrize("low", [-110, -118, -125])
+@pytest.mark.parametrize("M,K,N", SIZES)
+def test_linear_fp8_of_small_values(M, K, N, low):
+    """Values as quantising leaves them, of 2^low together: as product_tolerance has it, without its absolute part."""
+    g = gen(M + N - low)
+    x, xs, w, ws = operands(g, M, K, N, False)
+    xs, ws = xs * 2.0 ** (low // 2), ws * 2.0 ** (low - low // 2)
+    want = layer.linear_fp8(x, xs, w, ws)
+    terms = layer.linear_fp8(x.float().abs(), xs, w.float().abs(), ws)
+    got = mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV))
+    close(got, want, (K * 2.0 ** -23 + 2.0 ** -22) * terms + want.abs() * STEP + LEAST)
+
+
+def test_linear_fp8_of_the_smallest_scales():
+    """The scale that a block of values below 2^-100 has, 2^-100 / 448, on either side, and fp32's smallest number: what codes
+    of 448 make of them shows in bf16."""
+    M, K, N = 5, 4096, 136
+    x, w = torch.full((M, K), 448.0).to(E4M3), torch.full((N, K), 448.0).to(E4M3)
+    for a, b in ((2.0 ** -100 / 448, 2.0 ** -46), (2.0 ** -46, 2.0 ** -100 / 448), (2.0 ** -149, 1.0), (2.0 ** -149, 2.0 ** -8), (2.0 ** -75, 2.0 ** -81)):
+        xs, ws = torch.full((32, M), a), torch.full((2, 32), b)
+        want = layer.linear_fp8(x, xs, w, ws)
+        assert float(want[0, 0]) > 2.0 ** -128
+        # a block's scale and 32 of them added in fp32
+        close(mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV)), want, want * (STEP + 2.0 ** -18) + LEAST)
+
+
+@pytest.mark.parametrize("M,K,N", SIZES)
+def test_linear_fp8_of_scales_far_apart(M, K, N):
+    """Blocks of one row up to 2^200 apart, in an order of their own in each row: as test_linear_fp8, of all terms; where a block's scale is
+    past 2^16, the others' may be off by half an fp32 step of 2^-149, which is 2^-125 of codes' sum at most."""
+    g = gen(M + N)
+    x, w = whole_codes(g, M, K), whole_codes(g, N, K)
+    kb = -(-K // 128)
+    xs, ws = powers(g, kb, M, least=-80, most=45), powers(g, -(-N // 128), kb, least=-60, most=10)
+    want = layer.linear_fp8(x, xs, w, ws)
+    terms = layer.linear_fp8(x.float().abs(), xs, w.float().abs(), ws)
+    close(mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV)), want,
+          terms * (K * 2.0 ** -23) + want.abs() * STEP + LEAST + kb * 2.0 ** -125)
+
+
+@pytest.mark.parametrize("M,K,N", SIZES)
+def test_linear_fp8_of_large_scales(M, K, N):
+    """Scales' products around 2^85 of sums below 2^17 units (K times 16), of 2^2 at most between blocks: exact in fp32."""
+    g = gen(M + K)
+    x, w = whole_codes(g, M, K), whole_codes(g, N, K)
+    kb = -(-K // 128)
+    xs, ws = powers(g, kb, M, least=40, most=41), powers(g, -(-N // 128), kb, least=43, most=44)
+    want = layer.linear_fp8(x, xs, w, ws)
+    got = mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV))
+    assert torch.equal(got.cpu(), want.float().to(BF16))
+
+
+@pytest.mark.parametrize("M,K,N", SIZES)
+def test_linear_fp8_of_large_scales_beside_zeros(M, K, N):
+    """A scale of 2^66 or 2^120 beside a zero one is a block of zeros, whichever side it is on."""
+    g = gen(M + K + 1)
+    K += 256
+    x, w = whole_codes(g, M, K), whole_codes(g, N, K)
+    kb = -(-K // 128)
+    xs, ws = powers(g, kb, M, least=0, most=1), powers(g, -(-N // 128), kb, least=0, most=1)
+    xs[0], ws[:, 0] = 0.0, 2.0 ** 66
+    xs[2], ws[:, 2] = 2.0 ** 120, 0.0
+    want = layer.linear_fp8(x, xs, w, ws)
+    assert bool((want != 0).any())
+    got = mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV))
+    assert torch.equal(got.cpu(), want.float().to(BF16))
