@@ -224,13 +224,13 @@ __device__ __forceinline__ bool wait_for(bool done, uint64_t *bar, uint32_t pari
     }
 }
 
-// For what comes once the waits for work have ended, one way or the other (a whole warp).
-__device__ __forceinline__ bool wait_beyond(uint64_t *bar, uint32_t parity, uint64_t wait_ns) {
+// For what comes once the waits for work have ended, one way or the other (a whole warp); not if *lost.
+__device__ __forceinline__ bool wait_beyond(uint64_t *bar, uint32_t parity, uint64_t wait_ns, volatile int *lost) {
     const uint64_t t0 = globaltimer_ns(), ns = wait_ns + 2 * kWaitLimitNs;
     const long long c0 = clock64();
     while (!__all_sync(~0u, mbar_try_wait(bar, parity)))
-        if (__any_sync(~0u, globaltimer_ns() - t0 > ns || clock64() - c0 > (long long)(2 * ns))) return false;
-    return true;
+        if (__any_sync(~0u, *lost || globaltimer_ns() - t0 > ns || clock64() - c0 > (long long)(2 * ns))) return false;
+    return !__any_sync(~0u, *lost);
 }
 
 // A CTA's work (a pair's, "unit"): whole tiles, then, for a cluster's units together, a share of one
@@ -296,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a pair's: whether some pair of the cluster gave up, and the stages the other CTA issued
     volatile int *gave_up = abort_flag + 1;
     volatile uint32_t *peer_issued = reinterpret_cast<volatile uint32_t *>(gave_up + 1);
+    // some warp did not wait for the tile's memory: what lies there is not to be stored, of this tile or a later one
+    volatile int *lost = reinterpret_cast<volatile int *>(peer_issued + 1);
     const Patience patience{a.wait_ns, abort_flag};
     const int warp = __shfl_sync(~0u, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(tile_free, 1);
         mbar_init(tile_done, kSumWarps);
         mbar_init(drain, 1);
-        *abort_flag = *gave_up = 0;
+        *abort_flag = *gave_up = *lost = 0;
         *peer_issued = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_x);
@@ -436,11 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 2) {
             // The output's tiles: the residual comes to the tile's memory early (of a tile that a cluster
             // shares, the slabs with this CTA's columns), the sums' warps turn it into the result, and that is
-            // copied out.  They do so whatever else happens: the wait for them is not one for work.
+            // copied out.  The wait for them is not one for work: they come whatever else happens.  Once one of them has
+            // given up its wait for the tile's memory, that is offered no more, and the tiles that were not copied out yet become NaN
+            // from here.  (What the sums' warps still do with it, and with the barriers, is then nobody's.)
             uint8_t *slabs = smem + L::kStages * L::kStage;
             bool ok = true;
-            uint32_t i = 0;
-            for (; ok && walk.next(seg); ++i) {
+            uint32_t offered = 0;  // tiles whose memory was
+            while (walk.next(seg)) {
                 const int t0 = seg.m * kTileM + half * kRows;
                 int n0 = seg.n * kCols, used = kCols / 64;
                 if (seg.cut) {
@@ -449,19 +453,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     used = (walk.part * share + share - 1) / 64 - first + 1;
                 }
                 used = t0 < a.M && n0 < a.N ? min(used, (a.N - n0 + 63) / 64) : 0;
-                if (lane == 0) {
-                    if (a.residual && used > 0) {
-                        mbar_arrive_expect_tx(tile_free, used * (kRows * 128));
-                        for (int j = 0; j < used; ++j)
-                            tma_load_2d(slabs + j * (kRows * 128), &tm_res, tile_free, n0 + 64 * j, t0);
-                    } else {
-                        mbar_arrive(tile_free);
+                if (ok) {
+                    if (lane == 0) {
+                        if (a.residual && used > 0) {
+                            mbar_arrive_expect_tx(tile_free, used * (kRows * 128));
+                            for (int j = 0; j < used; ++j)
+                                tma_load_2d(slabs + j * (kRows * 128), &tm_res, tile_free, n0 + 64 * j, t0);
+                        } else {
+                            mbar_arrive(tile_free);
+                        }
                     }
+                    ++offered;
                 }
                 __syncwarp();
                 if (seg.cut) break;
-                ok = wait_beyond(tile_done, i & 1, a.wait_ns);
-                if (ok && lane == 0) {
+                ok = ok && wait_beyond(tile_done, (offered - 1) & 1, a.wait_ns, lost);
+                if (!ok) {
+                    if (used > 0 && n0 + 8 * lane < min(n0 + 64 * used, a.N)) {
+                        uint4 *to = reinterpret_cast<uint4 *>(a.out + (long long)t0 * a.out_stride + n0 + 8 * lane);
+                        uint4 *end = to + (long long)min(kRows, a.M - t0) * (a.out_stride / 8);
+#pragma unroll 1
+                        for (; to < end; to += a.out_stride / 8) *to = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                    }
+                } else if (lane == 0) {
                     for (int j = 0; j < used; ++j) tma_store_2d(&tm_out, slabs + j * (kRows * 128), n0 + 64 * j, t0);
                     bulk_commit();
                     bulk_wait_read_all();
@@ -469,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             if (lane == 0) bulk_wait_all();
+            if (offered > 0) mbar_wait(tile_free, (offered - 1) & 1);  // no residual is on its way
             if (!ok) *abort_flag = 1;
             __syncwarp();
         }
@@ -555,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int e = 0; e < kWide; ++e) sums[e] = __int_as_float(0x7fc00000);
             }
             if (!seg.cut) {
-                if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
+                const bool there = wait_for(false, tile_free, done & 1, patience);
+                if (!there) *lost = 1;  // then warp 2 does not copy the tile out
                 if (active) {
 #pragma unroll
                     for (int c = 0; c < kWide; c += 32) {
@@ -599,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (!__all_sync(~0u, mbar_wait(tile_free, done & 1))) *abort_flag = 1;
+                    const bool there = wait_for(false, tile_free, done & 1, patience) && !*lost;
                     cluster_sync();
                     // 32 tokens x 8 columns at a time, dealt out to the warps
                     const int runs = (nt + 31) / 32;
@@ -622,7 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 8; ++e) y[e] += f[e];
                         }
                         activate(a.act, y);
-                        if (a.residual) {
+                        if (!there) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = __int_as_float(0x7fc00000);
+                        } else if (a.residual) {
                             const int in_slabs = at - part * share / 64 * 64, chunk = in_slabs % 64 / 8;
                             Finish::unpack8(*reinterpret_cast<const uint4 *>(tile_memory + (in_slabs / 64 * kRows + token) * 128 +
                                                                              ((chunk ^ (token & 7)) << 4)), f);

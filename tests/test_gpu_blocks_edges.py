@@ -106,3 +106,38 @@ def test_linear_fp8_of_large_scales_beside_zeros(M, K, N):
     assert bool((want != 0).any())
     got = mla.linear_fp8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV))
     assert torch.equal(got.cpu(), want.float().to(BF16))
+
+
+# ----------------------------------------------------------------------------------------------------- waits that run out
+@pytest.mark.parametrize("M,K,N", [(4000, 16, 7160), (515, 208, 12760), (1039, 80, 20000), (3, 16, 41000), (2, 912, 20568), (262, 10896, 3768)])
+def test_linear_fp8_waits_for_the_residual_within_the_limit(M, K, N):
+    """Few blocks of K and several tiles a CTA: of a tile's time most goes to its residual, and to the copy of the tile before.
+    Limits that end those waits leave NaN, never a sum beside a residual that had not come, nor a tile as it was; the
+    next call knows nothing of it."""
+    g = gen(M + N)
+    x, xs, w, ws = (t.to(DEV) for t in operands(g, M, K, N, False))
+    r = randn(g, M, N, std=64.0).to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = mla.linear_fp8(x, xs, w, ws, residual=r)
+    seen = 0
+    try:
+        for ns in (1, 300, 1000, 2000, 4000, 8000, 16000):
+            mla.set_wait_limit_ns(ns)
+            for inplace in (False, True, False):
+                status.zero_()
+                out = r.clone() if inplace else torch.full((M, N), 77.0, dtype=BF16, device=DEV)
+                start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                start.record()
+                mla.linear_fp8(x, xs, w, ws, residual=out if inplace else r, status=status, out=out)
+                end.record()
+                torch.cuda.synchronize()
+                assert start.elapsed_time(end) < 1000.0
+                lost = torch.isnan(out)
+                assert torch.equal(torch.where(lost, want, out), want)
+                assert int(status) in (0, 8) and (int(status) == 8 or not bool(lost.any()))
+                seen += int(status) == 8
+    finally:
+        mla.set_wait_limit_ns(0)
+    assert seen > 0
+    status.zero_()
+    assert torch.equal(mla.linear_fp8(x, xs, w, ws, residual=r, status=status), want) and int(status) == 0
