@@ -599,7 +599,8 @@ MLA_API long long mla_latent_row_bytes(const mla_dims *dims);
  * positions[b*rows + i], or i where positions is NULL,
  *   out[b*out_stride + i*(d_c + d_rope) ...] = row of token p of sequence b
  * (an FP8 value is scale * code in fp32, rounded once).  A row whose p is outside [0,
- * seq_lens[b]) stays as it was, so that a list may be padded with -1.  out is then a
+ * seq_lens[b]) stays as it was, so that a list may be padded with -1 (at its end, where the
+ * attention is to read it: below the length it is given, every row counts).  out is then a
  * contiguous bf16 cache of `rows` tokens a sequence (seq_stride = out_stride), which
  * every entry point takes: whole histories for mla_prefill_expand, the tokens of a
  * selector for mla_decode_attn (with the number of them as lengths).  The cache is of

@@ -849,12 +849,14 @@ def linear_fp8_cut(M: int, K: int, N: int) -> LinearCut:
 
 def latent_load(prob: Problem, cache: Cache, rows: int, positions=None, out=None, status=None, stream=None):
     """mla_latent_load: ``rows`` tokens of each sequence back as bf16 [B, rows, d_c + d_rope] (``out``: any stride
-    between sequences), the first ones or those of ``positions`` [B, rows].  Rows of no token stay as they were."""
+    between sequences), the first ones or those of ``positions`` [B, rows].  Rows of no token stay as they were in ``out``;
+    without it they are 0, which costs a fill of the whole result before the call."""
     lib = _lib or load()
     B, width = prob.B, prob.d_c + prob.d_rope
     dev = _current_device()
     if out is None:
-        out = _allocator(stream)((B, rows, width), (rows * width, width, 1), _BF16)
+        with torch.cuda.stream(stream):
+            out = _empty_strided_cuda((B, rows, width), (rows * width, width, 1), _BF16).zero_()
         stride = rows * width
     else:
         if (out.dtype != _BF16 or out.get_device() != dev or out.shape != (B, rows, width) or out.stride(2) != 1 or

@@ -5,7 +5,7 @@ import torch
 
 from mla_decode_attention_absorbed_gb300 import build, mla
 from oracle import layer
-from test_gpu_blocks import BF16, DEV, E4M3, close, gen, operands, powers, randn, whole_codes
+from test_gpu_blocks import BF16, DEV, E4M3, cache_bytes, close, gen, operands, powers, problem, randn, whole_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,41 @@ def test_linear_fp8_waits_for_the_residual_within_the_limit(M, K, N):
     assert seen > 0
     status.zero_()
     assert torch.equal(mla.linear_fp8(x, xs, w, ws, residual=r, status=status), want) and int(status) == 0
+
+
+# ------------------------------------------------------------------------------------------------------- rows of no token
+@pytest.mark.parametrize("on_stream", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "blocks"])
+def test_load_without_out_gives_zeros_for_rows_of_no_token(kind, on_stream):
+    """Behind a length, of an empty sequence, of a position of -1 in a list, of a length or page out of range: 0 in a tensor that the call
+    makes, whatever lay in its memory before."""
+    g = gen(81)
+    B, rows, T, d_c, d_rope = 5, 1300, 320, 128, 32
+    prob, W = problem(B, 16, 1, d_c=d_c, d_rope=d_rope), d_c + d_rope
+    kv, values, scale = cache_bytes(g, kind, (B * 5, 64), d_c, d_rope)
+    table = torch.arange(B * 5, dtype=torch.int32).view(B, 5)
+    values = values.view(B, T, W)
+    lens = torch.tensor([320, 0, 130, 321, 320], dtype=torch.int32)
+    table[4, 1] = B * 5
+    kv, table_d, lens_d = kv.to(DEV), table.to(DEV), lens.to(DEV)
+    cache = mla.make_cache(prob, kv, lens_d, table_d, 64, kv_scale=scale)
+    at = torch.randint(0, T, (B, rows), generator=g)
+    at[:, ::7] = -1
+    stream = torch.cuda.Stream() if on_stream else None
+    torch.cuda.synchronize()
+    for positions in (None, at):
+        with torch.cuda.stream(stream):  # what the call gets next
+            torch.full((B, rows, W), float("nan"), dtype=BF16, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        torch.cuda.synchronize()
+        got = mla.latent_load(prob, cache, rows, positions=None if positions is None else at.to(torch.int32).to(DEV), status=status,
+                              stream=stream)
+        torch.cuda.synchronize()
+        assert int(status) in (layer.SEQLEN, layer.PAGE)
+        p = torch.arange(rows).expand(B, -1) if positions is None else at
+        there = (p >= 0) & (p < lens[:, None])
+        there[3] = False
+        there[4] &= p[4] // 64 != 1
+        want = torch.zeros(B, rows, W, dtype=torch.float64)
+        want[there] = values[torch.arange(B)[:, None].expand(-1, rows)[there], p[there]]
+        close(got, want, want.abs() * (0 if kind == "bf16" else 2.0 ** -8 * (1 + 2.0 ** -14)) + 2.0 ** -134)
