@@ -252,6 +252,8 @@ def make_cache(prob: Problem, kv: torch.Tensor, seq_lens: torch.Tensor, block_ta
         raise ValueError("kv must be bf16 or FP8 codes with rows of d_c + d_rope contiguous values")
     if fp8 and not blocks and kv_scale is None:
         raise ValueError("an FP8 cache needs its kv_scale")
+    if blocks and kv_scale is not None:
+        raise ValueError(f"uint8 rows of {W} bytes are blocks with scales of their own: they have no kv_scale")
     dt, sc = (KV_E4M3_BLOCKS, 1.0) if blocks else (KV_E4M3, float(kv_scale)) if fp8 else (KV_BF16, 1.0)
     if block_table is None:
         if kv.dim() != 3 or kv.stride(1) != W:
