@@ -813,8 +813,8 @@ def quantize(x, norm_weight=None, eps: float = 1e-6, block_rows: int = 1, codes=
 
 def linear_fp8(x, x_scale, w, w_scale, bias=None, residual=None, act: int = ACT_NONE, out=None, stream=None, status=None):
     """mla_linear_fp8: residual + act(x . w^T + bias) of E4M3 codes x [M, K] (rows any multiple of 16 bytes apart) and
-    w [N, K] dense, with the scales that ``quantize`` gives: x_scale [ceil(K / 128), M], w_scale [ceil(N / 128),
-    ceil(K / 128)].  bias, residual, out and ``status`` as for ``linear``."""
+    w [N, K] dense, with the scales that ``quantize`` gives: x_scale [ceil(K / 128), M] (rows any distance apart: those of a
+    slice of x are a slice of the whole's), w_scale [ceil(N / 128), ceil(K / 128)].  bias, residual, out and ``status`` as for ``linear``."""
     lib = _lib or load()
     dev = _device(x, "x")
     if w.dim() != 2 or x.dim() != 2:
@@ -825,7 +825,7 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, residual=None, act: int = ACT_
     if w.dtype != _E4M3 or w.get_device() != dev or not w.is_contiguous():
         _refuse(w, "w", f"a dense torch.float8_e4m3fn tensor on device {dev}")
     wide = (K + 127) // 128
-    xs = _dense(x_scale, "x_scale", _F32, dev, (wide, M))
+    xs, xs_stride = _matrix(x_scale, "x_scale", _F32, dev, wide, M)
     ws = _dense(w_scale, "w_scale", _F32, dev, ((N + 127) // 128, wide))
     b = None if bias is None else _dense(bias, "bias", _BF16, dev, (N,))
     res, res_stride = (None, N) if residual is None else _matrix(residual, "residual", _BF16, dev, M, N)
@@ -835,7 +835,7 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, residual=None, act: int = ACT_
         to, out_stride = out.data_ptr(), N
     else:
         to, out_stride = _matrix(out, "out", _BF16, dev, M, N)
-    desc = LinearFp8Desc(M, K, N, act, x_stride, M, out_stride, res_stride)
+    desc = LinearFp8Desc(M, K, N, act, x_stride, xs_stride, out_stride, res_stride)
     code = lib.mla_linear_fp8(ctypes.byref(desc), rows, xs, w.data_ptr(), ws, b, res, to, word, _raw_stream(dev, stream))
     if code:
         raise MLAError(code, "mla_linear_fp8")

@@ -15,3 +15,43 @@ def test_rows_of_blocks_take_no_scale(paged):
         mla.make_cache(prob, rows, lens, table, kv_scale=0.5)
     assert mla.make_cache(prob, rows, lens, table).kv_dtype == mla.KV_E4M3_BLOCKS
     assert mla.make_cache(prob, rows[:, :, :160].contiguous(), lens, table, kv_scale=0.5).kv_dtype == mla.KV_E4M3
+
+
+class OnDevice:
+    """A CPU tensor that says it lies on device 0."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return 0
+
+
+def test_linear_fp8_takes_the_scales_of_some_rows(monkeypatch):
+    """The rows [a, b) of quantised values and their scales, a slice of each, without a copy."""
+    seen = []
+
+    class Library:
+        def mla_linear_fp8(self, desc, x, x_scale, *rest):
+            seen.append((desc._obj.M, x, desc._obj.x_stride, x_scale, desc._obj.x_scale_stride))
+            return 0
+
+    monkeypatch.setattr(mla, "_lib", Library())
+    monkeypatch.setattr(mla, "_current_device", lambda: 0)
+    monkeypatch.setattr(mla, "_raw_stream", lambda dev, stream: 0)
+    x, scales = torch.zeros(40, 272).to(torch.float8_e4m3fn), torch.zeros(3, 40)
+    w, w_scale = OnDevice(torch.zeros(136, 272).to(torch.float8_e4m3fn)), OnDevice(torch.zeros(2, 3))
+    for a, b in ((0, 40), (8, 24), (39, 40), (5, 5)):
+        out = OnDevice(torch.zeros(b - a, 136, dtype=torch.bfloat16))
+        mla.linear_fp8(OnDevice(x[a:b]), OnDevice(scales[:, a:b]), w, w_scale, out=out)
+        M, at, _, scale_at, stride = seen.pop()
+        assert M == b - a
+        if M:
+            assert at == x.data_ptr() + 272 * a and scale_at == scales.data_ptr() + 4 * a and stride == 40
+    for bad in (scales.t().contiguous().t(), scales[:2], scales[:, :39], scales.double(), scales[:, ::2].repeat(1, 2)[:, ::2]):
+        with pytest.raises(ValueError):
+            mla.linear_fp8(OnDevice(x), OnDevice(bad), w, w_scale, out=OnDevice(torch.zeros(40, 136, dtype=torch.bfloat16)))
+    assert not seen

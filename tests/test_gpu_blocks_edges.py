@@ -179,3 +179,16 @@ def test_load_without_out_gives_zeros_for_rows_of_no_token(kind, on_stream):
         want = torch.zeros(B, rows, W, dtype=torch.float64)
         want[there] = values[torch.arange(B)[:, None].expand(-1, rows)[there], p[there]]
         close(got, want, want.abs() * (0 if kind == "bf16" else 2.0 ** -8 * (1 + 2.0 ** -14)) + 2.0 ** -134)
+
+
+# -------------------------------------------------------------------------------------------------- some of quantised rows
+def test_linear_fp8_of_some_of_the_rows():
+    """A part of a batch, and its scales where they lie among the others', gives what it gives with a copy of them."""
+    g = gen(91)
+    x, weight = randn(g, 300, 1040).to(DEV), randn(g, 1040).to(DEV)
+    w, ws = mla.quantize(randn(g, 520, 1040, std=1040 ** -0.5).to(DEV), block_rows=128)
+    codes, scales = mla.quantize(x, norm_weight=weight)
+    for a, b in ((0, 300), (3, 4), (7, 150), (290, 300), (299, 300)):
+        want = mla.linear_fp8(codes[a:b].clone(), scales[:, a:b].clone(memory_format=torch.contiguous_format), w, ws)
+        assert torch.equal(mla.linear_fp8(codes[a:b], scales[:, a:b], w, ws), want), (a, b)
+        assert torch.equal(mla.linear_fp8(*mla.quantize(x[a:b], norm_weight=weight), w, ws), want), (a, b)
