@@ -55,3 +55,19 @@ def test_linear_fp8_takes_the_scales_of_some_rows(monkeypatch):
         with pytest.raises(ValueError):
             mla.linear_fp8(OnDevice(x), OnDevice(bad), w, w_scale, out=OnDevice(torch.zeros(40, 136, dtype=torch.bfloat16)))
     assert not seen
+
+
+def test_whole_operands_sum_exactly():
+    """The products compared bit for bit: their codes' products are whole and their scales' at least 2^-4, so every sum is exact in fp32
+    while the absolute terms come to less than 2^24 times 2^-4.  16 x 16 a term holds that up to K = 4096; beyond, by the
+    data."""
+    from helpers import LINEAR_FP8_FORMS
+    from test_gpu_blocks import PRODUCT_CASES, gen, operands
+    sizes = [(M, K, N, 1) for M, K, N in LINEAR_FP8_FORMS.values()] + [(*case[:3], 0) for case in PRODUCT_CASES]
+    long = [s for s in sizes if s[1] > 4096]
+    assert long
+    for M, K, N, seed in long:
+        x, xs, w, ws = operands(gen(M + K + N + seed), M, K, N, True)
+        xv = x.float().abs() * xs.t().repeat_interleave(128, 1)[:, :K]
+        wv = w.float().abs() * ws.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        assert float((xv @ wv.t()).max()) * 2.0 ** 4 < 2.0 ** 24 * 0.99, (M, K, N)

@@ -192,3 +192,24 @@ def test_linear_fp8_of_some_of_the_rows():
         want = mla.linear_fp8(codes[a:b].clone(), scales[:, a:b].clone(memory_format=torch.contiguous_format), w, ws)
         assert torch.equal(mla.linear_fp8(codes[a:b], scales[:, a:b], w, ws), want), (a, b)
         assert torch.equal(mla.linear_fp8(*mla.quantize(x[a:b], norm_weight=weight), w, ws), want), (a, b)
+
+
+# ------------------------------------------------------------------------------------------------ the sum within a block
+def test_linear_fp8_keeps_small_terms_beside_large_ones():
+    """448 x 448 and its negative in one block of K, with a small term.  Where the large ones are among the same 32 values, which are one
+    instruction's, the smallest code survives beside them; across instructions the sum is an fp32 number, whose step at
+    200704 is 2^-6.  (What the card does; the contract is a sum in fp32.)"""
+    def one(terms):
+        x, w = torch.zeros(1, 128), torch.zeros(8, 128)
+        for k, a, b in terms:
+            x[0, k], w[:, k] = a, b
+        ones = torch.ones(1, 1, device=DEV)
+        got = mla.linear_fp8(x.to(E4M3).to(DEV), ones, w.to(E4M3).to(DEV), ones).cpu().float()
+        assert bool((got == got[0, 0]).all())
+        return float(got[0, 0])
+
+    for group in range(0, 128, 32):
+        for k, l, m in ((0, 1, 2), (31, 0, 17), (5, 30, 31), (16, 15, 0)):
+            assert one([(group + k, 448.0, 448.0), (group + l, 448.0, -448.0), (group + m, 2.0 ** -9, 1.0)]) == 2.0 ** -9
+    for first, second, small in ((0, 32, 64), (0, 127, 64), (96, 1, 33), (40, 70, 3)):
+        assert one([(first, 448.0, 448.0), (second, 448.0, -448.0), (small, 2.0 ** -6, 1.0)]) == 2.0 ** -6
