@@ -7,7 +7,7 @@
 // (8 codes a load and two turns: histories 64.1 us, so 55.4).
 //
 // Measured (device time): histories of 64 sequences, three quarters of 4096 tokens on average, in blocks 55.4 us = 0.94 of the
-// measured copy rate (a row of 656 bytes spans 21.5 sectors of 32 on average), as codes with one scale 53.3 = 0.94, as
+// measured copy rate (a row of 656 bytes spans 21 sectors of 32), as codes with one scale 53.3 = 0.94, as
 // bf16 68.5 = 0.97; 65536 listed tokens in blocks 21.2 us = 0.82, position, page and row one after another;
 // 3 x 333 rows 2.6 us, a launch and four round trips.  Two rows a warp 21.8, eight 23.6 (listed tokens).
 #include "quantize.cuh"

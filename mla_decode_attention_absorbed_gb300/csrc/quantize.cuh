@@ -3,8 +3,9 @@
 //   A = max(max |y|, 2^-100),   scale = A / 448,   code = E4M3(y * (448 / A))
 //
 // 448 is the largest E4M3 value, so the block's largest value takes the last code and nothing
-// saturates; both quotients are rounded once in fp32 (division, not a reciprocal's estimate, so
-// that any fp32 program gives the same codes and scales).  The 2^-100 keeps 448 / A finite for
+// saturates; both quotients are rounded once in fp32 (division, so that any program that divides so
+// gives the same codes and scales; one that multiplies by a reciprocal, as torch does for 448.0 / t and for t / 448.0 on
+// the GPU, has scales off in the last bit and at a tie the neighbouring code).  The 2^-100 keeps 448 / A finite for
 // a block of zeros or of values that no result can show.  A NaN keeps its own code and leaves the
 // rest of its block alone (fmaxf returns the other operand); an infinity makes A infinite and
 // with it every value of the block NaN or 0 x infinity, so that it shows in what is computed.
