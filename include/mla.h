@@ -649,8 +649,8 @@ typedef struct {
  *   x'[m, k] = x_scale[k/128][m] * x[m, k],  w'[n, k] = w_scale[n/128][k/128] * w[n, k]
  * The codes' products are summed block by block of K in fp32, and the scaled blocks
  * in fp32 in the order of K; epilogue as mla_linear, one rounding to bf16.  x_scale * w_scale
- * of a block has to be finite and may be as small as it likes (where a row's blocks meet one of 2^16
- * or more, those below 2^-126 are off by up to 2^-125 each).  x [M][K] and w [N][K] (dense; the rows are
+ * of a block has to be finite and may be as small as it likes (where a row has a block of 2^16 or more, or an
+ * x_scale of 2^64 or more, its blocks below 2^-126 are off by up to 2^-125 each).  x [M][K] and w [N][K] (dense; the rows are
  * output columns) are codes, x_scale fp32 [ceil(K/128)][M], w_scale fp32 [ceil(N/128)]
  * [ceil(K/128)]; bias [N], residual and out [M][N] bf16, as for mla_linear.  No
  * workspace.  Results do not depend on the timing of the GPU.  A bounded device wait that runs

@@ -244,7 +244,7 @@ struct Segment {
 constexpr int kBand = 8;
 // A lane's sums and a block's scale x_scale * w_scale are held times kLift, so that a small scale keeps its bits: a
 // block's codes sum to up to 128 * 448^2 < 2^25, and 2^25 times a scale below the normal numbers is one.  A
-// lane that meets a scale past kMostLifted, held so, puts its sums down for the rest of the tile (2^80 * 2^25
+// lane that meets a scale past kMostLifted, held so (or an x_scale that passes fp32 so), puts its sums down for the rest of the tile (2^80 * 2^25
 // in 2^13 blocks stays finite).  4096 x 16384 x 7168 321 us, without 319; 4096 x 512 x 7168 40.3, without 40.0.
 constexpr float kLift = 0x1p64f, kMostLifted = 0x1p80f;
 struct Walk {
